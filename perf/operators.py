@@ -145,7 +145,7 @@ def run(s):
         if op == "paged":
             return st.st_paged_attn(s["pattern"], s["q"], s["k_cache"], s["v_cache"], s["table"], s["cu"], s["kv_lens"],
                                     s["max_q"], s["max_kv"])
-        st.st_cache_append(s["k"], s["v"], s["k_cache"], s["v_cache"], s["table"], s["cu"], s["kv_lens"], s["max_q"])
+        st.st_cache_append(s["k"], s["v"], s["k_cache"], s["v_cache"], s["table"], s["cu"], s["kv_lens"])
         return s["k_cache"], s["v_cache"]
     if op == "prompt":
         return _plain_prompt(s)
