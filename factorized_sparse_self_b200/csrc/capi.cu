@@ -26,8 +26,9 @@ constexpr int kMaxDevices = 64;
 int* g_status[kMaxDevices] = {nullptr};
 std::mutex g_mu;
 
-// Device status word of the current device (allocated on first use, which
-// is always inside st_pattern_layout, never inside fwd/bwd).
+// Device status word of the current device (allocated on first use, which is
+// inside st_pattern_layout or the first call of the ragged and paged entry
+// points, never inside the layouts' fwd/bwd).
 int* status_word(int dev, bool create) {
   if (dev < 0 || dev >= kMaxDevices) return nullptr;
   std::lock_guard<std::mutex> lk(g_mu);
@@ -132,6 +133,11 @@ void arm(Call& c, int kernel) {
 }
 
 }  // namespace
+
+namespace st {
+int* device_status(int dev, bool create) { return status_word(dev, create); }
+uint64_t wait_limit_ns() { return g_wait_ns.load(); }
+}  // namespace st
 
 extern "C" {
 

@@ -31,6 +31,11 @@ inline void record_end(const Call& c) {
   if (c.ev_end) cudaEventRecord(c.ev_end, c.stream);
 }
 
+// Status word of device `dev` (null if it does not exist and is not to be
+// created, or cannot be), and the bound of on-device waits.
+int* device_status(int dev, bool create);
+uint64_t wait_limit_ns();
+
 // Multiprocessor count of the current device (queried once per device).
 int sm_count();
 

@@ -1,0 +1,307 @@
+// Index arithmetic of attention over ragged sequences (packed one behind the
+// other, or kept in a paged cache) restricted to the factorized patterns.
+//
+// The sets are those of the dense-batch calls: strided A1 (window), A2
+// (stride), fixed A1 (block), A2 (summary), and the unions. As there, every set
+// is split into segments in a row order that makes it dense, but the sequences
+// here have any length, so nothing is padded: each order lists a sequence's
+// positions one after the other,
+//   natural  0, 1, 2, ...
+//   summary  the last c positions of every l-block, packed (keys only)
+//   class    residue class 0 (0, l, 2l, ...), then class 1, ... up to l - 1
+// and in its order every query row's live keys are ONE interval [lo, hi) whose
+// ends never decrease from row to row (asserted for small sizes on the host by
+// the tests of the calls). A tile of rows therefore meets the keys from its
+// first row's lo to its last row's hi, and, the other way round, key k meets
+// the rows from the first with hi > k up to the first with lo > k.
+//
+// Grouped heads: the query heads that share a key/value head and have the same
+// index set form the rows of one unit, row x = e * Gc + g being query e of the
+// order, head g of the group, so that a K / V tile serves the whole group.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "device_common.cuh"
+
+namespace st {
+namespace rag {
+
+#define ST_HD __host__ __device__ __forceinline__
+
+ST_HD int qdiv(int n, FastDiv f, int d) {
+#ifdef __CUDA_ARCH__
+  (void)d;
+  return fdiv(n, f);
+#else
+  (void)f;
+  return n / d;
+#endif
+}
+
+struct Seg {
+  int32_t kview;  // View of the keys
+  int32_t rule;   // Rule
+};
+
+// One head class in one query order: its segments are attended by one softmax
+// (or, for the strided union, joined with the other order's result).
+struct Job {
+  int32_t hc;     // heads: 0 / 1 = even / odd heads only, -1 = all
+  int32_t qview;  // View of the queries
+  int32_t nseg;
+  Seg seg[2];
+};
+
+// Rows of one tensor as a matrix of d-element rows: the row of head h of a
+// token (packed: token index; paged: through the page table).
+struct Rows {
+  int32_t tok;   // rows from one token (slot) to the next
+  int32_t head;  // rows from one head to the next
+  int32_t page;  // rows from one page to the next (paged only)
+};
+
+struct Geo {
+  int32_t S, total;       // sequences, token rows
+  int32_t H, Hkv, G, d;
+  int32_t l, c, split;    // split: even / odd heads have different sets
+  FastDiv fl, fc;
+  const int32_t* cu;      // [S + 1] first token row of every sequence
+  // paged cache (null kv_lens: packed, keys are the sequence's own rows)
+  const int32_t* kv_lens; // [S]
+  const int32_t* table;   // [S, max_pages]
+  int32_t page_size, max_pages, num_pages;
+  FastDiv fpage;
+  Rows q, k, v;
+  int* status;
+};
+
+// One sequence.
+struct Seq {
+  int32_t s, qb;     // index, first token row
+  int32_t nq, nk;    // query rows, keys
+  int32_t off;       // position of query row 0 (nk - nq; negative rows attend nothing)
+  int32_t nqv;       // query rows at positions >= 0
+  int32_t P, rem;    // nk / l, nk mod l
+  int32_t Po, remo;  // the same of max(off, 0)
+  int32_t nsum;      // summary positions among the keys
+};
+
+ST_HD int imin(int a, int b) { return a < b ? a : b; }
+ST_HD int imax(int a, int b) { return a > b ? a : b; }
+
+ST_HD Seq make_seq(const Geo& g, int s, int qb, int nq, int nk) {
+  Seq q;
+  q.s = s;
+  q.qb = qb;
+  q.nq = nq;
+  q.nk = nk;
+  q.off = nk - nq;
+  const int o = imax(q.off, 0);
+  q.nqv = nk - o;
+  q.P = qdiv(nk, g.fl, g.l);
+  q.rem = nk - q.P * g.l;
+  q.Po = qdiv(o, g.fl, g.l);
+  q.remo = o - q.Po * g.l;
+  q.nsum = q.P * g.c + imax(0, q.rem - (g.l - g.c));
+  return q;
+}
+
+// First index of class r in the class order of the keys 0 .. nk-1.
+ST_HD int cls_key_start(const Seq& q, int r) { return r * q.P + imin(r, q.rem); }
+// First index of class r in the class order of the queries max(off, 0) .. nk-1.
+ST_HD int cls_query_start(const Seq& q, int r) {
+  return r * (q.P - q.Po) + imin(r, q.rem) - imin(r, q.remo);
+}
+
+// Position of key index e of an order (0 <= e < number of keys in it).
+ST_HD int key_pos(const Geo& g, const Seq& q, int view, int e) {
+  if (view == VIEW_NAT) return e;
+  if (view == VIEW_SUM) {
+    const int b = qdiv(e, g.fc, g.c);
+    return b * g.l + (g.l - g.c) + (e - b * g.c);
+  }
+  const int big = q.rem * (q.P + 1);  // <= nk
+  if (e < big) {
+    const int r = e / (q.P + 1);
+    return (e - r * (q.P + 1)) * g.l + r;
+  }
+  const int r = (e - big) / q.P;  // P >= 1 here: e - big < (l - rem) * P
+  return (e - big - r * q.P) * g.l + q.rem + r;
+}
+
+ST_HD int n_keys(const Seq& q, int view) { return view == VIEW_SUM ? q.nsum : q.nk; }
+
+// Token row of query index e of an order (0 <= e < nq), relative to the
+// sequence; its position is row + off. In the class order the rows at negative
+// positions come last.
+ST_HD int query_row(const Geo& g, const Seq& q, int view, int e) {
+  if (view == VIEW_NAT) return e;
+  if (e >= q.nqv) return e - q.nqv;
+  // Classes start at slope D = P - Po, one more between remo and rem (or one
+  // less between rem and remo): three pieces of equal classes.
+  const int D = q.P - q.Po;
+  const int a = imin(q.rem, q.remo), b = imax(q.rem, q.remo);
+  const int Dm = q.rem >= q.remo ? D + 1 : D - 1;
+  const int s1 = a * D, s2 = s1 + (b - a) * Dm;
+  int r, p;
+  if (e < s1) {
+    r = e / D;
+    p = e - r * D;
+  } else if (e < s2) {
+    r = (e - s1) / Dm;
+    p = e - s1 - r * Dm;
+    r += a;
+  } else {
+    r = (e - s2) / D;
+    p = e - s2 - r * D;
+    r += b;
+  }
+  // the class's first query position is the first one >= max(off, 0)
+  const int first = q.Po + (r < q.remo ? 1 : 0);
+  return (first + p) * g.l + r - q.off;
+}
+
+// Live keys [lo, hi) of the query at position i (>= 0), in the segment's key
+// order.
+ST_HD void live_keys(const Geo& g, const Seq& q, int rule, int i, int& lo, int& hi) {
+  lo = 0;
+  hi = i + 1;
+  if (rule == RULE_CAUSAL) return;
+  if (rule == RULE_BAND) {
+    lo = imax(0, i - g.l);
+    return;
+  }
+  const int b = qdiv(i, g.fl, g.l);
+  const int r = i - b * g.l;
+  switch (rule) {
+    case RULE_BLOCK:
+      lo = b * g.l;
+      break;
+    case RULE_STRIDE:
+      lo = cls_key_start(q, r);
+      hi = lo + b + 1;
+      break;
+    case RULE_STRIDE_FAR:
+      lo = cls_key_start(q, r);
+      hi = imax(lo, lo + b - 1);
+      break;
+    case RULE_SUMMARY:
+      hi = b * g.c + imax(0, r + 1 - (g.l - g.c));
+      break;
+    default:  // RULE_SUMMARY_EARLIER
+      hi = b * g.c;
+      break;
+  }
+}
+
+// Query indexes of an order that attend anything: [qv0, qv1).
+ST_HD void valid_rows(const Seq& q, int view, int& v0, int& v1) {
+  v0 = view == VIEW_NAT ? q.nq - q.nqv : 0;
+  v1 = view == VIEW_NAT ? q.nq : q.nqv;
+}
+
+// Query indexes [a, b) of an order whose live interval holds key k.
+ST_HD void live_queries(const Geo& g, const Seq& q, int view, int rule, int k, int& a, int& b) {
+  int v0, v1;
+  valid_rows(q, view, v0, v1);
+  int x = v0, y = v1;
+  while (x < y) {  // first row with hi > k
+    const int m = (x + y) >> 1;
+    int lo, hi;
+    live_keys(g, q, rule, query_row(g, q, view, m) + q.off, lo, hi);
+    if (hi > k) y = m;
+    else x = m + 1;
+  }
+  a = x;
+  y = v1;
+  while (x < y) {  // first row with lo > k
+    const int m = (x + y) >> 1;
+    int lo, hi;
+    live_keys(g, q, rule, query_row(g, q, view, m) + q.off, lo, hi);
+    if (lo > k) y = m;
+    else x = m + 1;
+  }
+  b = x;
+}
+
+// Query heads of a group that belong to a job: head = first + step * g.
+struct Heads3 {
+  int32_t first, step, n;
+};
+ST_HD Heads3 heads_of_group(const Geo& g, int hc, int kvh) {
+  Heads3 h;
+  h.first = kvh * g.G;
+  h.step = 1;
+  h.n = g.G;
+  if (hc >= 0) {
+    h.first += (hc ^ h.first) & 1;
+    h.step = 2;
+    const int end = kvh * g.G + g.G;
+    h.n = h.first < end ? (end - h.first + 1) / 2 : 0;
+  }
+  return h;
+}
+// The most heads of one job in a group: unit slots are numbered with it.
+ST_HD int most_heads(const Geo& g, int hc) { return hc >= 0 ? (g.G + 1) / 2 : g.G; }
+
+// Unit slots: sequence s owns the slots from floor(cu[s] * mult / BM) + s up to
+// the next sequence's first, at least ceil(n_s * mult / BM) of them, so a slot's
+// sequence is found by bisection of cu and no table of units is built.
+ST_HD long long slot_count(const Geo& g, int mult, int BM) {
+  return (long long)g.total * mult / BM + g.S;
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ int cu_at(const Geo& g, int s) {
+  return imin(imax(__ldg(g.cu + s), 0), g.total);
+}
+
+__device__ __forceinline__ Seq load_seq(const Geo& g, int s) {
+  const int a = cu_at(g, s);
+  const int b = imax(a, cu_at(g, s + 1));
+  int nk = b - a;
+  if (g.kv_lens) {
+    const int want = __ldg(g.kv_lens + s);
+    nk = imin(imax(want, 0), g.max_pages * g.page_size);
+    if (nk != want) set_status(g.status, ST_ERR_INVALID);
+  }
+  return make_seq(g, s, a, b - a, nk);
+}
+
+// Sequence and tile of a slot (the tile may be past the sequence's rows).
+__device__ __forceinline__ int find_slot(const Geo& g, int mult, int BM, int slot, int& tile) {
+  int a = 0, b = g.S - 1;
+  while (a < b) {
+    const int m = (a + b + 1) >> 1;
+    const int first = (int)((long long)cu_at(g, m) * mult / BM) + m;
+    if (first <= slot) a = m;
+    else b = m - 1;
+  }
+  tile = slot - ((int)((long long)cu_at(g, a) * mult / BM) + a);
+  return a;
+}
+
+// Row (in units of d elements) of key position j, key/value head kvh, of k or v
+// (r = g.k or g.v). A page number outside the cache is reported and read as
+// page 0.
+__device__ __forceinline__ int kv_row(const Geo& g, const Rows& r, const Seq& q, int j, int kvh) {
+  if (!g.kv_lens) return (q.qb + j) * r.tok + kvh * r.head;
+  const int pg = fdiv(j, g.fpage);
+  int page = __ldg(g.table + (size_t)q.s * g.max_pages + pg);
+  if ((unsigned)page >= (unsigned)g.num_pages) {
+    set_status(g.status, ST_ERR_INVALID);
+    page = 0;
+  }
+  return page * r.page + (j - pg * g.page_size) * r.tok + kvh * r.head;
+}
+
+// Row of token t (absolute), query head h.
+__device__ __forceinline__ int q_row(const Geo& g, int t, int h) {
+  return t * g.q.tok + h * g.q.head;
+}
+#endif
+
+}  // namespace rag
+}  // namespace st

@@ -1,0 +1,81 @@
+// Host-side launch entry points of the kernels for ragged and paged sequences
+// (internal; CUDA files only).
+#pragma once
+
+#include "launch.h"
+#include "ragged.cuh"
+
+namespace st {
+namespace rag {
+
+// What becomes of a unit's output rows.
+enum OutMode : int32_t {
+  OUT_FINAL = 0,    // O and LSE are written
+  OUT_PARTIAL = 1,  // fp32 O and LSE go to a part, joined later
+  OUT_MERGE = 2     // joined with part 0 (another order's result), then written
+};
+
+// Several results of one query row over disjoint key sets ("parts"): fp32 O
+// [parts][total][H][d] and natural-log LSE [parts][total][H], joined by their
+// log-sum-exp.
+struct Parts {
+  float* o;
+  float* lse;
+};
+
+// One launch of a forward kernel: one job, its keys cut into nsplit parts.
+struct FwdLaunch {
+  Geo g;
+  Job job;
+  const void *q, *k, *v;
+  void* o;
+  float* lse;
+  Parts parts;
+  int32_t part0;   // first part of this job
+  int32_t nsplit;  // OUT_PARTIAL: key ranges per unit (grid z)
+  int32_t mode;    // OutMode
+  float scale_log2;
+  uint64_t wait_ns;
+  int64_t q_rows, k_rows, v_rows;  // rows of the matrices behind q, k and v
+  cudaStream_t stream;
+};
+
+// Backward, one key order's share of dK and dV: fp32 parts [parts][total][Hkv][2][d]
+// when several jobs or key ranges add up, else written directly.
+struct BwdLaunch {
+  Geo g;
+  Job job[2];        // key jobs: one segment each
+  int32_t njobs;
+  const void *q, *k, *v, *dout;
+  const float *lse, *delta;
+  void *dq, *dk, *dv;
+  Rows dq_rows, dk_rows, dv_rows;  // of the gradients
+  float* parts;      // dK, dV parts
+  float* dq_part;    // fp32 dQ [total][H][d] of the first query order
+  int32_t nsplit;
+  float scale;
+  uint64_t wait_ns;
+  int64_t q_rows, k_rows, v_rows;
+  cudaStream_t stream;
+};
+
+// CUDA-core kernels in fp32 arithmetic.
+cudaError_t simt_ragged_fwd(const FwdLaunch& a, int dtype);
+cudaError_t simt_ragged_dq(const BwdLaunch& a, const Job& job, int mode, int dtype);
+cudaError_t simt_ragged_dkv(const BwdLaunch& a, int dtype);
+
+// Joins nparts parts of every query row (rows of no sequence are skipped).
+cudaError_t join_parts(const Geo& g, int dtype, const Parts& parts, int nparts,
+                       void* o, float* lse, cudaStream_t stream);
+// delta[t][h] = dout . o
+cudaError_t row_delta(const Geo& g, int dtype, const void* o, const void* dout, float* delta,
+                      cudaStream_t stream);
+// Sums the parts of dK, dV and rounds them.
+cudaError_t join_dkv(const BwdLaunch& a, int dtype);
+
+// Writes the token rows of k, v (rows kin, vin) into their slots of the cache.
+cudaError_t cache_append(const Geo& g, const Rows& kin, const Rows& vin, int elem_bytes,
+                         const void* k, const void* v, void* kc, void* vc, cudaStream_t s);
+
+}  // namespace rag
+}  // namespace st

@@ -1,0 +1,435 @@
+// C ABI of attention over ragged sequences and paged caches: argument checks,
+// workspace plans and launch sequences. See include/sparse_transformer_attn.h
+// for the contract of every entry point.
+#include <cmath>
+
+#include "ragged.h"
+
+using namespace st;
+using namespace st::rag;
+
+namespace {
+
+constexpr int kPartsLimit = 32;  // most key ranges of one row
+
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool known(st_dtype t) { return t == ST_F32 || t == ST_BF16 || t == ST_F16; }
+
+// The jobs (head class x query order) of a pattern.
+int make_jobs(const st_pattern_desc& p, Job jobs[2]) {
+  const bool split = p.head_mode == ST_HEADS_SPLIT;
+  auto one = [](int hc, int qv, int kv, int rule) {
+    return Job{hc, qv, 1, {{kv, rule}, {VIEW_NAT, RULE_CAUSAL}}};
+  };
+  if (p.kind == ST_DENSE_CAUSAL) {
+    jobs[0] = one(-1, VIEW_NAT, VIEW_NAT, RULE_CAUSAL);
+    return 1;
+  }
+  if (p.kind == ST_STRIDED) {
+    jobs[0] = one(split ? 0 : -1, VIEW_NAT, VIEW_NAT, RULE_BAND);
+    jobs[1] = one(split ? 1 : -1, VIEW_CLS, VIEW_CLS, split ? RULE_STRIDE : RULE_STRIDE_FAR);
+    return 2;
+  }
+  if (split) {
+    jobs[0] = one(0, VIEW_NAT, VIEW_NAT, RULE_BLOCK);
+    jobs[1] = one(1, VIEW_NAT, VIEW_SUM, RULE_SUMMARY);
+    return 2;
+  }
+  jobs[0] = Job{-1, VIEW_NAT, 2, {{VIEW_NAT, RULE_BLOCK}, {VIEW_SUM, RULE_SUMMARY_EARLIER}}};
+  return 1;
+}
+
+// Whether a row's result is joined from two query orders.
+bool two_orders(const st_pattern_desc& p) {
+  return p.kind == ST_STRIDED && p.head_mode == ST_HEADS_MERGED;
+}
+
+st_status check_pattern(const st_pattern_desc* p) {
+  if (!p || p->T < 1) return ST_ERR_INVALID;
+  if (p->kind != ST_STRIDED && p->kind != ST_FIXED && p->kind != ST_DENSE_CAUSAL)
+    return ST_ERR_INVALID;
+  if (p->kind != ST_DENSE_CAUSAL) {
+    if (p->head_mode != ST_HEADS_SPLIT && p->head_mode != ST_HEADS_MERGED) return ST_ERR_INVALID;
+    if (p->l < 1) return ST_ERR_INVALID;
+    if (p->kind == ST_FIXED && (p->c < 1 || p->c > p->l)) return ST_ERR_INVALID;
+  }
+  return ST_OK;
+}
+
+// Rows of d elements from token to token; false for a stride that is no
+// multiple of d or too small for the heads.
+bool stride_rows(int64_t stride, int heads, int d, int32_t* out) {
+  if (stride == 0) stride = (int64_t)heads * d;
+  if (stride < (int64_t)heads * d || stride % d) return false;
+  if (stride / d > 0x7fffffff) return false;
+  *out = (int32_t)(stride / d);
+  return true;
+}
+
+st_status fill_geo(const st_pattern_desc* p, st_dtype dtype, const st_packed_desc* x, bool sizes_16,
+                   Geo& g) {
+  st_status s = check_pattern(p);
+  if (s != ST_OK) return s;
+  if (!x || !known(dtype)) return ST_ERR_INVALID;
+  if (x->n_seqs < 1 || x->total < 0 || x->H < 1 || x->Hkv < 1 || x->d < 1 || x->H % x->Hkv)
+    return ST_ERR_INVALID;
+  if (sizes_16) {
+    const bool ok = dtype == ST_F32 ? (x->d == 32 || x->d == 64 || x->d == 128)
+                                    : (x->d == 64 || x->d == 128);
+    if (!ok) return ST_ERR_UNSUPPORTED;
+  }
+  g = Geo{};
+  g.S = x->n_seqs;
+  g.total = x->total;
+  g.H = x->H;
+  g.Hkv = x->Hkv;
+  g.G = x->H / x->Hkv;
+  g.d = x->d;
+  const bool dense = p->kind == ST_DENSE_CAUSAL;
+  g.l = dense ? 1 : p->l;
+  g.c = p->kind == ST_FIXED ? p->c : 1;
+  g.split = !dense && p->head_mode == ST_HEADS_SPLIT;
+  g.fl = make_fastdiv(g.l);
+  g.fc = make_fastdiv(g.c);
+  if (!stride_rows(x->q_stride, x->H, x->d, &g.q.tok) ||
+      !stride_rows(x->k_stride, x->Hkv, x->d, &g.k.tok) ||
+      !stride_rows(x->v_stride, x->Hkv, x->d, &g.v.tok))
+    return ST_ERR_INVALID;
+  g.q.head = g.k.head = g.v.head = 1;
+  // grids and row numbers are 31-bit
+  if ((int64_t)g.total * g.q.tok > 0x7fffffff || (int64_t)g.total * g.k.tok > 0x7fffffff ||
+      (int64_t)g.total * g.v.tok > 0x7fffffff || (int64_t)g.total * g.H > 0x7fffffff ||
+      (int64_t)g.total * g.G + g.S > 0x7fffffff || g.Hkv > 65535)
+    return ST_ERR_UNSUPPORTED;
+  return ST_OK;
+}
+
+st_status fill_cache(const st_cache_desc* c, Geo& g) {
+  if (!c || c->num_pages < 1 || c->page_size < 1 || c->max_pages < 1) return ST_ERR_INVALID;
+  const int64_t d = g.d;
+  if (c->page_stride < 0 || c->slot_stride < 0 || c->head_stride < 0 || c->page_stride % d ||
+      c->slot_stride % d || c->head_stride % d)
+    return ST_ERR_INVALID;
+  const int64_t last = (c->num_pages - 1) * (c->page_stride / d) +
+                       (c->page_size - 1) * (c->slot_stride / d) +
+                       (g.Hkv - 1) * (c->head_stride / d);
+  if (last >= 0x7fffffff || c->page_stride / d > 0x7fffffff ||
+      (int64_t)c->max_pages * c->page_size > 0x7fffffff ||
+      (int64_t)g.S * c->max_pages > 0x7fffffff)
+    return ST_ERR_UNSUPPORTED;
+  g.num_pages = c->num_pages;
+  g.page_size = c->page_size;
+  g.max_pages = c->max_pages;
+  g.fpage = make_fastdiv(c->page_size);
+  g.k.tok = (int32_t)(c->slot_stride / d);
+  g.k.head = (int32_t)(c->head_stride / d);
+  g.k.page = (int32_t)(c->page_stride / d);
+  g.v = g.k;
+  return ST_OK;
+}
+
+int64_t cache_rows(const Geo& g) {
+  return (int64_t)(g.num_pages - 1) * g.k.page + (int64_t)(g.page_size - 1) * g.k.tok +
+         (int64_t)(g.Hkv - 1) * g.k.head + 1;
+}
+
+// The status word of the current device; it is created by the first call
+// (which therefore may not be captured).
+st_status get_status(Geo& g, cudaStream_t stream) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
+  g.status = device_status(dev, false);
+  if (g.status) return ST_OK;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess || cap != cudaStreamCaptureStatusNone)
+    return ST_ERR_CUDA;
+  g.status = device_status(dev, true);
+  return g.status ? ST_OK : ST_ERR_CUDA;
+}
+
+// How a forward call is cut up.
+struct FwdPlan {
+  int nsplit;   // key ranges per unit and job
+  int nparts;   // parts of a row (0: rows are written directly)
+  bool merge;   // the second order joins the first's part itself
+  size_t parts_o, bytes;
+};
+
+// Key ranges: enough units for the GPU when there are few rows, none shorter
+// than `least` key tiles of the longest sequence.
+int choose_split(long long units, int longest_tiles, int least, int sms) {
+  if (units < 1) return 1;
+  long long n = (2LL * sms + units - 1) / units;
+  const long long cap = std::max(1, longest_tiles / least);
+  n = std::min(n, cap);
+  n = std::min<long long>(n, kPartsLimit);
+  return (int)std::max<long long>(1, n);
+}
+
+FwdPlan plan_fwd(const Geo& g, const st_pattern_desc& p, int nsplit) {
+  FwdPlan f{};
+  f.nsplit = nsplit;
+  const bool two = two_orders(p);
+  f.merge = two && nsplit == 1;
+  f.nparts = nsplit > 1 ? (two ? 2 * nsplit : nsplit) : two ? 1 : 0;
+  const size_t rows = (size_t)g.total * g.H;
+  f.parts_o = round256(rows * g.d * sizeof(float) * f.nparts);
+  f.bytes = f.nparts ? f.parts_o + round256(rows * sizeof(float) * f.nparts) : 0;
+  return f;
+}
+
+bool workspace_ok(const void* ws, size_t have, size_t need) {
+  return need == 0 || (ws && have >= need && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0);
+}
+
+// Rows that one query row's pattern lets it attend, at most, in a sequence of T.
+int most_keys(const st_pattern_desc& p) {
+  if (p.kind == ST_DENSE_CAUSAL) return p.T;
+  const long long a = p.kind == ST_STRIDED ? (long long)p.l + 1 : p.l;
+  const long long b = p.kind == ST_STRIDED ? (p.T + p.l - 1LL) / p.l
+                                           : ((long long)p.T / p.l + 1) * p.c;
+  return (int)std::min<long long>(p.T, p.head_mode == ST_HEADS_MERGED ? a + b : std::max(a, b));
+}
+
+int fwd_split(const Geo& g, const st_pattern_desc& p) {
+  const long long units = ((long long)g.total * g.G + 63) / 64 * g.Hkv;
+  return choose_split(units, (most_keys(p) + 63) / 64, 8, sm_count());
+}
+
+st_status run_fwd(const st_pattern_desc& p, st_dtype dtype, Geo& g, float scale, const FwdPlan& f,
+                  const void* q, const void* k, const void* v, void* o, float* lse, void* ws,
+                  int64_t q_rows, int64_t k_rows, int64_t v_rows, cudaStream_t stream) {
+  FwdLaunch a{};
+  a.g = g;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.lse = lse;
+  a.q_rows = q_rows;
+  a.k_rows = k_rows;
+  a.v_rows = v_rows;
+  a.parts.o = static_cast<float*>(ws);
+  a.parts.lse = reinterpret_cast<float*>(static_cast<char*>(ws) + f.parts_o);
+  a.nsplit = f.nsplit;
+  a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)g.d)) * 1.4426950408889634f;
+  a.wait_ns = wait_limit_ns();
+  a.stream = stream;
+  Job jobs[2];
+  const int n = make_jobs(p, jobs);
+  cudaError_t e = cudaSuccess;
+  for (int j = 0; j < n && e == cudaSuccess; ++j) {
+    a.job = jobs[j];
+    a.part0 = two_orders(p) && j == 1 && !f.merge ? f.nsplit : 0;
+    a.mode = f.merge ? (j == 0 ? OUT_PARTIAL : OUT_MERGE) : f.nparts ? OUT_PARTIAL : OUT_FINAL;
+    e = simt_ragged_fwd(a, dtype);
+  }
+  if (e == cudaSuccess && f.nparts && !f.merge)
+    e = join_parts(g, dtype, a.parts, f.nparts, o, lse, stream);
+  return e == cudaSuccess ? ST_OK : ST_ERR_CUDA;
+}
+
+// How a backward call is cut up: key jobs (one segment each), query-row ranges
+// per key tile.
+struct BwdPlan {
+  Job kjob[2];
+  int njobs, nsplit;
+  bool parts;
+  size_t delta, dq_part, parts_bytes, bytes;
+};
+
+BwdPlan plan_bwd(const Geo& g, const st_pattern_desc& p) {
+  BwdPlan b{};
+  Job jobs[2];
+  const int n = make_jobs(p, jobs);
+  for (int j = 0; j < n; ++j)
+    for (int s = 0; s < jobs[j].nseg; ++s)
+      b.kjob[b.njobs++] = Job{jobs[j].hc, jobs[j].qview, 1, {jobs[j].seg[s], jobs[j].seg[s]}};
+  const long long units = ((long long)g.total + 63) / 64 * g.Hkv;
+  long long rows = (long long)p.T * g.G;  // query rows that reach one key, at most
+  b.nsplit = choose_split(units, (int)std::min<long long>((rows + 63) / 64, 1 << 20), 8, sm_count());
+  // one part is enough only where every key head has one job over all its keys
+  b.parts = b.nsplit > 1 || (b.njobs == 2 && !(g.split && g.G == 1 && b.kjob[1].seg[0].kview != VIEW_SUM));
+  const size_t qrows = (size_t)g.total * g.H, krows = (size_t)g.total * g.Hkv;
+  b.delta = round256(qrows * sizeof(float));
+  b.dq_part = two_orders(p) ? round256(qrows * g.d * sizeof(float)) : 0;
+  b.parts_bytes = b.parts ? round256(krows * 2 * g.d * sizeof(float) * b.njobs * b.nsplit) : 0;
+  b.bytes = b.delta + b.dq_part + b.parts_bytes;
+  return b;
+}
+
+}  // namespace
+
+extern "C" {
+
+st_status st_packed_attn_fwd_workspace(const st_pattern_desc* p, st_dtype dtype,
+                                       const st_packed_desc* x, size_t* bytes) {
+  Geo g;
+  if (!bytes) return ST_ERR_INVALID;
+  st_status s = fill_geo(p, dtype, x, true, g);
+  if (s != ST_OK) return s;
+  *bytes = plan_fwd(g, *p, fwd_split(g, *p)).bytes;
+  return ST_OK;
+}
+
+st_status st_packed_attn_fwd(const st_pattern_desc* p, st_dtype dtype, const st_packed_desc* x,
+                             float scale, const void* q, const void* k, const void* v,
+                             const int32_t* cu, void* o, float* lse, void* ws, size_t ws_bytes,
+                             void* stream) {
+  Geo g;
+  st_status s = fill_geo(p, dtype, x, true, g);
+  if (s != ST_OK) return s;
+  if (g.total == 0) return ST_OK;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) ||
+      !aligned4(cu))
+    return ST_ERR_INVALID;
+  const FwdPlan f = plan_fwd(g, *p, fwd_split(g, *p));
+  if (!workspace_ok(ws, ws_bytes, f.bytes)) return ST_ERR_WORKSPACE;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  s = get_status(g, cs);
+  if (s != ST_OK) return s;
+  g.cu = cu;
+  return run_fwd(*p, dtype, g, scale, f, q, k, v, o, lse, ws,
+                 (int64_t)(g.total - 1) * g.q.tok + g.H, (int64_t)(g.total - 1) * g.k.tok + g.Hkv,
+                 (int64_t)(g.total - 1) * g.v.tok + g.Hkv, cs);
+}
+
+st_status st_packed_attn_bwd_workspace(const st_pattern_desc* p, st_dtype dtype,
+                                       const st_packed_desc* x, size_t* bytes) {
+  Geo g;
+  if (!bytes) return ST_ERR_INVALID;
+  st_status s = fill_geo(p, dtype, x, true, g);
+  if (s != ST_OK) return s;
+  *bytes = plan_bwd(g, *p).bytes;
+  return ST_OK;
+}
+
+st_status st_packed_attn_bwd(const st_pattern_desc* p, st_dtype dtype, const st_packed_desc* x,
+                             float scale, const void* q, const void* k, const void* v,
+                             const void* o, const float* lse, const void* dout, const int32_t* cu,
+                             void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                             void* stream) {
+  Geo g;
+  st_status s = fill_geo(p, dtype, x, true, g);
+  if (s != ST_OK) return s;
+  BwdLaunch a{};
+  if (!stride_rows(x->dq_stride, g.H, g.d, &a.dq_rows.tok) ||
+      !stride_rows(x->dk_stride, g.Hkv, g.d, &a.dk_rows.tok) ||
+      !stride_rows(x->dv_stride, g.Hkv, g.d, &a.dv_rows.tok))
+    return ST_ERR_INVALID;
+  a.dq_rows.head = a.dk_rows.head = a.dv_rows.head = 1;
+  if (g.total == 0) return ST_OK;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) ||
+      !aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned4(cu))
+    return ST_ERR_INVALID;
+  const BwdPlan b = plan_bwd(g, *p);
+  if (!workspace_ok(ws, ws_bytes, b.bytes)) return ST_ERR_WORKSPACE;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  s = get_status(g, cs);
+  if (s != ST_OK) return s;
+  g.cu = cu;
+  a.g = g;
+  for (int j = 0; j < 2; ++j) a.job[j] = b.kjob[j];
+  a.njobs = b.njobs;
+  a.nsplit = b.nsplit;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.dout = dout;
+  a.lse = lse;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  char* w = static_cast<char*>(ws);
+  float* delta = reinterpret_cast<float*>(w);
+  a.delta = delta;
+  a.dq_part = reinterpret_cast<float*>(w + b.delta);
+  a.parts = reinterpret_cast<float*>(w + b.delta + b.dq_part);
+  a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)g.d);
+  a.wait_ns = wait_limit_ns();
+  a.q_rows = (int64_t)(g.total - 1) * g.q.tok + g.H;
+  a.k_rows = (int64_t)(g.total - 1) * g.k.tok + g.Hkv;
+  a.v_rows = (int64_t)(g.total - 1) * g.v.tok + g.Hkv;
+  a.stream = cs;
+  cudaError_t e = row_delta(g, dtype, o, dout, delta, cs);
+  if (e == cudaSuccess) e = simt_ragged_dkv(a, dtype);
+  if (e == cudaSuccess && b.parts) e = join_dkv(a, dtype);
+  Job jobs[2];
+  const int n = make_jobs(*p, jobs);
+  for (int j = 0; j < n && e == cudaSuccess; ++j)
+    e = simt_ragged_dq(a, jobs[j],
+                       two_orders(*p) ? (j == 0 ? OUT_PARTIAL : OUT_MERGE) : OUT_FINAL, dtype);
+  return e == cudaSuccess ? ST_OK : ST_ERR_CUDA;
+}
+
+st_status st_paged_attn_workspace(const st_pattern_desc* p, st_dtype dtype,
+                                  const st_packed_desc* x, const st_cache_desc* c, int32_t max_q,
+                                  size_t* bytes) {
+  Geo g;
+  if (!bytes || max_q < 1) return ST_ERR_INVALID;
+  st_status s = fill_geo(p, dtype, x, true, g);
+  if (s == ST_OK) s = fill_cache(c, g);
+  if (s != ST_OK) return s;
+  *bytes = plan_fwd(g, *p, fwd_split(g, *p)).bytes;
+  return ST_OK;
+}
+
+st_status st_paged_attn(const st_pattern_desc* p, st_dtype dtype, const st_packed_desc* x,
+                        const st_cache_desc* c, int32_t max_q, float scale, const void* q,
+                        const void* kc, const void* vc, const int32_t* table, const int32_t* cu,
+                        const int32_t* kv_lens, void* o, float* lse, void* ws, size_t ws_bytes,
+                        void* stream) {
+  Geo g;
+  if (max_q < 1) return ST_ERR_INVALID;
+  st_status s = fill_geo(p, dtype, x, true, g);
+  if (s == ST_OK) s = fill_cache(c, g);
+  if (s != ST_OK) return s;
+  if (g.total == 0) return ST_OK;
+  if (!aligned16(q) || !aligned16(kc) || !aligned16(vc) || !aligned16(o) || !aligned16(lse) ||
+      !aligned4(cu) || !aligned4(kv_lens) || !aligned4(table))
+    return ST_ERR_INVALID;
+  const FwdPlan f = plan_fwd(g, *p, fwd_split(g, *p));
+  if (!workspace_ok(ws, ws_bytes, f.bytes)) return ST_ERR_WORKSPACE;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  s = get_status(g, cs);
+  if (s != ST_OK) return s;
+  g.cu = cu;
+  g.kv_lens = kv_lens;
+  g.table = table;
+  return run_fwd(*p, dtype, g, scale, f, q, kc, vc, o, lse, ws,
+                 (int64_t)(g.total - 1) * g.q.tok + g.H, cache_rows(g), cache_rows(g), cs);
+}
+
+st_status st_cache_append(st_dtype dtype, const st_packed_desc* x, const st_cache_desc* c,
+                          const void* k, const void* v, void* kc, void* vc, const int32_t* table,
+                          const int32_t* cu, const int32_t* kv_lens, void* stream) {
+  Geo g;
+  const st_pattern_desc dense = {ST_DENSE_CAUSAL, ST_HEADS_MERGED, 1, 1, 1};
+  if (!x) return ST_ERR_INVALID;
+  st_packed_desc y = *x;
+  y.H = y.Hkv;
+  y.q_stride = 0;
+  st_status s = fill_geo(&dense, dtype, &y, false, g);
+  if (s != ST_OK) return s;
+  if (g.d % (dtype == ST_F32 ? 4 : 8)) return ST_ERR_UNSUPPORTED;
+  Geo gc = g;
+  s = fill_cache(c, gc);
+  if (s != ST_OK) return s;
+  if (g.total == 0) return ST_OK;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(kc) || !aligned16(vc) || !aligned4(table) ||
+      !aligned4(cu) || !aligned4(kv_lens))
+    return ST_ERR_INVALID;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  s = get_status(gc, cs);
+  if (s != ST_OK) return s;
+  gc.cu = cu;
+  gc.kv_lens = kv_lens;
+  gc.table = table;
+  return cache_append(gc, g.k, g.v, dtype == ST_F32 ? 4 : 2, k, v, kc, vc, cs) == cudaSuccess
+             ? ST_OK
+             : ST_ERR_CUDA;
+}
+
+}  // extern "C"

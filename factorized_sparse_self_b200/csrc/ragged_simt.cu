@@ -1,0 +1,769 @@
+// CUDA-core kernels for attention over ragged sequences: the float32 forward
+// and backward (fp32 products and sums throughout), and the streaming kernels
+// around every path (delta, joins of parts).
+//
+// One block of 256 threads (16 x 16) owns 64 rows; 64 x 64 tiles of products
+// come from shared memory with a 4 x 4 micro-tile per thread. At 64 rows the
+// products do 16 FMAs for 2 float4 loads, so the kernels are bound by shared
+// memory and the FMA pipe together.
+#include "ragged.h"
+
+namespace st {
+namespace rag {
+namespace {
+
+constexpr int BM = 64;   // rows of a unit
+constexpr int BN = 64;   // rows of the tiles it meets
+constexpr int NT = 256;
+constexpr int SP = BN + 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+template <class T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+  return __ldg(reinterpret_cast<const float4*>(p));
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+template <>
+__device__ __forceinline__ float4 load4<__half>(const __half* p) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+template <class T>
+__device__ __forceinline__ T round_to(float x);
+template <>
+__device__ __forceinline__ float round_to<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+template <>
+__device__ __forceinline__ __half round_to<__half>(float x) {
+  return __float2half_rn(x);
+}
+
+// Copies 64 rows of D elements into dst [64][D + 4] as fp32; row(i) gives the
+// row index of tile row i, or -1 for a row of zeros.
+template <int D, class T, class F>
+__device__ __forceinline__ void load_rows(float* dst, const T* base, F row) {
+  constexpr int C4 = D / 4;
+  for (int x = threadIdx.x; x < BM * C4; x += NT) {
+    const int i = x / C4, c = x - i * C4;
+    const int r = row(i);
+    const float4 v = r >= 0 ? load4(base + (size_t)r * D + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<float4*>(dst + i * (D + 4) + c * 4) = v;
+  }
+}
+
+// acc[i][j] += A[4 ty + i] . B[tx + 16 j] over D
+template <int D>
+__device__ __forceinline__ void dot_tile(const float* A, const float* B, int ty, int tx,
+                                         float acc[4][4]) {
+#pragma unroll 4
+  for (int k = 0; k < D; k += 4) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * (D + 4) + k);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      b[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * (D + 4) + k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z,
+                         fmaf(a[i].w, b[j].w, acc[i][j]))));
+  }
+}
+
+// acc[i][j] += sum_k W[4 ty + i][k] * B[k][tx + 16 j]
+template <int D>
+__device__ __forceinline__ void weigh_tile(const float* W, const float* B, int ty, int tx,
+                                           float acc[4][D / 16]) {
+#pragma unroll 4
+  for (int k = 0; k < BN; ++k) {
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = W[(4 * ty + i) * SP + k];
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+      const float b = B[k * (D + 4) + tx + 16 * j];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i][j] = fmaf(w[i], b, acc[i][j]);
+    }
+  }
+}
+
+// Query row x of a unit's order: token row (absolute), head, position; false
+// past the unit's rows.
+struct QRow {
+  int t, h, pos;
+};
+__device__ __forceinline__ bool query_at(const Geo& g, const Seq& q, int view, const Heads3& hs,
+                                         int x, QRow& r) {
+  if (x >= q.nq * hs.n) return false;
+  const int e = x / hs.n;
+  const int row = query_row(g, q, view, e);
+  r.t = q.qb + row;
+  r.pos = row + q.off;
+  r.h = hs.first + hs.step * (x - e * hs.n);
+  return true;
+}
+
+// First and last key tile of the unit's rows x0 .. x0+BM-1 in a segment.
+__device__ __forceinline__ void tile_range(const Geo& g, const Seq& q, const Job& job, int seg,
+                                           const Heads3& hs, int x0, int rows, int bn, int& j0,
+                                           int& j1) {
+  j0 = j1 = 0;
+  int v0, v1;
+  valid_rows(q, job.qview, v0, v1);
+  const int e0 = imax(x0 / hs.n, v0), e1 = imin((imin(x0 + rows, q.nq * hs.n) - 1) / hs.n, v1 - 1);
+  if (e0 > e1) return;
+  int lo, hi, a, b;
+  live_keys(g, q, job.seg[seg].rule, query_row(g, q, job.qview, e0) + q.off, lo, hi);
+  live_keys(g, q, job.seg[seg].rule, query_row(g, q, job.qview, e1) + q.off, a, b);
+  if (b > lo) {
+    j0 = lo / bn;
+    j1 = (b + bn - 1) / bn;
+  }
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(NT) ragged_fwd_simt(const __grid_constant__ FwdLaunch a) {
+  extern __shared__ float sm[];
+  float* A = sm;
+  float* B = A + BM * (D + 4);
+  float* W = B + BN * (D + 4);
+  float* scl = W + BM * SP;  // per row: factor of the old accumulator
+  float* den = scl + BM;     // per row: 1 / sum, at the end
+  const Geo& g = a.g;
+  const int kvh = blockIdx.y, part = blockIdx.z;
+  int tile;
+  const int s = find_slot(g, most_heads(g, a.job.hc), BM, gridDim.x - 1 - blockIdx.x, tile);
+  const Seq q = load_seq(g, s);
+  const Heads3 hs = heads_of_group(g, a.job.hc, kvh);
+  const int x0 = tile * BM;
+  if (hs.n == 0 || x0 >= q.nq * hs.n) return;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const T* qp = static_cast<const T*>(a.q);
+  const T* kp = static_cast<const T*>(a.k);
+  const T* vp = static_cast<const T*>(a.v);
+  load_rows<D>(A, qp, [&](int i) {
+    QRow r;
+    return query_at(g, q, a.job.qview, hs, x0 + i, r) ? q_row(g, r.t, r.h) : -1;
+  });
+  float acc[4][D / 16] = {};
+  // softmax state of row tid / 4, kept by four threads
+  const int row = tid >> 2;
+  QRow qr;
+  const bool have = query_at(g, q, a.job.qview, hs, x0 + row, qr);
+  float m = -INFINITY, sum = 0.f;
+  int cnt[2] = {0, 0}, j0[2] = {0, 0}, total = 0;
+  for (int sg = 0; sg < a.job.nseg; ++sg) {
+    int j1;
+    tile_range(g, q, a.job, sg, hs, x0, BM, BN, j0[sg], j1);
+    cnt[sg] = j1 - j0[sg];
+    total += cnt[sg];
+  }
+  const int it1 = (int)((long long)total * (part + 1) / a.nsplit);
+  for (int it = (int)((long long)total * part / a.nsplit); it < it1; ++it) {
+    const int sg = it >= cnt[0] ? 1 : 0;
+    const int kb = (j0[sg] + it - (sg ? cnt[0] : 0)) * BN;
+    const int nk = n_keys(q, a.job.seg[sg].kview);
+    __syncthreads();
+    load_rows<D>(B, kp, [&](int i) {
+      return kb + i < nk ? kv_row(g, g.k, q, key_pos(g, q, a.job.seg[sg].kview, kb + i), kvh) : -1;
+    });
+    __syncthreads();
+    float sc[4][4] = {};
+    dot_tile<D>(A, B, ty, tx, sc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) W[(4 * ty + i) * SP + tx + 16 * j] = sc[i][j] * a.scale_log2;
+    __syncthreads();
+    load_rows<D>(B, vp, [&](int i) {
+      return kb + i < nk ? kv_row(g, g.v, q, key_pos(g, q, a.job.seg[sg].kview, kb + i), kvh) : -1;
+    });
+    int lo = 0, hi = 0;
+    if (have && qr.pos >= 0) live_keys(g, q, a.job.seg[sg].rule, qr.pos, lo, hi);
+    float mt = -INFINITY;
+    for (int x = tid & 3; x < BN; x += 4) {
+      const int k = kb + x;
+      float v = W[row * SP + x];
+      v = (k >= lo && k < hi) ? v : -INFINITY;
+      W[row * SP + x] = v;
+      mt = fmaxf(mt, v);
+    }
+    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+    const float mn = fmaxf(m, mt);
+    const float mu = mn == -INFINITY ? 0.f : mn;
+    const float al = exp2f(m - mu);
+    float ps = 0.f;
+    for (int x = tid & 3; x < BN; x += 4) {
+      const float p = exp2f(W[row * SP + x] - mu);
+      W[row * SP + x] = p;
+      ps += p;
+    }
+    ps += __shfl_xor_sync(0xffffffffu, ps, 1);
+    ps += __shfl_xor_sync(0xffffffffu, ps, 2);
+    sum = sum * al + ps;
+    m = mn;
+    if ((tid & 3) == 0) scl[row] = al;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = scl[4 * ty + i];
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) acc[i][j] *= f;
+    }
+    weigh_tile<D>(W, B, ty, tx, acc);
+  }
+  // log-sum-exp of the row; joined with the other order's where asked
+  const float lse = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+  float wc = sum > 0.f ? 1.f / sum : 0.f, wp = 0.f, out = lse;
+  const size_t rr = have ? (size_t)qr.t * g.H + qr.h : 0;
+  if (a.mode == OUT_MERGE && have) {
+    const float lp = a.parts.lse[rr];
+    const float mx = fmaxf(lp, lse);
+    if (mx > -INFINITY) {
+      out = mx + logf(expf(lp - mx) + expf(lse - mx));
+      wp = expf(lp - out);
+      wc *= expf(lse - out);
+    }
+  }
+  __syncthreads();
+  if ((tid & 3) == 0) {
+    scl[row] = wp;
+    den[row] = wc;
+    if (have) {
+      if (a.mode == OUT_PARTIAL)
+        a.parts.lse[(size_t)(a.part0 + part) * g.total * g.H + rr] = out;
+      else
+        a.lse[rr] = out;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    QRow r;
+    if (!query_at(g, q, a.job.qview, hs, x0 + 4 * ty + i, r)) continue;
+    const size_t o = ((size_t)r.t * g.H + r.h) * D;
+    const float f = den[4 * ty + i], fp = scl[4 * ty + i];
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+      const int c = tx + 16 * j;
+      float v = acc[i][j] * f;
+      if (a.mode == OUT_PARTIAL) {
+        a.parts.o[(size_t)(a.part0 + part) * g.total * g.H * D + o + c] = v;
+      } else {
+        if (a.mode == OUT_MERGE && fp > 0.f) v = fmaf(fp, a.parts.o[o + c], v);
+        static_cast<T*>(a.o)[o + c] = round_to<T>(v);
+      }
+    }
+  }
+}
+
+// dQ of 64 query rows: S and dP = dO V^T again, dS = P (dP - delta), dQ += dS K.
+template <int D, class T>
+__global__ void __launch_bounds__(NT) ragged_dq_simt(const __grid_constant__ BwdLaunch a,
+                                                     const __grid_constant__ Job job, int mode) {
+  extern __shared__ float sm[];
+  float* A = sm;
+  float* A2 = A + BM * (D + 4);
+  float* B = A2 + BM * (D + 4);
+  float* B2 = B + BN * (D + 4);
+  float* W = B2 + BN * (D + 4);
+  __shared__ float sl[BM], sd[BM];
+  __shared__ int slo[BM], shi[BM];
+  const Geo& g = a.g;
+  const int kvh = blockIdx.y;
+  int tile;
+  const int s = find_slot(g, most_heads(g, job.hc), BM, gridDim.x - 1 - blockIdx.x, tile);
+  const Seq q = load_seq(g, s);
+  const Heads3 hs = heads_of_group(g, job.hc, kvh);
+  const int x0 = tile * BM;
+  if (hs.n == 0 || x0 >= q.nq * hs.n) return;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const T *kp = static_cast<const T*>(a.k), *vp = static_cast<const T*>(a.v);
+  load_rows<D>(A, static_cast<const T*>(a.q), [&](int i) {
+    QRow r;
+    return query_at(g, q, job.qview, hs, x0 + i, r) ? q_row(g, r.t, r.h) : -1;
+  });
+  load_rows<D>(A2, static_cast<const T*>(a.dout), [&](int i) {
+    QRow r;
+    return query_at(g, q, job.qview, hs, x0 + i, r) ? r.t * g.H + r.h : -1;
+  });
+  QRow mine = {0, 0, -1};
+  if (tid < BM) {
+    const bool have = query_at(g, q, job.qview, hs, x0 + tid, mine);
+    sl[tid] = have ? a.lse[(size_t)mine.t * g.H + mine.h] * kLog2e : 0.f;
+    sd[tid] = have ? a.delta[(size_t)mine.t * g.H + mine.h] : 0.f;
+    if (!have) mine.pos = -1;
+  }
+  const float sc2 = a.scale * kLog2e;
+  float acc[4][D / 16] = {};
+  for (int sg = 0; sg < job.nseg; ++sg) {
+    int j0, j1;
+    tile_range(g, q, job, sg, hs, x0, BM, BN, j0, j1);
+    const int nk = n_keys(q, job.seg[sg].kview);
+    __syncthreads();
+    if (tid < BM) {
+      int lo = 0, hi = 0;
+      if (mine.pos >= 0) live_keys(g, q, job.seg[sg].rule, mine.pos, lo, hi);
+      slo[tid] = lo;
+      shi[tid] = hi;
+    }
+    for (int j = j0; j < j1; ++j) {
+      const int kb = j * BN;
+      __syncthreads();
+      load_rows<D>(B, kp, [&](int i) {
+        return kb + i < nk ? kv_row(g, g.k, q, key_pos(g, q, job.seg[sg].kview, kb + i), kvh) : -1;
+      });
+      load_rows<D>(B2, vp, [&](int i) {
+        return kb + i < nk ? kv_row(g, g.v, q, key_pos(g, q, job.seg[sg].kview, kb + i), kvh) : -1;
+      });
+      __syncthreads();
+      float sc[4][4] = {}, dp[4][4] = {};
+      dot_tile<D>(A, B, ty, tx, sc);
+      dot_tile<D>(A2, B2, ty, tx, dp);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          const int r = 4 * ty + i, k = kb + tx + 16 * jj;
+          const bool live = k >= slo[r] && k < shi[r];
+          W[r * SP + tx + 16 * jj] =
+              live ? exp2f(sc[i][jj] * sc2 - sl[r]) * (dp[i][jj] - sd[r]) : 0.f;
+        }
+      __syncthreads();
+      weigh_tile<D>(W, B, ty, tx, acc);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    QRow r;
+    if (!query_at(g, q, job.qview, hs, x0 + 4 * ty + i, r)) continue;
+    const size_t po = ((size_t)r.t * g.H + r.h) * D;
+    const size_t o = ((size_t)r.t * a.dq_rows.tok + r.h * a.dq_rows.head) * D;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+      const int c = tx + 16 * j;
+      float v = acc[i][j] * a.scale;
+      if (mode == OUT_PARTIAL) {
+        a.dq_part[po + c] = v;
+      } else {
+        if (mode == OUT_MERGE) v += a.dq_part[po + c];
+        static_cast<T*>(a.dq)[o + c] = round_to<T>(v);
+      }
+    }
+  }
+}
+
+// Key heads that a job reaches: whether any query head of the group is in its
+// class.
+__device__ __forceinline__ bool job_reaches(const Geo& g, const Job& job, int kvh) {
+  return heads_of_group(g, job.hc, kvh).n > 0;
+}
+// Whether kvh's dK, dV come from one unit alone and are written by it: one key
+// range, one job, and an order that lists every key.
+__device__ __forceinline__ bool dkv_direct(const BwdLaunch& a, int kvh) {
+  if (a.nsplit > 1) return false;
+  int n = 0, view = VIEW_NAT;
+  for (int j = 0; j < a.njobs; ++j)
+    if (job_reaches(a.g, a.job[j], kvh)) {
+      ++n;
+      view = a.job[j].seg[0].kview;
+    }
+  return n == 1 && view != VIEW_SUM;
+}
+
+// dK, dV of 64 keys: S^T, dP^T = V dO^T, P^T and dS^T, dV += P^T dO, dK += dS^T Q.
+template <int D, class T>
+__global__ void __launch_bounds__(NT) ragged_dkv_simt(const __grid_constant__ BwdLaunch a) {
+  extern __shared__ float sm[];
+  float* A = sm;
+  float* A2 = A + BM * (D + 4);
+  float* B = A2 + BM * (D + 4);
+  float* B2 = B + BN * (D + 4);
+  float* W = B2 + BN * (D + 4);
+  float* W2 = W + BM * SP;
+  __shared__ float sl[BN], sd[BN];
+  __shared__ int sa[BM], sb[BM], lim[2];
+  const Geo& g = a.g;
+  const int kvh = blockIdx.y;
+  const int jb = blockIdx.z / a.nsplit, split = blockIdx.z - jb * a.nsplit;
+  const Job& job = a.job[jb];
+  int tile;
+  const int s = find_slot(g, 1, BM, blockIdx.x, tile);
+  const Seq q = load_seq(g, s);
+  const Heads3 hs = heads_of_group(g, job.hc, kvh);
+  const int view = job.seg[0].kview, rule = job.seg[0].rule;
+  const int k0 = tile * BM, nk = n_keys(q, view);
+  if (hs.n == 0 || k0 >= nk) return;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const T *kp = static_cast<const T*>(a.k), *vp = static_cast<const T*>(a.v);
+  load_rows<D>(A, kp, [&](int i) {
+    return k0 + i < nk ? kv_row(g, g.k, q, key_pos(g, q, view, k0 + i), kvh) : -1;
+  });
+  load_rows<D>(A2, vp, [&](int i) {
+    return k0 + i < nk ? kv_row(g, g.v, q, key_pos(g, q, view, k0 + i), kvh) : -1;
+  });
+  if (tid < BM) {
+    int x = 0, y = 0;
+    if (k0 + tid < nk) live_queries(g, q, job.qview, rule, k0 + tid, x, y);
+    sa[tid] = x * hs.n;
+    sb[tid] = y * hs.n;
+    if (tid == 0) lim[0] = x * hs.n;
+    if (k0 + tid == imin(k0 + BM, nk) - 1) lim[1] = y * hs.n;
+  }
+  __syncthreads();
+  const int t0 = lim[0] / BN, t1 = lim[1] > lim[0] ? (lim[1] + BN - 1) / BN : t0;
+  const int tb = t0 + (int)((long long)(t1 - t0) * split / a.nsplit);
+  const int te = t0 + (int)((long long)(t1 - t0) * (split + 1) / a.nsplit);
+  const float sc2 = a.scale * kLog2e;
+  float dk[4][D / 16] = {}, dv[4][D / 16] = {};
+  for (int t = tb; t < te; ++t) {
+    const int xb = t * BN;
+    __syncthreads();
+    load_rows<D>(B, static_cast<const T*>(a.q), [&](int i) {
+      QRow r;
+      return query_at(g, q, job.qview, hs, xb + i, r) ? q_row(g, r.t, r.h) : -1;
+    });
+    load_rows<D>(B2, static_cast<const T*>(a.dout), [&](int i) {
+      QRow r;
+      return query_at(g, q, job.qview, hs, xb + i, r) ? r.t * g.H + r.h : -1;
+    });
+    if (tid < BN) {
+      QRow r;
+      const bool have = query_at(g, q, job.qview, hs, xb + tid, r);
+      sl[tid] = have ? a.lse[(size_t)r.t * g.H + r.h] * kLog2e : 0.f;
+      sd[tid] = have ? a.delta[(size_t)r.t * g.H + r.h] : 0.f;
+    }
+    __syncthreads();
+    float sc[4][4] = {}, dp[4][4] = {};
+    dot_tile<D>(A, B, ty, tx, sc);
+    dot_tile<D>(A2, B2, ty, tx, dp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 4 * ty + i, cq = tx + 16 * j, x = xb + cq;
+        const bool live = x >= sa[r] && x < sb[r];
+        const float p = live ? exp2f(sc[i][j] * sc2 - sl[cq]) : 0.f;
+        W[r * SP + cq] = p;
+        W2[r * SP + cq] = live ? p * (dp[i][j] - sd[cq]) : 0.f;
+      }
+    __syncthreads();
+    weigh_tile<D>(W, B2, ty, tx, dv);
+    weigh_tile<D>(W2, B, ty, tx, dk);
+  }
+  const bool direct = dkv_direct(a, kvh);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = k0 + 4 * ty + i;
+    if (k >= nk) continue;
+    const int t = q.qb + key_pos(g, q, view, k);
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+      const int c = tx + 16 * j;
+      if (direct) {
+        static_cast<T*>(a.dk)[((size_t)t * a.dk_rows.tok + kvh * a.dk_rows.head) * D + c] =
+            round_to<T>(dk[i][j] * a.scale);
+        static_cast<T*>(a.dv)[((size_t)t * a.dv_rows.tok + kvh * a.dv_rows.head) * D + c] =
+            round_to<T>(dv[i][j]);
+      } else {
+        float* p = a.parts + (((size_t)blockIdx.z * g.total + t) * g.Hkv + kvh) * 2 * D;
+        p[c] = dk[i][j] * a.scale;
+        p[D + c] = dv[i][j];
+      }
+    }
+  }
+}
+
+// Sequence of token row t, or false for a row of no sequence.
+__device__ __forceinline__ bool seq_of_token(const Geo& g, int t, int& s) {
+  if (t < cu_at(g, 0) || t >= cu_at(g, g.S)) return false;
+  int a = 0, b = g.S - 1;
+  while (a < b) {  // last sequence that starts at or before t
+    const int m = (a + b + 1) >> 1;
+    if (cu_at(g, m) <= t) a = m;
+    else b = m - 1;
+  }
+  s = a;
+  return t < cu_at(g, a + 1);
+}
+
+constexpr int kJoinRows = 8;  // rows (warps) of a block of the streaming kernels
+
+// One warp per query row: o = sum_p exp(lse_p - lse) o_p.
+template <class T>
+__global__ void __launch_bounds__(32 * kJoinRows)
+    join_parts_kernel(const __grid_constant__ Geo g, const Parts parts, int nparts, T* o,
+                      float* lse) {
+  const long long row = (long long)blockIdx.x * kJoinRows + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const long long rows = (long long)g.total * g.H;
+  if (row >= rows) return;
+  int s;
+  if (!seq_of_token(g, (int)(row / g.H), s)) return;
+  float m = -INFINITY;
+  for (int p = lane; p < nparts; p += 32) m = fmaxf(m, parts.lse[p * rows + row]);
+#pragma unroll
+  for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  float sum = 0.f;
+  if (m > -INFINITY)
+    for (int p = lane; p < nparts; p += 32) sum += expf(parts.lse[p * rows + row] - m);
+#pragma unroll
+  for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  const float L = m > -INFINITY ? m + logf(sum) : -INFINITY;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  if (m > -INFINITY)
+    for (int p = 0; p < nparts; ++p) {
+      const float w = expf(parts.lse[p * rows + row] - L);
+      if (w == 0.f) continue;
+      const float* src = parts.o + (p * rows + row) * g.d;
+      for (int x = 0, c = lane; c < g.d; ++x, c += 32) acc[x] = fmaf(w, src[c], acc[x]);
+    }
+  for (int x = 0, c = lane; c < g.d; ++x, c += 32) o[row * g.d + c] = round_to<T>(acc[x]);
+  if (lane == 0) lse[row] = L;
+}
+
+template <class T>
+__global__ void __launch_bounds__(32 * kJoinRows)
+    row_delta_kernel(long long rows, int d, const T* o, const T* dout, float* delta) {
+  const long long row = (long long)blockIdx.x * kJoinRows + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  float acc = 0.f;
+  for (int c = lane * 4; c < d; c += 128) {
+    const float4 x = load4(o + row * d + c), y = load4(dout + row * d + c);
+    acc = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, acc))));
+  }
+#pragma unroll
+  for (int x = 16; x; x >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, x);
+  if (lane == 0) delta[row] = acc;
+}
+
+// One warp per key row and head: the parts that hold it, added in order.
+template <class T>
+__global__ void __launch_bounds__(32 * kJoinRows) join_dkv_kernel(const __grid_constant__ BwdLaunch a) {
+  const Geo& g = a.g;
+  const long long row = (long long)blockIdx.x * kJoinRows + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const long long rows = (long long)g.total * g.Hkv;
+  if (row >= rows) return;
+  const int t = (int)(row / g.Hkv), kvh = (int)(row - (long long)t * g.Hkv);
+  if (dkv_direct(a, kvh)) return;
+  int s;
+  if (!seq_of_token(g, t, s)) return;
+  const int pos = t - cu_at(g, s);
+  const bool summary = pos - fdiv(pos, g.fl) * g.l >= g.l - g.c;
+  float acc[8] = {};
+  for (int j = 0; j < a.njobs; ++j) {
+    if (!job_reaches(g, a.job[j], kvh)) continue;
+    if (a.job[j].seg[0].kview == VIEW_SUM && !summary) continue;
+    for (int p = j * a.nsplit; p < (j + 1) * a.nsplit; ++p) {
+      const float* src = a.parts + (p * rows + row) * 2 * g.d;
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (lane + 32 * x < 2 * g.d) acc[x] += src[lane + 32 * x];
+    }
+  }
+  T* dk = static_cast<T*>(a.dk) + ((size_t)t * a.dk_rows.tok + kvh * a.dk_rows.head) * g.d;
+  T* dv = static_cast<T*>(a.dv) + ((size_t)t * a.dv_rows.tok + kvh * a.dv_rows.head) * g.d;
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const int c = lane + 32 * x;
+    if (c < g.d) dk[c] = round_to<T>(acc[x]);
+    else if (c < 2 * g.d) dv[c - g.d] = round_to<T>(acc[x]);
+  }
+}
+
+// One warp per new token and key/value head: 16-byte chunks of the key row and
+// of the value row go to the slot of the token's position. Tokens at negative
+// positions, positions past the page table and pages outside the cache are
+// dropped (the last two are reported).
+__global__ void __launch_bounds__(32 * kJoinRows)
+    cache_append_kernel(const __grid_constant__ Geo g, const Rows kin, const Rows vin,
+                        int row_chunks, const uint4* k, const uint4* v, uint4* kc, uint4* vc) {
+  const long long row = (long long)blockIdx.x * kJoinRows + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= (long long)g.total * g.Hkv) return;
+  const int t = (int)(row / g.Hkv), h = (int)(row - (long long)t * g.Hkv);
+  int s;
+  if (!seq_of_token(g, t, s)) return;
+  const int pos = __ldg(g.kv_lens + s) - (cu_at(g, s + 1) - t);
+  if (pos < 0) return;
+  const int pg = fdiv(pos, g.fpage);
+  const int page = pg < g.max_pages ? __ldg(g.table + (size_t)s * g.max_pages + pg) : -1;
+  if ((unsigned)page >= (unsigned)g.num_pages) {
+    set_status(g.status, ST_ERR_INVALID);
+    return;
+  }
+  const size_t dst = (size_t)page * g.k.page + (size_t)(pos - pg * g.page_size) * g.k.tok +
+                     (size_t)h * g.k.head;
+  const size_t ks = (size_t)t * kin.tok + h, vs = (size_t)t * vin.tok + h;
+  for (int c = lane; c < 2 * row_chunks; c += 32) {
+    if (c < row_chunks)
+      kc[dst * row_chunks + c] = __ldg(k + ks * row_chunks + c);
+    else
+      vc[dst * row_chunks + c - row_chunks] = __ldg(v + vs * row_chunks + c - row_chunks);
+  }
+}
+
+template <class K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <int D, class T>
+cudaError_t fwd_t(const FwdLaunch& a) {
+  const size_t smem = sizeof(float) * (2 * BM * (D + 4) + BM * SP + 2 * BM);
+  cudaError_t e = allow_smem(ragged_fwd_simt<D, T>, smem);
+  if (e != cudaSuccess) return e;
+  const long long slots = slot_count(a.g, most_heads(a.g, a.job.hc), BM);
+  ragged_fwd_simt<D, T><<<dim3((unsigned)slots, a.g.Hkv, a.nsplit), NT, smem, a.stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D, class T>
+cudaError_t dq_t(const BwdLaunch& a, const Job& job, int mode) {
+  const size_t smem = sizeof(float) * (4 * BM * (D + 4) + BM * SP);
+  cudaError_t e = allow_smem(ragged_dq_simt<D, T>, smem);
+  if (e != cudaSuccess) return e;
+  const long long slots = slot_count(a.g, most_heads(a.g, job.hc), BM);
+  ragged_dq_simt<D, T><<<dim3((unsigned)slots, a.g.Hkv), NT, smem, a.stream>>>(a, job, mode);
+  return cudaGetLastError();
+}
+
+template <int D, class T>
+cudaError_t dkv_t(const BwdLaunch& a) {
+  const size_t smem = sizeof(float) * (4 * BM * (D + 4) + 2 * BM * SP);
+  cudaError_t e = allow_smem(ragged_dkv_simt<D, T>, smem);
+  if (e != cudaSuccess) return e;
+  const long long slots = slot_count(a.g, 1, BM);
+  ragged_dkv_simt<D, T>
+      <<<dim3((unsigned)slots, a.g.Hkv, a.njobs * a.nsplit), NT, smem, a.stream>>>(a);
+  return cudaGetLastError();
+}
+
+// f(std::integral_constant-like D, T tag) for the element type and head size
+template <class F>
+cudaError_t pick(int dtype, int d, F f) {
+#define ST_PICK(T)                                      \
+  switch (d) {                                          \
+    case 32: return f.template run<32, T>();            \
+    case 64: return f.template run<64, T>();            \
+    case 128: return f.template run<128, T>();          \
+  }
+  if (dtype == ST_F32) {
+    ST_PICK(float)
+  } else if (dtype == ST_BF16) {
+    ST_PICK(__nv_bfloat16)
+  } else {
+    ST_PICK(__half)
+  }
+#undef ST_PICK
+  return cudaErrorInvalidValue;
+}
+
+struct RunFwd {
+  const FwdLaunch& a;
+  template <int D, class T>
+  cudaError_t run() { return fwd_t<D, T>(a); }
+};
+struct RunDq {
+  const BwdLaunch& a;
+  const Job& job;
+  int mode;
+  template <int D, class T>
+  cudaError_t run() { return dq_t<D, T>(a, job, mode); }
+};
+struct RunDkv {
+  const BwdLaunch& a;
+  template <int D, class T>
+  cudaError_t run() { return dkv_t<D, T>(a); }
+};
+
+unsigned join_blocks(long long rows) { return (unsigned)((rows + kJoinRows - 1) / kJoinRows); }
+
+}  // namespace
+
+cudaError_t simt_ragged_fwd(const FwdLaunch& a, int dtype) { return pick(dtype, a.g.d, RunFwd{a}); }
+cudaError_t simt_ragged_dq(const BwdLaunch& a, const Job& job, int mode, int dtype) {
+  return pick(dtype, a.g.d, RunDq{a, job, mode});
+}
+cudaError_t simt_ragged_dkv(const BwdLaunch& a, int dtype) {
+  return pick(dtype, a.g.d, RunDkv{a});
+}
+
+cudaError_t join_parts(const Geo& g, int dtype, const Parts& parts, int nparts, void* o,
+                       float* lse, cudaStream_t s) {
+  const unsigned nb = join_blocks((long long)g.total * g.H);
+  const int nt = 32 * kJoinRows;
+  if (dtype == ST_F32)
+    join_parts_kernel<float><<<nb, nt, 0, s>>>(g, parts, nparts, static_cast<float*>(o), lse);
+  else if (dtype == ST_BF16)
+    join_parts_kernel<__nv_bfloat16>
+        <<<nb, nt, 0, s>>>(g, parts, nparts, static_cast<__nv_bfloat16*>(o), lse);
+  else
+    join_parts_kernel<__half><<<nb, nt, 0, s>>>(g, parts, nparts, static_cast<__half*>(o), lse);
+  return cudaGetLastError();
+}
+
+cudaError_t row_delta(const Geo& g, int dtype, const void* o, const void* dout, float* delta,
+                      cudaStream_t s) {
+  const long long rows = (long long)g.total * g.H;
+  const unsigned nb = join_blocks(rows);
+  const int nt = 32 * kJoinRows;
+  if (dtype == ST_F32)
+    row_delta_kernel<float><<<nb, nt, 0, s>>>(rows, g.d, static_cast<const float*>(o),
+                                              static_cast<const float*>(dout), delta);
+  else if (dtype == ST_BF16)
+    row_delta_kernel<__nv_bfloat16>
+        <<<nb, nt, 0, s>>>(rows, g.d, static_cast<const __nv_bfloat16*>(o),
+                           static_cast<const __nv_bfloat16*>(dout), delta);
+  else
+    row_delta_kernel<__half><<<nb, nt, 0, s>>>(rows, g.d, static_cast<const __half*>(o),
+                                               static_cast<const __half*>(dout), delta);
+  return cudaGetLastError();
+}
+
+cudaError_t join_dkv(const BwdLaunch& a, int dtype) {
+  const unsigned nb = join_blocks((long long)a.g.total * a.g.Hkv);
+  const int nt = 32 * kJoinRows;
+  if (dtype == ST_F32)
+    join_dkv_kernel<float><<<nb, nt, 0, a.stream>>>(a);
+  else if (dtype == ST_BF16)
+    join_dkv_kernel<__nv_bfloat16><<<nb, nt, 0, a.stream>>>(a);
+  else
+    join_dkv_kernel<__half><<<nb, nt, 0, a.stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t cache_append(const Geo& g, const Rows& kin, const Rows& vin, int elem_bytes,
+                         const void* k, const void* v, void* kc, void* vc, cudaStream_t s) {
+  const unsigned nb = join_blocks((long long)g.total * g.Hkv);
+  cache_append_kernel<<<nb, 32 * kJoinRows, 0, s>>>(
+      g, kin, vin, g.d * elem_bytes / 16, static_cast<const uint4*>(k),
+      static_cast<const uint4*>(v), static_cast<uint4*>(kc), static_cast<uint4*>(vc));
+  return cudaGetLastError();
+}
+
+}  // namespace rag
+}  // namespace st

@@ -236,6 +236,119 @@ st_status st_sparse_attn_bwd_noalloc(const st_layout* layout, st_dtype dtype, in
                                      const float* lse, const void* dout, void* dq, void* dk,
                                      void* dv, void* stream);
 
+/* ---- ragged sequences, grouped heads, paged caches --------------------------
+ *
+ * The same attention, O_i = softmax(q_i K_{S_i}^T * scale) V_{S_i}, for sequences
+ * of any length: prompts packed one behind the other (forward and backward),
+ * and the newest tokens of sequences whose keys and values lie in the pages of
+ * a cache. Positions count from the start of each sequence; no sequence sees
+ * another. No layout is built: the kernels work the sets out from the lengths,
+ * which they read on the device, so captured graphs replay with other lengths.
+ *
+ * Conventions, beside those at the top of this file:
+ *  - Pattern: an st_pattern_desc. kind, head_mode, l and c as for a layout, with
+ *    1 <= c <= l (fixed); l need not divide anything. T is the longest sequence
+ *    (keys) the caller expects, T >= 1: it only sets how work is split over the
+ *    GPU, a longer sequence is still attended in full.
+ *  - Grouped heads: query head h reads key/value head h / (H / Hkv); Hkv divides
+ *    H. Split heads go by the parity of the query head.
+ *  - Types: bf16 or fp16 with d = 64 or 128 (tensor cores, fp32 softmax and
+ *    sums), float32 with d = 32, 64 or 128 (fp32 throughout).
+ *  - Tensors hold token rows: [total, H, d] or [total, Hkv, d] with the heads of
+ *    a token d apart and tokens `stride` elements apart (0 = contiguous), a
+ *    multiple of d: a slice of a fused QKV tensor needs no copy. o and dout are
+ *    contiguous, LSE is float32 [total, H]. Pointers are 16-byte aligned.
+ *  - cu (device, int32 [n_seqs + 1]): sequence s is the token rows cu[s] ..
+ *    cu[s + 1] - 1. Values must not decrease; they are clamped to 0 .. total.
+ *    Rows of no sequence (behind the last one) are neither read for any
+ *    result nor written.
+ *  - Keys and values of a sequence's own rows must be finite; whatever lies in
+ *    rows of no sequence, unused pages and unused slots of a page (infinities,
+ *    NaN) has no effect.
+ *  - workspace: device memory of at least the queried size, 256-byte aligned,
+ *    overwritten; may be NULL when the size is 0. Calls (or replays of captured
+ *    graphs) that may run at the same time need a workspace each.
+ *  - The first of these calls on a device creates the word that kernels report
+ *    to (the device status; a few bytes): make it, a workspace query for
+ *    instance, before any stream capture. Afterwards no call allocates, and none
+ *    synchronises.
+ *  - The results are bitwise reproducible from run to run.
+ *  - Everything runs on the current device, on which the tensors must lie.
+ */
+
+/* Packed token rows. */
+typedef struct {
+  int32_t n_seqs;      /* >= 1 */
+  int32_t total;       /* token rows of q, k, v (paged: of q), >= 0 */
+  int32_t H, Hkv, d;
+  int64_t q_stride, k_stride, v_stride;    /* elements from token to token, 0 = contiguous */
+  int64_t dq_stride, dk_stride, dv_stride; /* of the gradients (backward only) */
+} st_packed_desc;
+
+/* A paged cache: K and V are arrays of num_pages pages of page_size slots of
+ * Hkv heads of d elements, at the given strides (elements, multiples of d; the
+ * same for K and V): [num_pages, page_size, Hkv, d] has page_stride =
+ * page_size * Hkv * d, slot_stride = Hkv * d, head_stride = d. Page table:
+ * device, int32 [n_seqs, max_pages]; key j of sequence s is slot j mod
+ * page_size of page table[s][j / page_size]. A page number in use that is not
+ * in 0 .. num_pages - 1 sets the device status to ST_ERR_INVALID (reads take
+ * page 0 instead, writes are dropped). kv_lens: device, int32 [n_seqs], keys of
+ * each sequence, the new tokens included: new token t of n is at position
+ * kv_len - n + t. Rows at negative positions attend nothing (O = 0, LSE = -inf),
+ * so a padding sequence may have kv_len 0. A kv_len outside 0 .. max_pages *
+ * page_size is clamped and sets the device status to ST_ERR_INVALID. */
+typedef struct {
+  int32_t num_pages, page_size, max_pages;
+  int64_t page_stride, slot_stride, head_stride;
+} st_cache_desc;
+
+/* Attention over packed sequences, forward: o [total, H, d] and lse [total, H].
+ * Rows with an empty set get O = 0 and LSE = -inf. */
+st_status st_packed_attn_fwd_workspace(const st_pattern_desc* pattern, st_dtype dtype,
+                                       const st_packed_desc* desc, size_t* bytes);
+st_status st_packed_attn_fwd(const st_pattern_desc* pattern, st_dtype dtype,
+                             const st_packed_desc* desc, float scale, const void* q,
+                             const void* k, const void* v, const int32_t* cu, void* o, float* lse,
+                             void* workspace, size_t ws_bytes, void* stream);
+
+/* Its backward: dq [total, H, d], dk, dv [total, Hkv, d] (at their strides, in
+ * the dtype of the inputs, summed in fp32 over the heads of a group) from the
+ * forward's o and lse and the upstream gradient dout. P is recomputed from lse.
+ * dq, dk, dv rows of queries with an empty set, and of keys in no query's set,
+ * are zero. */
+st_status st_packed_attn_bwd_workspace(const st_pattern_desc* pattern, st_dtype dtype,
+                                       const st_packed_desc* desc, size_t* bytes);
+st_status st_packed_attn_bwd(const st_pattern_desc* pattern, st_dtype dtype,
+                             const st_packed_desc* desc, float scale, const void* q,
+                             const void* k, const void* v, const void* o, const float* lse,
+                             const void* dout, const int32_t* cu, void* dq, void* dk, void* dv,
+                             void* workspace, size_t ws_bytes, void* stream);
+
+/* Attention of the newest tokens of every sequence (one: a decoding step; more:
+ * a chunk of a prompt) over a paged cache that holds their keys and values
+ * already (st_cache_append). q, o [total, H, d]; cu gives each sequence's new
+ * rows; max_q >= 1 is the most new tokens of a sequence the caller expects (like
+ * pattern->T it only chooses the kernel and the split). desc->k_stride,
+ * v_stride and the gradients' strides are not used. */
+st_status st_paged_attn_workspace(const st_pattern_desc* pattern, st_dtype dtype,
+                                  const st_packed_desc* desc, const st_cache_desc* cache,
+                                  int32_t max_q, size_t* bytes);
+st_status st_paged_attn(const st_pattern_desc* pattern, st_dtype dtype, const st_packed_desc* desc,
+                        const st_cache_desc* cache, int32_t max_q, float scale, const void* q,
+                        const void* k_cache, const void* v_cache, const int32_t* page_table,
+                        const int32_t* cu, const int32_t* kv_lens, void* o, float* lse,
+                        void* workspace, size_t ws_bytes, void* stream);
+
+/* Writes new keys and values k, v [total, Hkv, d] (at k_stride, v_stride; H and
+ * q_stride are not used) into their slots of the cache: new token t of n of
+ * sequence s goes to position kv_lens[s] - n + t. Tokens at negative positions
+ * are dropped. No two sequences may have a page in common at the positions
+ * written. Any d that is a multiple of 8 (float32: of 4). */
+st_status st_cache_append(st_dtype dtype, const st_packed_desc* desc, const st_cache_desc* cache,
+                          const void* k, const void* v, void* k_cache, void* v_cache,
+                          const int32_t* page_table, const int32_t* cu, const int32_t* kv_lens,
+                          void* stream);
+
 /* Synchronises `stream`, then returns and clears the device-side status word
  * of the current device: ST_ERR_DEVICE_TIMEOUT after a kernel's bounded wait
  * ran out, ST_ERR_UNSUPPORTED if the backward kernel found its shared memory
