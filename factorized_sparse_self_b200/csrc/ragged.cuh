@@ -301,6 +301,40 @@ __device__ __forceinline__ int kv_row(const Geo& g, const Rows& r, const Seq& q,
 __device__ __forceinline__ int q_row(const Geo& g, int t, int h) {
   return t * g.q.tok + h * g.q.head;
 }
+// Query row x of a unit's order: token row (absolute), head, position; false
+// past the unit's rows.
+struct QRow {
+  int t, h, pos;
+};
+__device__ __forceinline__ bool query_at(const Geo& g, const Seq& q, int view, const Heads3& hs,
+                                         int x, QRow& r) {
+  if (x >= q.nq * hs.n) return false;
+  const int e = x / hs.n;
+  const int row = query_row(g, q, view, e);
+  r.t = q.qb + row;
+  r.pos = row + q.off;
+  r.h = hs.first + hs.step * (x - e * hs.n);
+  return true;
+}
+
+// Key tiles [j0, j1) of bn keys that the unit's rows x0 .. x0+rows-1 meet in a
+// segment.
+__device__ __forceinline__ void tile_range(const Geo& g, const Seq& q, const Job& job, int seg,
+                                           const Heads3& hs, int x0, int rows, int bn, int& j0,
+                                           int& j1) {
+  j0 = j1 = 0;
+  int v0, v1;
+  valid_rows(q, job.qview, v0, v1);
+  const int e0 = imax(x0 / hs.n, v0), e1 = imin((imin(x0 + rows, q.nq * hs.n) - 1) / hs.n, v1 - 1);
+  if (e0 > e1) return;
+  int lo, hi, a, b;
+  live_keys(g, q, job.seg[seg].rule, query_row(g, q, job.qview, e0) + q.off, lo, hi);
+  live_keys(g, q, job.seg[seg].rule, query_row(g, q, job.qview, e1) + q.off, a, b);
+  if (b > lo) {
+    j0 = lo / bn;
+    j1 = (b + bn - 1) / bn;
+  }
+}
 #endif
 
 }  // namespace rag

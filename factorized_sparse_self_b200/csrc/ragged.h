@@ -59,6 +59,29 @@ struct BwdLaunch {
   cudaStream_t stream;
 };
 
+#ifdef __CUDACC__
+// Key heads that a job reaches: whether any query head of the group is in its
+// class.
+__device__ __forceinline__ bool job_reaches(const Geo& g, const Job& job, int kvh) {
+  return heads_of_group(g, job.hc, kvh).n > 0;
+}
+// Whether kvh's dK, dV come from one unit alone and are written by it: one key
+// range, one job, and an order that lists every key.
+__device__ __forceinline__ bool dkv_direct(const BwdLaunch& a, int kvh) {
+  if (a.nsplit > 1) return false;
+  int n = 0, view = VIEW_NAT;
+  for (int j = 0; j < a.njobs; ++j)
+    if (job_reaches(a.g, a.job[j], kvh)) {
+      ++n;
+      view = a.job[j].seg[0].kview;
+    }
+  return n == 1 && view != VIEW_SUM;
+}
+#endif
+
+// Tensor-core forward: bf16 / fp16, d = 64 or 128.
+cudaError_t tc_ragged_fwd(const FwdLaunch& a, int dtype);
+
 // CUDA-core kernels in fp32 arithmetic.
 cudaError_t simt_ragged_fwd(const FwdLaunch& a, int dtype);
 cudaError_t simt_ragged_dq(const BwdLaunch& a, const Job& job, int mode, int dtype);

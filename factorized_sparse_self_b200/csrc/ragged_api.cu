@@ -224,7 +224,7 @@ st_status run_fwd(const st_pattern_desc& p, st_dtype dtype, Geo& g, float scale,
     a.job = jobs[j];
     a.part0 = two_orders(p) && j == 1 && !f.merge ? f.nsplit : 0;
     a.mode = f.merge ? (j == 0 ? OUT_PARTIAL : OUT_MERGE) : f.nparts ? OUT_PARTIAL : OUT_FINAL;
-    e = simt_ragged_fwd(a, dtype);
+    e = dtype == ST_F32 ? simt_ragged_fwd(a, dtype) : tc_ragged_fwd(a, dtype);
   }
   if (e == cudaSuccess && f.nparts && !f.merge)
     e = join_parts(g, dtype, a.parts, f.nparts, o, lse, stream);

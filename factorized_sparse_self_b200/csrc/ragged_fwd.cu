@@ -1,0 +1,507 @@
+// Forward of attention over ragged and paged sequences on the tensor cores
+// (bf16, fp16; d = 64, 128).
+//
+// Persistent CTAs, one per SM (384 threads). A unit is 256 query rows of one
+// (sequence, key/value head): two halves of 128 rows that share every K and V
+// tile, so a tile brought from L2 serves 256 rows and the two halves' softmax and
+// products alternate. Warp roles:
+//   warp 10      scheduler: decodes the CTA's units into a small ring;
+//   warp 8       producer: Q rows, then K and V tiles of 128 rows in turn into
+//                one ring. Rows are gathered (32 lanes, four rows each) through the
+//                order's index map and the page table; 128 consecutive rows of a
+//                packed sequence come as one box. Rows behind the last key repeat
+//                it: masked entries have weight 0 and must not meet another
+//                sequence's infinities;
+//   warp 9       MMA issuer: S_h = Q_h K^T (128 x 128 fp32 in TMEM), O_h += P_h V
+//                with P_h read from TMEM; the order S0 S1 | P0V S0' | P1V S1' | ..
+//                keeps one half's products under the other half's softmax;
+//   warps 0..7   softmax of half 0 and 1: thread = query row = TMEM lane, running
+//                maximum (O is rescaled in TMEM only when it grows by more than 2^8)
+//                and sum in fp32, P as 16-bit pairs over S.
+// TMEM: S0 S1 (P0 P1 in their first 64 columns) O0 O1, 128 columns each.
+#include "ragged_tc.cuh"
+
+namespace st {
+namespace rag {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRows = 256;  // query rows of a unit
+constexpr int kSched = 3;   // units decoded ahead
+constexpr uint32_t kRegsSoftmax = 216, kRegsIssue = 72;  // 168 at launch: 2 * 216 + 72 = 3 * 168
+constexpr float kRescale = 8.f;  // log2
+constexpr float kLn2 = 0.69314718055994531f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kStages = D == 64 ? 8 : 5;
+};
+
+template <int D>
+struct alignas(1024) Smem {
+  uint8_t q[2][Cfg<D>::kTileBytes];
+  uint8_t kv[Cfg<D>::kStages][Cfg<D>::kTileBytes];
+  uint64_t q_full, q_empty;
+  uint64_t kv_full[Cfg<D>::kStages], kv_empty[Cfg<D>::kStages];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t sched_full[kSched], sched_empty[kSched];
+  uint64_t fin;
+  Unit unit[kSched];
+  uint32_t tmem;
+  int abort;
+};
+
+struct Maps {
+  CUtensorMap q, k, v, kbox, vbox;
+};
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    ragged_fwd_tc(const __grid_constant__ FwdLaunch a, const __grid_constant__ Maps maps, int slots,
+                  int n_units, int boxes) {
+  extern __shared__ uint8_t raw[];
+  Smem<D>& S = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  constexpr int NS = Cfg<D>::kStages, TB = Cfg<D>::kTileBytes;
+  constexpr uint32_t kColO = 256;
+  const Geo& g = a.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t limit = a.wait_ns;
+  volatile int* abort = &S.abort;
+  if (threadIdx.x == 0) {
+    S.abort = 0;
+    mbar_init(&S.q_full, 1);
+    mbar_init(&S.q_empty, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&S.kv_full[i], 1);
+      mbar_init(&S.kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_full[i], 128);
+      mbar_init(&S.o_full[i], 1);
+    }
+    for (int i = 0; i < kSched; ++i) {
+      mbar_init(&S.sched_full[i], 1);
+      mbar_init(&S.sched_empty[i], 10);  // producer, MMA, eight softmax warps
+    }
+    mbar_init(&S.fin, 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&S.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem;
+  auto fail = [&]() {
+    S.abort = 1;
+    set_status(g.status, ST_ERR_DEVICE_TIMEOUT);
+  };
+
+  if (warp >= 8) {
+    regs_decrease<kRegsIssue>();
+    if (warp == 10) {
+      // ---------------- scheduler ----------------
+      int k = 0;
+      bool ok = true;
+      auto slot_free = [&]() {
+        return k < kSched || __all_sync(0xffffffffu, mbar_wait(&S.sched_empty[k % kSched],
+                                                               (k / kSched + 1) & 1, limit, abort));
+      };
+      for (int n = blockIdx.x; n < n_units && ok; n += gridDim.x) {
+        ok = slot_free();
+        if (!ok) break;
+        if (!decode_unit(g, a.job, a.nsplit, slots, n, kRows, &S.unit[k % kSched])) continue;
+        __threadfence_block();
+        if (lane == 0) mbar_arrive(&S.sched_full[k % kSched]);
+        ++k;
+      }
+      if (ok) ok = slot_free();
+      if (ok && lane == 0) {
+        S.unit[k % kSched].live = 0;
+        __threadfence_block();
+        mbar_arrive(&S.sched_full[k % kSched]);
+      }
+      if (!ok && lane == 0) fail();
+    } else if (warp == 8) {
+      // ---------------- producer ----------------
+      if (lane == 0) {
+        tma_prefetch_desc(&maps.q);
+        tma_prefetch_desc(&maps.k);
+        tma_prefetch_desc(&maps.v);
+      }
+      int used = 0, kt = 0;  // units with tiles, ring slots filled
+      bool ok = true;
+      for (int n = 0;; ++n) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.sched_full[n % kSched], (n / kSched) & 1, limit, abort));
+        if (!ok || !S.unit[n % kSched].live) break;
+        const Unit& u = S.unit[n % kSched];
+        if (u.t1 <= u.t0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
+          continue;
+        }
+        // Q
+        ok = __all_sync(0xffffffffu, used == 0 || mbar_wait(&S.q_empty, (used - 1) & 1, limit, abort));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&S.q_full, 2 * TB);
+        ++used;
+        __syncwarp();
+        const int rows = u.q.nq * u.hs.n;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          int r[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            QRow qr;
+            query_at(g, u.q, a.job.qview, u.hs, imin(u.x0 + h * 128 + lane * 4 + i, rows - 1), qr);
+            r[i] = q_row(g, qr.t, qr.h);
+          }
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_gather4(smem_u32(S.q[h]) + c * 16384 + lane * 512, &maps.q, &S.q_full, c * 64, r[0], r[1],
+                        r[2], r[3]);
+        }
+        // K and V
+        for (int t = u.t0; t < u.t1 && ok; ++t) {
+          int seg, j;
+          unit_tile(u, t, seg, j);
+          const int view = a.job.seg[seg].kview, nk = n_keys(u.q, view);
+          const bool box = boxes && view == VIEW_NAT && j * 128 + 128 <= nk;
+          int pos[4];
+          if (!box) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              pos[i] = key_pos(g, u.q, view, imin(j * 128 + lane * 4 + i, nk - 1));
+          }
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++kt) {
+            const int s = kt % NS;
+            ok = __all_sync(0xffffffffu,
+                            kt < NS || mbar_wait(&S.kv_empty[s], (kt / NS + 1) & 1, limit, abort));
+            if (!ok) break;
+            const uint32_t dst = smem_u32(S.kv[s]);
+            if (lane == 0) mbar_arrive_expect_tx(&S.kv_full[s], TB);
+            __syncwarp();
+            if (box) {
+              if (lane < D / 64)
+                tma_box(dst + lane * 16384, kv ? &maps.vbox : &maps.kbox, &S.kv_full[s], lane * 64, u.kvh,
+                        u.q.qb + j * 128);
+            } else {
+              const Rows& rw = kv ? g.v : g.k;
+              int r[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) r[i] = kv_row(g, rw, u.q, pos[i], u.kvh);
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_gather4(dst + c * 16384 + lane * 512, kv ? &maps.v : &maps.k, &S.kv_full[s], c * 64,
+                            r[0], r[1], r[2], r[3]);
+            }
+          }
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
+      }
+      if (!ok) {
+        if (lane == 0) fail();
+        // copies in flight land before the CTA may exit
+        if (used > 0) mbar_wait_drain(&S.q_full, (used - 1) & 1, limit);
+        for (int i = imax(0, kt - NS); i < kt; ++i)
+          mbar_wait_drain(&S.kv_full[i % NS], (i / NS) & 1, limit);
+      }
+    } else if (warp == 9) {
+      // ---------------- MMA issuer ----------------
+      if (lane == 0) {
+        const uint32_t idS = idesc_16(128, 128, false, false, F16);
+        const uint32_t idPV = idesc_16(128, D, false, true, F16);
+        int kt = 0, used = 0;         // ring slots consumed, units with tiles
+        int np[2] = {0, 0};           // tiles of each half so far
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          if (ok && !mbar_wait(bar, parity, limit, abort)) ok = false;
+          return ok;
+        };
+        auto issue_s = [&](int h, uint32_t ks) {
+          const uint64_t qd = sdesc(smem_u32(S.q[h]), 16, 1024), kd = sdesc(ks, 16, 1024);
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x)
+            mma_ss(tmem + h * 128, sdesc_at(qd, (x & 3) * 32 + (x >> 2) * 16384),
+                   sdesc_at(kd, (x & 3) * 32 + (x >> 2) * 16384), idS, x > 0);
+          mma_commit(&S.s_full[h]);
+        };
+        for (int n = 0;; ++n) {
+          if (!wait(&S.sched_full[n % kSched], (n / kSched) & 1)) break;
+          const Unit& u = S.unit[n % kSched];
+          if (!u.live) break;
+          const int t1 = u.t1;
+          if (t1 <= u.t0) {
+            mbar_arrive(&S.sched_empty[n % kSched]);
+            continue;
+          }
+          if (!wait(&S.q_full, used & 1)) break;
+          ++used;
+          bool fresh[2] = {true, true};
+          int seg, j;
+          unit_tile(u, u.t0, seg, j);
+          bool act[2] = {half_meets(u, 0, seg, j), half_meets(u, 1, seg, j)};
+          if (!wait(&S.kv_full[kt % NS], (kt / NS) & 1)) break;
+          tc_fence_after();
+          for (int h = 0; h < 2; ++h)
+            if (act[h]) issue_s(h, smem_u32(S.kv[kt % NS]));
+          mma_commit(&S.kv_empty[kt % NS]);
+          if (u.t0 + 1 == t1) mma_commit(&S.q_empty);
+          for (int t = u.t0; t < t1 && ok; ++t, kt += 2) {
+            const int sv = (kt + 1) % NS, sk = (kt + 2) % NS;
+            const bool more = t + 1 < t1;
+            bool nact[2] = {false, false};
+            if (more) {
+              unit_tile(u, t + 1, seg, j);
+              nact[0] = half_meets(u, 0, seg, j);
+              nact[1] = half_meets(u, 1, seg, j);
+            }
+            const uint64_t vd = sdesc(smem_u32(S.kv[sv]), 16384, 1024);
+            bool have_v = false, have_k = false;
+            for (int h = 0; h < 2; ++h) {
+              if (act[h]) {
+                if (!wait(&S.p_full[h], np[h] & 1)) break;
+                ++np[h];
+                if (!have_v && !wait(&S.kv_full[sv], ((kt + 1) / NS) & 1)) break;
+                have_v = true;
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                  mma_ts(tmem + kColO + h * D, tmem + h * 128 + x * 8, sdesc_at(vd, x * 2048), idPV,
+                         !fresh[h] || x > 0);
+                fresh[h] = false;
+                mma_commit(&S.o_full[h]);
+              }
+              if (nact[h]) {
+                if (!have_k && !wait(&S.kv_full[sk], ((kt + 2) / NS) & 1)) break;
+                have_k = true;
+                tc_fence_after();
+                issue_s(h, smem_u32(S.kv[sk]));
+              }
+            }
+            if (!ok) break;
+            // tiles that neither half met are let go once they have landed
+            if (!have_v && !wait(&S.kv_full[sv], ((kt + 1) / NS) & 1)) break;
+            mma_commit(&S.kv_empty[sv]);
+            if (more) {
+              if (!have_k && !wait(&S.kv_full[sk], ((kt + 2) / NS) & 1)) break;
+              mma_commit(&S.kv_empty[sk]);
+              if (t + 2 == t1) mma_commit(&S.q_empty);
+            }
+            act[0] = nact[0];
+            act[1] = nact[1];
+          }
+          if (!ok) break;
+          mbar_arrive(&S.sched_empty[n % kSched]);
+        }
+        if (!ok) fail();
+        mma_commit(&S.fin);
+        if (!mbar_wait_drain(&S.fin, 0, limit)) fail();
+      }
+      __syncwarp();
+    }
+  } else {
+    regs_increase<kRegsSoftmax>();
+    // ---------------- softmax ----------------
+    const int h = warp >> 2;
+    const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + tl + h * 128, tO = tmem + tl + kColO + h * D;
+    const int row = (warp & 3) * 32 + lane;
+    bool ok = true;
+    int ns = 0;  // tiles of this half so far
+    for (int n = 0;; ++n) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&S.sched_full[n % kSched], (n / kSched) & 1, limit, abort));
+      if (!ok) break;
+      const Unit& su = S.unit[n % kSched];
+      if (!su.live) break;
+      QRow qr;
+      const bool have = query_at(g, su.q, a.job.qview, su.hs, su.x0 + h * 128 + row, qr);
+      int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0;
+      if (have && qr.pos >= 0) {
+        live_keys(g, su.q, a.job.seg[0].rule, qr.pos, lo0, hi0);
+        if (a.job.nseg > 1) live_keys(g, su.q, a.job.seg[1].rule, qr.pos, lo1, hi1);
+      }
+      const int t1 = su.t1, part = su.part;
+      float m = -INFINITY, l = 0.f;
+      bool any = false;
+      for (int t = su.t0; t < t1; ++t) {
+        int seg, j;
+        unit_tile(su, t, seg, j);
+        if (!half_meets(su, h, seg, j)) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full[h], ns & 1, limit, abort));
+        if (!ok) break;
+        tc_fence_after();
+        float s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, reinterpret_cast<uint32_t*>(s) + c * 32);
+        tmem_wait_ld();
+        const int kl = (seg ? lo1 : lo0) - j * 128, kh = (seg ? hi1 : hi0) - j * 128;
+        if (!__all_sync(0xffffffffu, kl <= 0 && kh >= 128)) mask_cols<4>(s, 0, kl, kh);
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int x = 0; x < 128; x += 8) {
+          m4[0] = fmax3(m4[0], s[x + 0], s[x + 1]);
+          m4[1] = fmax3(m4[1], s[x + 2], s[x + 3]);
+          m4[2] = fmax3(m4[2], s[x + 4], s[x + 5]);
+          m4[3] = fmax3(m4[3], s[x + 6], s[x + 7]);
+        }
+        const float mt = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * a.scale_log2;
+        float alpha = 1.f;
+        bool rescale = false;
+        if (mt > m + kRescale) {
+          rescale = m != -INFINITY;
+          alpha = fast_exp2(m - mt);
+          m = mt;
+        }
+        const float nmu = m == -INFINITY ? 0.f : -m;
+        float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[64];
+#pragma unroll
+        for (int x = 0; x < 128; x += 2) {
+          float a0, a1;
+          ffma2(a0, a1, s[x], s[x + 1], a.scale_log2, a.scale_log2, nmu, nmu);
+          const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+          const int y = (x >> 1) & 3;
+          fadd2(sa[y], sb[y], sa[y], sb[y], p0, p1);
+          pk[x >> 1] = pack2<F16>(p0, p1);
+        }
+        l = l * alpha + (((sa[0] + sb[0]) + (sa[1] + sb[1])) + ((sa[2] + sb[2]) + (sa[3] + sb[3])));
+        if (__any_sync(0xffffffffu, rescale)) {
+          // the previous tile's P V has ended before O is touched
+          ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[h], (ns - 1) & 1, limit, abort));
+          if (!ok) break;
+          tc_fence_after();
+          const float f = rescale ? alpha : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 8) {
+            uint32_t o[8];
+            tmem_ld8(tO + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+            tmem_st8(tO + c, o);
+          }
+        }
+        tmem_st32(tS, pk);
+        tmem_st32(tS + 32, pk + 32);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&S.p_full[h]);
+        any = true;
+        ++ns;
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
+      // ---- the unit's rows ----
+      if (any) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[h], (ns - 1) & 1, limit, abort));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      float L = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+      float wc = l > 0.f ? 1.f / l : 0.f, wp = 0.f;
+      const size_t rr = have ? (size_t)qr.t * g.H + qr.h : 0;
+      if (a.mode == OUT_MERGE && have) {
+        const float lp = a.parts.lse[rr], mx = fmaxf(lp, L);
+        if (mx > -INFINITY) {
+          const float out = mx + __logf(__expf(lp - mx) + __expf(L - mx));
+          wp = __expf(lp - out);
+          wc *= __expf(L - out);
+          L = out;
+        }
+      }
+      if (have) {
+        if (a.mode == OUT_PARTIAL)
+          a.parts.lse[(size_t)(a.part0 + part) * g.total * g.H + rr] = L;
+        else
+          a.lse[rr] = L;
+      }
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (any) {
+          tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
+          tmem_wait_ld();
+        }
+        if (!have) continue;
+#pragma unroll
+        for (int x = 0; x < 32; ++x) o[x] = any ? o[x] * wc : 0.f;
+        if (a.mode == OUT_PARTIAL) {
+          if (wc > 0.f) {  // a part without weight is not read
+            float4* dst = reinterpret_cast<float4*>(
+                a.parts.o + ((size_t)(a.part0 + part) * g.total * g.H + rr) * D + c);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          }
+          continue;
+        }
+        if (a.mode == OUT_MERGE && wp > 0.f) {
+          const float4* src = reinterpret_cast<const float4*>(a.parts.o + rr * D + c);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const float4 f = src[x];
+            o[4 * x] = fmaf(wp, f.x, o[4 * x]);
+            o[4 * x + 1] = fmaf(wp, f.y, o[4 * x + 1]);
+            o[4 * x + 2] = fmaf(wp, f.z, o[4 * x + 2]);
+            o[4 * x + 3] = fmaf(wp, f.w, o[4 * x + 3]);
+          }
+        }
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + rr * D + c);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          dst[x] = make_uint4(pack2<F16>(o[8 * x], o[8 * x + 1]), pack2<F16>(o[8 * x + 2], o[8 * x + 3]),
+                              pack2<F16>(o[8 * x + 4], o[8 * x + 5]), pack2<F16>(o[8 * x + 6], o[8 * x + 7]));
+      }
+      tc_fence_before();
+    }
+    if (!ok) fail();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool F16>
+cudaError_t launch(const FwdLaunch& a) {
+  const Geo& g = a.g;
+  Maps m;
+  if (!make_gather_map(&m.q, a.q, F16, a.q_rows, D) || !make_gather_map(&m.k, a.k, F16, a.k_rows, D) ||
+      !make_gather_map(&m.v, a.v, F16, a.v_rows, D))
+    return cudaErrorInvalidValue;
+  m.kbox = m.k;
+  m.vbox = m.v;
+  const bool boxes = !g.kv_lens;
+  if (boxes && (!make_box_map(&m.kbox, a.k, F16, g.total, g.Hkv, g.k.tok, D) ||
+                !make_box_map(&m.vbox, a.v, F16, g.total, g.Hkv, g.v.tok, D)))
+    return cudaErrorInvalidValue;
+  const size_t smem = sizeof(Smem<D>) + 1024;
+  static_assert(sizeof(Smem<D>) + 1024 <= 232448, "shared memory");
+  cudaError_t e = cudaFuncSetAttribute(ragged_fwd_tc<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  const long long slots = slot_count(g, most_heads(g, a.job.hc), kRows);
+  const long long units = slots * g.Hkv * a.nsplit;
+  if (units > 0x7fffffff) return cudaErrorInvalidValue;
+  const int grid = (int)std::min<long long>(units, sm_count());
+  ragged_fwd_tc<D, F16><<<grid, kThreads, smem, a.stream>>>(a, m, (int)slots, (int)units, boxes);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t tc_ragged_fwd(const FwdLaunch& a, int dtype) {
+  if (a.g.d == 64) return dtype == ST_F16 ? launch<64, true>(a) : launch<64, false>(a);
+  return dtype == ST_F16 ? launch<128, true>(a) : launch<128, false>(a);
+}
+
+}  // namespace rag
+}  // namespace st

@@ -107,40 +107,6 @@ __device__ __forceinline__ void weigh_tile(const float* W, const float* B, int t
   }
 }
 
-// Query row x of a unit's order: token row (absolute), head, position; false
-// past the unit's rows.
-struct QRow {
-  int t, h, pos;
-};
-__device__ __forceinline__ bool query_at(const Geo& g, const Seq& q, int view, const Heads3& hs,
-                                         int x, QRow& r) {
-  if (x >= q.nq * hs.n) return false;
-  const int e = x / hs.n;
-  const int row = query_row(g, q, view, e);
-  r.t = q.qb + row;
-  r.pos = row + q.off;
-  r.h = hs.first + hs.step * (x - e * hs.n);
-  return true;
-}
-
-// First and last key tile of the unit's rows x0 .. x0+BM-1 in a segment.
-__device__ __forceinline__ void tile_range(const Geo& g, const Seq& q, const Job& job, int seg,
-                                           const Heads3& hs, int x0, int rows, int bn, int& j0,
-                                           int& j1) {
-  j0 = j1 = 0;
-  int v0, v1;
-  valid_rows(q, job.qview, v0, v1);
-  const int e0 = imax(x0 / hs.n, v0), e1 = imin((imin(x0 + rows, q.nq * hs.n) - 1) / hs.n, v1 - 1);
-  if (e0 > e1) return;
-  int lo, hi, a, b;
-  live_keys(g, q, job.seg[seg].rule, query_row(g, q, job.qview, e0) + q.off, lo, hi);
-  live_keys(g, q, job.seg[seg].rule, query_row(g, q, job.qview, e1) + q.off, a, b);
-  if (b > lo) {
-    j0 = lo / bn;
-    j1 = (b + bn - 1) / bn;
-  }
-}
-
 template <int D, class T>
 __global__ void __launch_bounds__(NT) ragged_fwd_simt(const __grid_constant__ FwdLaunch a) {
   extern __shared__ float sm[];
@@ -372,24 +338,6 @@ __global__ void __launch_bounds__(NT) ragged_dq_simt(const __grid_constant__ Bwd
       }
     }
   }
-}
-
-// Key heads that a job reaches: whether any query head of the group is in its
-// class.
-__device__ __forceinline__ bool job_reaches(const Geo& g, const Job& job, int kvh) {
-  return heads_of_group(g, job.hc, kvh).n > 0;
-}
-// Whether kvh's dK, dV come from one unit alone and are written by it: one key
-// range, one job, and an order that lists every key.
-__device__ __forceinline__ bool dkv_direct(const BwdLaunch& a, int kvh) {
-  if (a.nsplit > 1) return false;
-  int n = 0, view = VIEW_NAT;
-  for (int j = 0; j < a.njobs; ++j)
-    if (job_reaches(a.g, a.job[j], kvh)) {
-      ++n;
-      view = a.job[j].seg[0].kview;
-    }
-  return n == 1 && view != VIEW_SUM;
 }
 
 // dK, dV of 64 keys: S^T, dP^T = V dO^T, P^T and dS^T, dV += P^T dO, dK += dS^T Q.

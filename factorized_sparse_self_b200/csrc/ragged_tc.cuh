@@ -1,0 +1,118 @@
+// What the tensor-core kernels for ragged sequences share: row-gather TMA
+// loads, the tensor maps behind them, and the units that a scheduler warp
+// decodes for the other warps of its CTA.
+#pragma once
+
+#include "ragged.h"
+#include "tc_common.cuh"
+
+namespace st {
+namespace rag {
+
+using namespace st::tc;
+
+constexpr int kNeed = 128;  // rows of an operand tile
+
+// Four rows (64 elements from column c on) of a matrix, to 4 x 128 bytes of
+// shared memory. The destination lies on a 512-byte boundary of a buffer that
+// starts on a 1024-byte boundary, so the 128-byte swizzle, which goes by the
+// address, is that of one tile. Row numbers are always in range.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c,
+                                            int r0, int r1, int r2, int r3) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(r0), "r"(r1), "r"(r2),
+      "r"(r3)
+      : "memory");
+}
+
+// 64 columns x 128 consecutive tokens of one head.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c,
+                                        int head, int tok) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(head), "r"(tok)
+      : "memory");
+}
+
+// Host: the map of a matrix [rows][d] of 16-bit elements for row gathers, and
+// of token rows [tokens][heads][d] (tok rows of d elements from token to token)
+// for boxes of 128 tokens of one head. False when the driver refuses.
+bool make_gather_map(CUtensorMap* out, const void* base, bool f16, int64_t rows, int d);
+bool make_box_map(CUtensorMap* out, const void* base, bool f16, int tokens, int heads, int tok, int d);
+
+// One query-major unit: 2 x 128 rows of one (sequence, key/value head, job),
+// against the key tiles it meets. Key tiles are numbered through the job's
+// segments: t < cnt0 is tile u0[0] + t of segment 0, later ones of segment 1.
+struct Unit {
+  int32_t live;  // 0: no more units
+  Seq q;
+  Heads3 hs;
+  int32_t kvh, x0, part;
+  int32_t t0, t1;          // key tiles of this unit
+  int32_t cnt0;            // of segment 0
+  int32_t u0[2];           // first tile of each segment
+  int32_t ja[2][2], jb[2][2];  // [128-row half][segment]: tiles it meets
+};
+
+__device__ __forceinline__ void unit_tile(const Unit& u, int t, int& seg, int& j) {
+  seg = t >= u.cnt0 ? 1 : 0;
+  j = u.u0[seg] + t - (seg ? u.cnt0 : 0);
+}
+__device__ __forceinline__ bool half_meets(const Unit& u, int w, int seg, int j) {
+  return j >= u.ja[w][seg] && j < u.jb[w][seg];
+}
+
+// Decodes unit number n into *out (by a whole warp); false if it has no rows.
+// Slots are taken from the last to the first: a sequence's last tiles have the
+// most keys.
+__device__ __forceinline__ bool decode_unit(const Geo& g, const Job& job, int nsplit, int slots,
+                                            int n, int rows, Unit* out) {
+  const int lane = threadIdx.x & 31;
+  const int part = n % nsplit, m = n / nsplit;
+  const int kvh = m % g.Hkv, slot = slots - 1 - m / g.Hkv;
+  int tile;
+  const int s = find_slot(g, most_heads(g, job.hc), rows, slot, tile);
+  const Seq q = load_seq(g, s);
+  const Heads3 hs = heads_of_group(g, job.hc, kvh);
+  const int x0 = tile * rows;
+  if (hs.n == 0 || x0 >= q.nq * hs.n) return false;
+  // lane 2 * half + segment: the tiles that half meets in that segment
+  const int w = (lane >> 1) & 1, sg = lane & 1;
+  int j0 = 0, j1 = 0;
+  if (lane < 4 && sg < job.nseg && w * kNeed < rows && x0 + w * kNeed < q.nq * hs.n)
+    tile_range(g, q, job, sg, hs, x0 + w * kNeed, kNeed, kNeed, j0, j1);
+  // both halves together: rows follow one another, and so do their intervals
+  const int o0 = __shfl_xor_sync(0xffffffffu, j0, 2), o1 = __shfl_xor_sync(0xffffffffu, j1, 2);
+  int a = j0, b = j1;
+  if (o1 > o0) {
+    a = j1 > j0 ? imin(j0, o0) : o0;
+    b = j1 > j0 ? imax(j1, o1) : o1;
+  }
+  const int cnt = b - a;
+  const int cnt1 = __shfl_sync(0xffffffffu, cnt, 1);
+  if (lane < 4) {
+    out->ja[w][sg] = j0;
+    out->jb[w][sg] = j1;
+    if (lane < 2) out->u0[sg] = a;
+    if (lane == 0) {
+      out->live = 1;
+      out->q = q;
+      out->hs = hs;
+      out->kvh = kvh;
+      out->x0 = x0;
+      out->part = part;
+      out->cnt0 = cnt;
+      const long long total = cnt + cnt1;
+      out->t0 = (int)(total * part / nsplit);
+      out->t1 = (int)(total * (part + 1) / nsplit);
+    }
+  }
+  __syncwarp();
+  return true;
+}
+
+}  // namespace rag
+}  // namespace st

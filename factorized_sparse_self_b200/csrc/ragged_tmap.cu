@@ -1,0 +1,55 @@
+// Tensor maps of token-row tensors for the ragged kernels. They are encoded in
+// every call (a few hundred nanoseconds each): callers' buffers come and go.
+#include <cuda.h>
+
+#include "ragged_tc.cuh"
+
+namespace st {
+namespace rag {
+namespace {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+bool encode(CUtensorMap* out, const void* base, bool f16, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+  const EncodeTiledFn enc = encode_fn();
+  const cuuint32_t one[3] = {1, 1, 1};
+  return enc && enc(out, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                    const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool make_gather_map(CUtensorMap* out, const void* base, bool f16, int64_t rows, int d) {
+  const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+  const cuuint32_t box[2] = {64, 1};
+  return encode(out, base, f16, 2, dims, strides, box);
+}
+
+bool make_box_map(CUtensorMap* out, const void* base, bool f16, int tokens, int heads, int tok, int d) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)tok * d * 2};
+  const cuuint32_t box[3] = {64, 1, 128};
+  return encode(out, base, f16, 3, dims, strides, box);
+}
+
+}  // namespace rag
+}  // namespace st
