@@ -1,7 +1,8 @@
 // Forward of attention over ragged and paged sequences on the tensor cores
 // (bf16, fp16; d = 64, 128).
 //
-// Persistent CTAs, one per SM (384 threads). A unit is 256 query rows of one
+// One CTA per SM (384 threads) that goes on with the units of CTAs that have not
+// started (cluster launch control). A unit is 256 query rows of one
 // (sequence, key/value head): two halves of 128 rows that share every K and V
 // tile, so a tile brought from L2 serves 256 rows and the two halves' softmax and
 // products alternate. Warp roles:
@@ -47,6 +48,8 @@ struct alignas(1024) Smem {
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t sched_full[kSched], sched_empty[kSched];
   uint64_t fin;
+  alignas(16) uint4 claim[2];
+  uint64_t claim_bar[2];
   Unit unit[kSched];
   uint32_t tmem;
   int abort;
@@ -59,7 +62,7 @@ struct Maps {
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
     ragged_fwd_tc(const __grid_constant__ FwdLaunch a, const __grid_constant__ Maps maps, int slots,
-                  int n_units, int boxes) {
+                  int boxes) {
   extern __shared__ uint8_t raw[];
   Smem<D>& S = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   constexpr int NS = Cfg<D>::kStages, TB = Cfg<D>::kTileBytes;
@@ -86,6 +89,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.sched_empty[i], 10);  // producer, MMA, eight softmax warps
     }
     mbar_init(&S.fin, 1);
+    mbar_init(&S.claim_bar[0], 1);
+    mbar_init(&S.claim_bar[1], 1);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -108,16 +113,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       int k = 0;
       bool ok = true;
       auto slot_free = [&]() {
-        return k < kSched || __all_sync(0xffffffffu, mbar_wait(&S.sched_empty[k % kSched],
+        return k < kSched || __all_sync(0xffffffffu, bar_wait(&S.sched_empty[k % kSched],
                                                                (k / kSched + 1) & 1, limit, abort));
       };
-      for (int n = blockIdx.x; n < n_units && ok; n += gridDim.x) {
+      Claims claims = {S.claim, S.claim_bar, 0};
+      if (lane == 0) claims_issue(claims, 0);
+      for (int n = blockIdx.x; n >= 0;) {
         ok = slot_free();
         if (!ok) break;
-        if (!decode_unit(g, a.job, a.nsplit, slots, n, kRows, &S.unit[k % kSched])) continue;
-        __threadfence_block();
-        if (lane == 0) mbar_arrive(&S.sched_full[k % kSched]);
-        ++k;
+        if (decode_unit(g, a.job, a.nsplit, slots, n, kRows, &S.unit[k % kSched])) {
+          __threadfence_block();
+          if (lane == 0) mbar_arrive(&S.sched_full[k % kSched]);
+          ++k;
+        }
+        n = claims_take(claims, limit, abort);
+        ok = n != -2;
       }
       if (ok) ok = slot_free();
       if (ok && lane == 0) {
@@ -125,7 +135,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         __threadfence_block();
         mbar_arrive(&S.sched_full[k % kSched]);
       }
-      if (!ok && lane == 0) fail();
+      if (!ok) {
+        if (lane == 0) fail();
+        // a claim in flight lands before the CTA may exit
+        const int last = claims.n > 0 ? claims.n - 1 : 0;
+        mbar_wait_drain(&S.claim_bar[last & 1], (last >> 1) & 1, limit);
+        if (claimed(&S.claim[last & 1]) >= 0) mbar_wait_drain(&S.claim_bar[(last + 1) & 1], ((last + 1) >> 1) & 1, limit);
+      }
     } else if (warp == 8) {
       // ---------------- producer ----------------
       if (lane == 0) {
@@ -136,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int used = 0, kt = 0;  // units with tiles, ring slots filled
       bool ok = true;
       for (int n = 0;; ++n) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&S.sched_full[n % kSched], (n / kSched) & 1, limit, abort));
+        ok = __all_sync(0xffffffffu, bar_wait(&S.sched_full[n % kSched], (n / kSched) & 1, limit, abort));
         if (!ok || !S.unit[n % kSched].live) break;
         const Unit& u = S.unit[n % kSched];
         if (u.t1 <= u.t0) {
@@ -145,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         // Q
-        ok = __all_sync(0xffffffffu, used == 0 || mbar_wait(&S.q_empty, (used - 1) & 1, limit, abort));
+        ok = __all_sync(0xffffffffu, used == 0 || bar_wait(&S.q_empty, (used - 1) & 1, limit, abort));
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&S.q_full, 2 * TB);
         ++used;
@@ -181,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kv = 0; kv < 2; ++kv, ++kt) {
             const int s = kt % NS;
             ok = __all_sync(0xffffffffu,
-                            kt < NS || mbar_wait(&S.kv_empty[s], (kt / NS + 1) & 1, limit, abort));
+                            kt < NS || bar_wait(&S.kv_empty[s], (kt / NS + 1) & 1, limit, abort));
             if (!ok) break;
             const uint32_t dst = smem_u32(S.kv[s]);
             if (lane == 0) mbar_arrive_expect_tx(&S.kv_full[s], TB);
@@ -215,33 +231,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 9) {
       // ---------------- MMA issuer ----------------
-      if (lane == 0) {
-        const uint32_t idS = idesc_16(128, 128, false, false, F16);
-        const uint32_t idPV = idesc_16(128, D, false, true, F16);
-        int kt = 0, used = 0;         // ring slots consumed, units with tiles
-        int np[2] = {0, 0};           // tiles of each half so far
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          if (ok && !mbar_wait(bar, parity, limit, abort)) ok = false;
-          return ok;
-        };
-        auto issue_s = [&](int h, uint32_t ks) {
-          const uint64_t qd = sdesc(smem_u32(S.q[h]), 16, 1024), kd = sdesc(ks, 16, 1024);
+      const uint32_t idS = idesc_16(128, 128, false, false, F16);
+      const uint32_t idPV = idesc_16(128, D, false, true, F16);
+      int kt = 0, used = 0;  // ring slots consumed, units with tiles
+      int np[2] = {0, 0};    // tiles of each half so far
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, limit, abort));
+        return ok;
+      };
+      const uint64_t qd0 = sdesc(smem_u32(S.q[0]), 16, 1024);
+      const uint64_t kd0 = sdesc(smem_u32(S.kv[0]), 16, 1024);
+      const uint64_t vd0 = sdesc(smem_u32(S.kv[0]), 16384, 1024);
+      auto issue_s = [&](int h, int stage) {
+        const uint64_t qd = sdesc_at(qd0, h * TB), kd = sdesc_at(kd0, stage * TB);
+        if (elect_one()) {
 #pragma unroll
           for (int x = 0; x < D / 16; ++x)
             mma_ss(tmem + h * 128, sdesc_at(qd, (x & 3) * 32 + (x >> 2) * 16384),
                    sdesc_at(kd, (x & 3) * 32 + (x >> 2) * 16384), idS, x > 0);
           mma_commit(&S.s_full[h]);
-        };
-        for (int n = 0;; ++n) {
-          if (!wait(&S.sched_full[n % kSched], (n / kSched) & 1)) break;
-          const Unit& u = S.unit[n % kSched];
-          if (!u.live) break;
-          const int t1 = u.t1;
-          if (t1 <= u.t0) {
-            mbar_arrive(&S.sched_empty[n % kSched]);
-            continue;
-          }
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) mma_commit(bar);
+        __syncwarp();
+      };
+      for (int n = 0;; ++n) {
+        if (!wait(&S.sched_full[n % kSched], (n / kSched) & 1)) break;
+        const Unit& u = S.unit[n % kSched];
+        if (!u.live) break;
+        const int t1 = u.t1;
+        if (t1 > u.t0) {
           if (!wait(&S.q_full, used & 1)) break;
           ++used;
           bool fresh[2] = {true, true};
@@ -250,11 +272,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool act[2] = {half_meets(u, 0, seg, j), half_meets(u, 1, seg, j)};
           if (!wait(&S.kv_full[kt % NS], (kt / NS) & 1)) break;
           tc_fence_after();
+#pragma unroll
           for (int h = 0; h < 2; ++h)
-            if (act[h]) issue_s(h, smem_u32(S.kv[kt % NS]));
-          mma_commit(&S.kv_empty[kt % NS]);
-          if (u.t0 + 1 == t1) mma_commit(&S.q_empty);
-          for (int t = u.t0; t < t1 && ok; ++t, kt += 2) {
+            if (act[h]) issue_s(h, kt % NS);
+          commit(&S.kv_empty[kt % NS]);
+          if (u.t0 + 1 == t1) commit(&S.q_empty);
+          for (int t = u.t0; t < t1; ++t, kt += 2) {
             const int sv = (kt + 1) % NS, sk = (kt + 2) % NS;
             const bool more = t + 1 < t1;
             bool nact[2] = {false, false};
@@ -263,48 +286,48 @@ __global__ void __launch_bounds__(kThreads, 1)
               nact[0] = half_meets(u, 0, seg, j);
               nact[1] = half_meets(u, 1, seg, j);
             }
-            const uint64_t vd = sdesc(smem_u32(S.kv[sv]), 16384, 1024);
-            bool have_v = false, have_k = false;
+            // K of the next tile and V of this one are here long before P is
+            if (!wait(&S.kv_full[sv], ((kt + 1) / NS) & 1)) break;
+            if (more && !wait(&S.kv_full[sk], ((kt + 2) / NS) & 1)) break;
+            const uint64_t vd = sdesc_at(vd0, sv * TB);
+#pragma unroll
             for (int h = 0; h < 2; ++h) {
               if (act[h]) {
                 if (!wait(&S.p_full[h], np[h] & 1)) break;
                 ++np[h];
-                if (!have_v && !wait(&S.kv_full[sv], ((kt + 1) / NS) & 1)) break;
-                have_v = true;
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
-                  mma_ts(tmem + kColO + h * D, tmem + h * 128 + x * 8, sdesc_at(vd, x * 2048), idPV,
-                         !fresh[h] || x > 0);
+                  for (int x = 0; x < 8; ++x)
+                    mma_ts(tmem + kColO + h * D, tmem + h * 128 + x * 8, sdesc_at(vd, x * 2048), idPV,
+                           !fresh[h] || x > 0);
+                  mma_commit(&S.o_full[h]);
+                }
+                __syncwarp();
                 fresh[h] = false;
-                mma_commit(&S.o_full[h]);
               }
               if (nact[h]) {
-                if (!have_k && !wait(&S.kv_full[sk], ((kt + 2) / NS) & 1)) break;
-                have_k = true;
                 tc_fence_after();
-                issue_s(h, smem_u32(S.kv[sk]));
+                issue_s(h, sk);
               }
             }
             if (!ok) break;
-            // tiles that neither half met are let go once they have landed
-            if (!have_v && !wait(&S.kv_full[sv], ((kt + 1) / NS) & 1)) break;
-            mma_commit(&S.kv_empty[sv]);
+            commit(&S.kv_empty[sv]);
             if (more) {
-              if (!have_k && !wait(&S.kv_full[sk], ((kt + 2) / NS) & 1)) break;
-              mma_commit(&S.kv_empty[sk]);
-              if (t + 2 == t1) mma_commit(&S.q_empty);
+              commit(&S.kv_empty[sk]);
+              if (t + 2 == t1) commit(&S.q_empty);
             }
             act[0] = nact[0];
             act[1] = nact[1];
           }
           if (!ok) break;
-          mbar_arrive(&S.sched_empty[n % kSched]);
         }
-        if (!ok) fail();
-        mma_commit(&S.fin);
-        if (!mbar_wait_drain(&S.fin, 0, limit)) fail();
+        if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
+        __syncwarp();
       }
+      if (!ok && lane == 0) fail();
+      commit(&S.fin);
+      if (!mbar_wait_drain(&S.fin, 0, limit) && lane == 0) fail();
       __syncwarp();
     }
   } else {
@@ -317,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int ns = 0;  // tiles of this half so far
     for (int n = 0;; ++n) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&S.sched_full[n % kSched], (n / kSched) & 1, limit, abort));
+      ok = __all_sync(0xffffffffu, bar_wait(&S.sched_full[n % kSched], (n / kSched) & 1, limit, abort));
       if (!ok) break;
       const Unit& su = S.unit[n % kSched];
       if (!su.live) break;
@@ -335,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int seg, j;
         unit_tile(su, t, seg, j);
         if (!half_meets(su, h, seg, j)) continue;
-        ok = __all_sync(0xffffffffu, mbar_wait(&S.s_full[h], ns & 1, limit, abort));
+        ok = __all_sync(0xffffffffu, bar_wait(&S.s_full[h], ns & 1, limit, abort));
         if (!ok) break;
         tc_fence_after();
         float s[128];
@@ -375,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = l * alpha + (((sa[0] + sb[0]) + (sa[1] + sb[1])) + ((sa[2] + sb[2]) + (sa[3] + sb[3])));
         if (__any_sync(0xffffffffu, rescale)) {
           // the previous tile's P V has ended before O is touched
-          ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[h], (ns - 1) & 1, limit, abort));
+          ok = __all_sync(0xffffffffu, bar_wait(&S.o_full[h], (ns - 1) & 1, limit, abort));
           if (!ok) break;
           tc_fence_after();
           const float f = rescale ? alpha : 1.f;
@@ -402,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
       // ---- the unit's rows ----
       if (any) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&S.o_full[h], (ns - 1) & 1, limit, abort));
+        ok = __all_sync(0xffffffffu, bar_wait(&S.o_full[h], (ns - 1) & 1, limit, abort));
         if (!ok) break;
         tc_fence_after();
       }
@@ -491,8 +514,7 @@ cudaError_t launch(const FwdLaunch& a) {
   const long long slots = slot_count(g, most_heads(g, a.job.hc), kRows);
   const long long units = slots * g.Hkv * a.nsplit;
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
-  const int grid = (int)std::min<long long>(units, sm_count());
-  ragged_fwd_tc<D, F16><<<grid, kThreads, smem, a.stream>>>(a, m, (int)slots, (int)units, boxes);
+  ragged_fwd_tc<D, F16><<<(unsigned)units, kThreads, smem, a.stream>>>(a, m, (int)slots, boxes);
   return cudaGetLastError();
 }
 

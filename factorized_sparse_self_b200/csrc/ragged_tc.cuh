@@ -13,6 +13,36 @@ using namespace st::tc;
 
 constexpr int kNeed = 128;  // rows of an operand tile
 
+// One lane of the (converged) warp, the same one every time. The MMA warps run
+// their control flow with all lanes and pick the issuing lane around the
+// tcgen05 instructions only: descriptors then stay in uniform registers. With
+// the whole role inside `if (lane == 0)` each MMA took 80 to 130 cycles to
+// issue (d = 64's P V needs 32 on the pipe).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Waits for a phase; gives up after limit_ns or when another role raised
+// `abort`. The clock and the flag are looked at after every 64 attempts only:
+// read in every attempt, they delay the waking thread.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                         volatile int* abort) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 63) == 0) {
+      if (*abort) return false;
+      const uint64_t now = globaltimer();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > limit_ns) return false;
+    }
+  }
+}
+
 // Four rows (64 elements from column c on) of a matrix, to 4 x 128 bytes of
 // shared memory. The destination lies on a 512-byte boundary of a buffer that
 // starts on a 1024-byte boundary, so the 128-byte swizzle, which goes by the
@@ -35,6 +65,60 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, ui
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(head), "r"(tok)
       : "memory");
+}
+
+// ---- work claimed from the grid ------------------------------------------------
+// A kernel is launched with one CTA per unit; a running CTA takes over units
+// whose CTAs have not started yet (cluster launch control), so units go to
+// whichever SM is free, in order, without a counter in memory.
+
+// Asks for the next CTA of the grid; the 16-byte answer lands in `dst`.
+__device__ __forceinline__ void claim_next(void* dst, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(dst)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// The claimed CTA's index, or -1 if none was left.
+__device__ __forceinline__ int claimed(const void* src) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(src))
+      : "memory");
+  return ok ? (int)x : -1;
+}
+
+// One scheduler warp's claims, one ahead.
+struct Claims {
+  uint4* slot;     // [2], shared memory
+  uint64_t* bar;   // [2]
+  int n;           // claims taken
+};
+__device__ __forceinline__ void claims_issue(const Claims& c, int k) {
+  mbar_arrive_expect_tx(&c.bar[k & 1], 16);
+  claim_next(&c.slot[k & 1], &c.bar[k & 1]);
+}
+// Next unit index (by a whole warp): -1 when the grid is used up, -2 when the
+// wait ran out. The claim after it is asked for before this one is used.
+__device__ __forceinline__ int claims_take(Claims& c, uint64_t limit, volatile int* abort) {
+  const int k = c.n++;
+  if (!__all_sync(0xffffffffu, bar_wait(&c.bar[k & 1], (k >> 1) & 1, limit, abort))) return -2;
+  const int got = claimed(&c.slot[k & 1]);
+  __syncwarp();
+  if (got >= 0 && (threadIdx.x & 31) == 0) {
+    fence_async_smem();  // the answer in the other slot was read before it is written anew
+    claims_issue(c, k + 1);
+  }
+  __syncwarp();
+  return got;
 }
 
 // Host: the map of a matrix [rows][d] of 16-bit elements for row gathers, and
