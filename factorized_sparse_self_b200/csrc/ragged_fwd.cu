@@ -29,7 +29,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kRows = 256;  // query rows of a unit
 constexpr int kSched = 3;   // units decoded ahead
-constexpr uint32_t kRegsSoftmax = 216, kRegsIssue = 72;  // 168 at launch: 2 * 216 + 72 = 3 * 168
+constexpr uint32_t kRegsSoftmax = 224, kRegsIssue = 56;  // 168 at launch: 2 * 224 + 56 = 3 * 168
 constexpr float kRescale = 8.f;  // log2
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -235,10 +235,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idPV = idesc_16(128, D, false, true, F16);
       int kt = 0, used = 0;  // ring slots consumed, units with tiles
       int np[2] = {0, 0};    // tiles of each half so far
+      // A lane's failed wait is remembered and agreed on at the end of the unit:
+      // until then the warp goes on (later waits of that lane return at once).
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, limit, abort));
-        return ok;
+        if (ok) ok = bar_wait(bar, parity, limit, abort);
+        __syncwarp();
       };
       const uint64_t qd0 = sdesc(smem_u32(S.q[0]), 16, 1024);
       const uint64_t kd0 = sdesc(smem_u32(S.kv[0]), 16, 1024);
@@ -259,41 +261,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       };
       for (int n = 0;; ++n) {
-        if (!wait(&S.sched_full[n % kSched], (n / kSched) & 1)) break;
+        wait(&S.sched_full[n % kSched], (n / kSched) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         const Unit& u = S.unit[n % kSched];
         if (!u.live) break;
-        const int t1 = u.t1;
-        if (t1 > u.t0) {
-          if (!wait(&S.q_full, used & 1)) break;
+        const int t0 = u.t0, t1 = u.t1, cnt0 = u.cnt0, first0 = u.u0[0], first1 = u.u0[1] - cnt0;
+        if (t1 > t0) {
+          // the tiles of a half, as numbers t, segment by segment, and its last
+          int a0[2], b0[2], a1[2], b1[2], last[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            a0[h] = u.ja[h][0] - first0;
+            b0[h] = u.jb[h][0] - first0;
+            a1[h] = imax(u.ja[h][1] - first1, cnt0);
+            b1[h] = u.jb[h][1] - first1;
+            last[h] = imin(b1[h], t1) > imax(a1[h], t0) ? imin(b1[h], t1) - 1 : imin(imin(b0[h], cnt0), t1) - 1;
+          }
+          auto meets = [&](int h, int t) {
+            return t < t1 && (t < cnt0 ? t >= a0[h] && t < b0[h] : t >= a1[h] && t < b1[h]);
+          };
+          wait(&S.q_full, used & 1);
           ++used;
           bool fresh[2] = {true, true};
-          int seg, j;
-          unit_tile(u, u.t0, seg, j);
-          bool act[2] = {half_meets(u, 0, seg, j), half_meets(u, 1, seg, j)};
-          if (!wait(&S.kv_full[kt % NS], (kt / NS) & 1)) break;
+          bool act[2] = {meets(0, t0), meets(1, t0)};
+          wait(&S.kv_full[kt % NS], (kt / NS) & 1);
           tc_fence_after();
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             if (act[h]) issue_s(h, kt % NS);
           commit(&S.kv_empty[kt % NS]);
-          if (u.t0 + 1 == t1) commit(&S.q_empty);
-          for (int t = u.t0; t < t1; ++t, kt += 2) {
-            const int sv = (kt + 1) % NS, sk = (kt + 2) % NS;
-            const bool more = t + 1 < t1;
-            bool nact[2] = {false, false};
-            if (more) {
-              unit_tile(u, t + 1, seg, j);
-              nact[0] = half_meets(u, 0, seg, j);
-              nact[1] = half_meets(u, 1, seg, j);
+          if (t0 + 1 == t1) commit(&S.q_empty);
+          int sv = (kt + 1) % NS, pv = ((kt + 1) / NS) & 1;
+          for (int t = t0; t < t1; ++t, kt += 2) {
+            int sk = sv + 1, pk = pv;
+            if (sk == NS) {
+              sk = 0;
+              pk ^= 1;
             }
-            // K of the next tile and V of this one are here long before P is
-            if (!wait(&S.kv_full[sv], ((kt + 1) / NS) & 1)) break;
-            if (more && !wait(&S.kv_full[sk], ((kt + 2) / NS) & 1)) break;
+            const bool more = t + 1 < t1;
+            const bool nact[2] = {meets(0, t + 1), meets(1, t + 1)};
             const uint64_t vd = sdesc_at(vd0, sv * TB);
+            wait(&S.kv_full[sv], pv);
+            if (more) wait(&S.kv_full[sk], pk);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               if (act[h]) {
-                if (!wait(&S.p_full[h], np[h] & 1)) break;
+                wait(&S.p_full[h], np[h] & 1);
                 ++np[h];
                 tc_fence_after();
                 if (elect_one()) {
@@ -301,17 +315,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                   for (int x = 0; x < 8; ++x)
                     mma_ts(tmem + kColO + h * D, tmem + h * 128 + x * 8, sdesc_at(vd, x * 2048), idPV,
                            !fresh[h] || x > 0);
-                  mma_commit(&S.o_full[h]);
+                  // the next S of this half is issued behind this product, so
+                  // only the unit's last one needs a signal of its own
+                  if (t == last[h]) mma_commit(&S.o_full[h]);
                 }
                 __syncwarp();
                 fresh[h] = false;
               }
-              if (nact[h]) {
-                tc_fence_after();
-                issue_s(h, sk);
-              }
+              if (nact[h]) issue_s(h, sk);
             }
-            if (!ok) break;
             commit(&S.kv_empty[sv]);
             if (more) {
               commit(&S.kv_empty[sk]);
@@ -319,8 +331,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             act[0] = nact[0];
             act[1] = nact[1];
+            sv = sk + 1;
+            pv = pk;
+            if (sv == NS) {
+              sv = 0;
+              pv ^= 1;
+            }
           }
-          if (!ok) break;
         }
         if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
         __syncwarp();
@@ -338,20 +355,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + tl + h * 128, tO = tmem + tl + kColO + h * D;
     const int row = (warp & 3) * 32 + lane;
     bool ok = true;
-    int ns = 0;  // tiles of this half so far
+    int ns = 0, no = 0;  // tiles of this half so far, units with tiles
     for (int n = 0;; ++n) {
       ok = __all_sync(0xffffffffu, bar_wait(&S.sched_full[n % kSched], (n / kSched) & 1, limit, abort));
       if (!ok) break;
       const Unit& su = S.unit[n % kSched];
       if (!su.live) break;
-      QRow qr;
-      const bool have = query_at(g, su.q, a.job.qview, su.hs, su.x0 + h * 128 + row, qr);
       int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0;
-      if (have && qr.pos >= 0) {
-        live_keys(g, su.q, a.job.seg[0].rule, qr.pos, lo0, hi0);
-        if (a.job.nseg > 1) live_keys(g, su.q, a.job.seg[1].rule, qr.pos, lo1, hi1);
+      {
+        QRow qr;
+        if (query_at(g, su.q, a.job.qview, su.hs, su.x0 + h * 128 + row, qr) && qr.pos >= 0) {
+          live_keys(g, su.q, a.job.seg[0].rule, qr.pos, lo0, hi0);
+          if (a.job.nseg > 1) live_keys(g, su.q, a.job.seg[1].rule, qr.pos, lo1, hi1);
+        }
       }
-      const int t1 = su.t1, part = su.part;
+      const int t1 = su.t1;
       float m = -INFINITY, l = 0.f;
       bool any = false;
       for (int t = su.t0; t < t1; ++t) {
@@ -385,22 +403,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float nmu = m == -INFINITY ? 0.f : -m;
         float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t pk[64];
 #pragma unroll
-        for (int x = 0; x < 128; x += 2) {
-          float a0, a1;
-          ffma2(a0, a1, s[x], s[x + 1], a.scale_log2, a.scale_log2, nmu, nmu);
-          const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
-          const int y = (x >> 1) & 3;
-          fadd2(sa[y], sb[y], sa[y], sb[y], p0, p1);
-          pk[x >> 1] = pack2<F16>(p0, p1);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int x = 0; x < 64; x += 2) {
+            float a0, a1;
+            ffma2(a0, a1, s[c * 64 + x], s[c * 64 + x + 1], a.scale_log2, a.scale_log2, nmu, nmu);
+            const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+            const int y = (x >> 1) & 3;
+            fadd2(sa[y], sb[y], sa[y], sb[y], p0, p1);
+            pk[x >> 1] = pack2<F16>(p0, p1);
+          }
+          tmem_st32(tS + c * 32, pk);
         }
         l = l * alpha + (((sa[0] + sb[0]) + (sa[1] + sb[1])) + ((sa[2] + sb[2]) + (sa[3] + sb[3])));
         if (__any_sync(0xffffffffu, rescale)) {
-          // the previous tile's P V has ended before O is touched
-          ok = __all_sync(0xffffffffu, bar_wait(&S.o_full[h], (ns - 1) & 1, limit, abort));
-          if (!ok) break;
-          tc_fence_after();
+          // the previous tile's P V was issued before this tile's S, so it has ended
           const float f = rescale ? alpha : 1.f;
 #pragma unroll 1
           for (int c = 0; c < D; c += 8) {
@@ -412,8 +431,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st8(tO + c, o);
           }
         }
-        tmem_st32(tS, pk);
-        tmem_st32(tS + 32, pk + 32);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&S.p_full[h]);
@@ -421,12 +438,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ns;
       }
       if (!ok) break;
+      // ---- the unit's rows ----
+      // (the row is worked out again: kept over the tiles it would cost them registers)
+      QRow qr;
+      const bool have = query_at(g, su.q, a.job.qview, su.hs, su.x0 + h * 128 + row, qr);
+      const int part = su.part;
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
-      // ---- the unit's rows ----
       if (any) {
-        ok = __all_sync(0xffffffffu, bar_wait(&S.o_full[h], (ns - 1) & 1, limit, abort));
+        ok = __all_sync(0xffffffffu, bar_wait(&S.o_full[h], no & 1, limit, abort));
         if (!ok) break;
+        ++no;
         tc_fence_after();
       }
       float L = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
