@@ -8,10 +8,11 @@
 // positions one after the other,
 //   natural  0, 1, 2, ...
 //   summary  the last c positions of every l-block, packed (keys only)
-//   class    residue class 0 (0, l, 2l, ...), then class 1, ... up to l - 1
+//   class    residue class by residue class (p, p + l, p + 2l, ...), beginning
+//            with the class of the first query: a chunk's queries then stand in
+//            the classes that follow one another, not at both ends of the order
 // and in its order every query row's live keys are ONE interval [lo, hi) whose
-// ends never decrease from row to row (asserted for small sizes on the host by
-// the tests of the calls). A tile of rows therefore meets the keys from its
+// ends never decrease from row to row. A tile of rows therefore meets the keys from its
 // first row's lo to its last row's hi, and, the other way round, key k meets
 // the rows from the first with hi > k up to the first with lo > k.
 //
@@ -86,6 +87,7 @@ struct Seq {
   int32_t P, rem;    // nk / l, nk mod l
   int32_t Po, remo;  // the same of max(off, 0)
   int32_t nsum;      // summary positions among the keys
+  int32_t rotk, rotq;  // keys / queries of the classes below the first query's
 };
 
 ST_HD int imin(int a, int b) { return a < b ? a : b; }
@@ -104,15 +106,16 @@ ST_HD Seq make_seq(const Geo& g, int s, int qb, int nq, int nk) {
   q.rem = nk - q.P * g.l;
   q.Po = qdiv(o, g.fl, g.l);
   q.remo = o - q.Po * g.l;
+  q.rotk = q.remo * q.P + imin(q.remo, q.rem);
+  q.rotq = q.rotk - q.remo * q.Po - q.remo;
   q.nsum = q.P * g.c + imax(0, q.rem - (g.l - g.c));
   return q;
 }
 
 // First index of class r in the class order of the keys 0 .. nk-1.
-ST_HD int cls_key_start(const Seq& q, int r) { return r * q.P + imin(r, q.rem); }
-// First index of class r in the class order of the queries max(off, 0) .. nk-1.
-ST_HD int cls_query_start(const Seq& q, int r) {
-  return r * (q.P - q.Po) + imin(r, q.rem) - imin(r, q.remo);
+ST_HD int cls_key_start(const Seq& q, int r) {
+  const int s = r * q.P + imin(r, q.rem) - q.rotk;
+  return r >= q.remo ? s : s + q.nk;
 }
 
 // Position of key index e of an order (0 <= e < number of keys in it).
@@ -122,6 +125,8 @@ ST_HD int key_pos(const Geo& g, const Seq& q, int view, int e) {
     const int b = qdiv(e, g.fc, g.c);
     return b * g.l + (g.l - g.c) + (e - b * g.c);
   }
+  e += q.rotk;
+  if (e >= q.nk) e -= q.nk;
   const int big = q.rem * (q.P + 1);  // <= nk
   if (e < big) {
     const int r = e / (q.P + 1);
@@ -139,6 +144,8 @@ ST_HD int n_keys(const Seq& q, int view) { return view == VIEW_SUM ? q.nsum : q.
 ST_HD int query_row(const Geo& g, const Seq& q, int view, int e) {
   if (view == VIEW_NAT) return e;
   if (e >= q.nqv) return e - q.nqv;
+  e += q.rotq;
+  if (e >= q.nqv) e -= q.nqv;
   // Classes start at slope D = P - Po, one more between remo and rem (or one
   // less between rem and remo): three pieces of equal classes.
   const int D = q.P - q.Po;

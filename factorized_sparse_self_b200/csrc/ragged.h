@@ -23,20 +23,30 @@ struct Parts {
   float* lse;
 };
 
-// One launch of a forward kernel: one job, its keys cut into nsplit parts.
+// A unit's keys are cut into at most nsplit parts of at least `least` key tiles;
+// its first part marks the parts it does not use as empty (LSE = -inf).
+ST_HD int parts_of(int tiles, int nsplit, int least) {
+  return imax(1, imin(nsplit, (tiles + least - 1) / least));
+}
+
+// One launch of a forward kernel: one job (the few-row kernel: all jobs at
+// once), its keys cut into up to nsplit parts.
 struct FwdLaunch {
   Geo g;
   Job job;
+  Job job1;          // few-row kernel: the second job
+  int32_t njobs;
   const void *q, *k, *v;
   void* o;
   float* lse;
   Parts parts;
   int32_t part0;   // first part of this job
-  int32_t nsplit;  // OUT_PARTIAL: key ranges per unit (grid z)
+  int32_t part1;   // few-row kernel: of the second job
+  int32_t nsplit;  // OUT_PARTIAL: most key ranges of a unit
+  int32_t least;   // fewest key tiles of a range
   int32_t mode;    // OutMode
   float scale_log2;
   uint64_t wait_ns;
-  int64_t q_rows, k_rows, v_rows;  // rows of the matrices behind q, k and v
   cudaStream_t stream;
 };
 
@@ -55,7 +65,6 @@ struct BwdLaunch {
   int32_t nsplit;
   float scale;
   uint64_t wait_ns;
-  int64_t q_rows, k_rows, v_rows;
   cudaStream_t stream;
 };
 
@@ -81,6 +90,10 @@ __device__ __forceinline__ bool dkv_direct(const BwdLaunch& a, int kvh) {
 
 // Tensor-core forward: bf16 / fp16, d = 64 or 128.
 cudaError_t tc_ragged_fwd(const FwdLaunch& a, int dtype);
+
+// Few query rows per key/value head over a paged cache (decoding steps): bf16 /
+// fp16, d = 64 or 128.
+cudaError_t few_rows_fwd(const FwdLaunch& a, int dtype);
 
 // CUDA-core kernels in fp32 arithmetic.
 cudaError_t simt_ragged_fwd(const FwdLaunch& a, int dtype);

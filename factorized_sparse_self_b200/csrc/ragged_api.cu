@@ -11,6 +11,7 @@ using namespace st::rag;
 namespace {
 
 constexpr int kPartsLimit = 32;  // most key ranges of one row
+constexpr int kFewRows = 32;     // most query rows per key/value head for the few-row kernel
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -130,11 +131,6 @@ st_status fill_cache(const st_cache_desc* c, Geo& g) {
   return ST_OK;
 }
 
-int64_t cache_rows(const Geo& g) {
-  return (int64_t)(g.num_pages - 1) * g.k.page + (int64_t)(g.page_size - 1) * g.k.tok +
-         (int64_t)(g.Hkv - 1) * g.k.head + 1;
-}
-
 // The status word of the current device; it is created by the first call
 // (which therefore may not be captured).
 st_status get_status(Geo& g, cudaStream_t stream) {
@@ -151,32 +147,63 @@ st_status get_status(Geo& g, cudaStream_t stream) {
 
 // How a forward call is cut up.
 struct FwdPlan {
-  int nsplit;   // key ranges per unit and job
+  bool few;     // the few-row kernel
+  int nsplit;   // most key ranges per unit and job
+  int least;    // fewest key tiles (of the kernel) of a range
   int nparts;   // parts of a row (0: rows are written directly)
   bool merge;   // the second order joins the first's part itself
   size_t parts_o, bytes;
 };
 
-// Key ranges: enough units for the GPU when there are few rows, none shorter
-// than `least` key tiles of the longest sequence.
-int choose_split(long long units, int longest_tiles, int least, int sms) {
-  if (units < 1) return 1;
-  long long n = (2LL * sms + units - 1) / units;
-  const long long cap = std::max(1, longest_tiles / least);
-  n = std::min(n, cap);
-  n = std::min<long long>(n, kPartsLimit);
-  return (int)std::max<long long>(1, n);
+// Rows that one query row's pattern lets it attend, at most, in a sequence of T.
+long long most_keys(const st_pattern_desc& p) {
+  if (p.kind == ST_DENSE_CAUSAL) return p.T;
+  const long long a = p.kind == ST_STRIDED ? (long long)p.l + 1 : p.l;
+  const long long b = p.kind == ST_STRIDED ? (p.T + p.l - 1LL) / p.l
+                                           : ((long long)p.T / p.l + 1) * p.c;
+  return std::min<long long>(p.T, p.head_mode == ST_HEADS_MERGED ? a + b : std::max(a, b));
 }
 
-FwdPlan plan_fwd(const Geo& g, const st_pattern_desc& p, int nsplit) {
+int clamp_int(long long x, long long lo, long long hi) {
+  return (int)std::max(lo, std::min(x, hi));
+}
+
+// Key ranges (the kernels cut short units into fewer). Units go to free SMs one
+// by one, so only few units leave SMs idle: those of one longest sequence (the
+// others may be short) have to be worth the GPU. A prompt's units see 1 .. T
+// keys, the longest ones first; a chunk's see all of the context, so they should
+// come in twos per SM. Dense, H = 32, Hkv = 8, d = 128, chunks of 512 tokens behind
+// 32 K, 8 K, 4 K keys: 2334 us with one range each, 1194 with five.
+FwdPlan plan_fwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype, long long max_q, bool paged) {
   FwdPlan f{};
-  f.nsplit = nsplit;
+  const long long sms = sm_count(), keys = most_keys(p);
+  const int G = g.split ? (g.G + 1) / 2 : g.G;
+  f.few = paged && dtype != ST_F32 && max_q * G <= kFewRows;
+  const int rows = f.few ? 16 : dtype == ST_F32 ? 64 : 256;
+  const int key_tile = f.few ? 16 : dtype == ST_F32 ? 64 : 128;
+  const long long longest = std::max(1LL, (max_q * G + rows - 1) / rows * g.Hkv);
+  const long long all = std::max(longest, ((long long)g.total * G + rows - 1) / rows * g.Hkv);
+  if (f.few) {
+    // ranges of 128 to 1024 keys, about four for each of the CTAs that run at once
+    const long long want = keys * all / (8 * sms);
+    f.least = clamp_int(want, 128, 1024) / key_tile;
+    f.nsplit = clamp_int((keys + f.least * key_tile - 1) / (f.least * key_tile), 1, kPartsLimit);
+  } else {
+    f.least = 512 / key_tile;
+    long long n = 1;
+    if (paged) {
+      if (all < 4 * sms) n = (2 * sms + longest - 1) / longest;
+    } else if (longest < sms) {
+      n = (sms + longest - 1) / longest;
+    }
+    f.nsplit = clamp_int(std::min(n, keys / 512), 1, kPartsLimit);
+  }
   const bool two = two_orders(p);
-  f.merge = two && nsplit == 1;
-  f.nparts = nsplit > 1 ? (two ? 2 * nsplit : nsplit) : two ? 1 : 0;
-  const size_t rows = (size_t)g.total * g.H;
-  f.parts_o = round256(rows * g.d * sizeof(float) * f.nparts);
-  f.bytes = f.nparts ? f.parts_o + round256(rows * sizeof(float) * f.nparts) : 0;
+  f.merge = two && f.nsplit == 1 && !f.few;
+  f.nparts = f.merge ? 1 : two ? 2 * f.nsplit : f.nsplit > 1 ? f.nsplit : 0;
+  const size_t qrows = (size_t)g.total * g.H;
+  f.parts_o = round256(qrows * g.d * sizeof(float) * f.nparts);
+  f.bytes = f.nparts ? f.parts_o + round256(qrows * sizeof(float) * f.nparts) : 0;
   return f;
 }
 
@@ -184,23 +211,9 @@ bool workspace_ok(const void* ws, size_t have, size_t need) {
   return need == 0 || (ws && have >= need && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0);
 }
 
-// Rows that one query row's pattern lets it attend, at most, in a sequence of T.
-int most_keys(const st_pattern_desc& p) {
-  if (p.kind == ST_DENSE_CAUSAL) return p.T;
-  const long long a = p.kind == ST_STRIDED ? (long long)p.l + 1 : p.l;
-  const long long b = p.kind == ST_STRIDED ? (p.T + p.l - 1LL) / p.l
-                                           : ((long long)p.T / p.l + 1) * p.c;
-  return (int)std::min<long long>(p.T, p.head_mode == ST_HEADS_MERGED ? a + b : std::max(a, b));
-}
-
-int fwd_split(const Geo& g, const st_pattern_desc& p) {
-  const long long units = ((long long)g.total * g.G + 63) / 64 * g.Hkv;
-  return choose_split(units, (most_keys(p) + 63) / 64, 8, sm_count());
-}
-
 st_status run_fwd(const st_pattern_desc& p, st_dtype dtype, Geo& g, float scale, const FwdPlan& f,
                   const void* q, const void* k, const void* v, void* o, float* lse, void* ws,
-                  int64_t q_rows, int64_t k_rows, int64_t v_rows, cudaStream_t stream) {
+                  cudaStream_t stream) {
   FwdLaunch a{};
   a.g = g;
   a.q = q;
@@ -208,19 +221,25 @@ st_status run_fwd(const st_pattern_desc& p, st_dtype dtype, Geo& g, float scale,
   a.v = v;
   a.o = o;
   a.lse = lse;
-  a.q_rows = q_rows;
-  a.k_rows = k_rows;
-  a.v_rows = v_rows;
   a.parts.o = static_cast<float*>(ws);
   a.parts.lse = reinterpret_cast<float*>(static_cast<char*>(ws) + f.parts_o);
   a.nsplit = f.nsplit;
+  a.least = f.least;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)g.d)) * 1.4426950408889634f;
   a.wait_ns = wait_limit_ns();
   a.stream = stream;
   Job jobs[2];
   const int n = make_jobs(p, jobs);
   cudaError_t e = cudaSuccess;
-  for (int j = 0; j < n && e == cudaSuccess; ++j) {
+  if (f.few) {
+    a.job = jobs[0];
+    a.job1 = jobs[n - 1];
+    a.njobs = n;
+    a.part1 = two_orders(p) ? f.nsplit : 0;
+    a.mode = f.nparts ? OUT_PARTIAL : OUT_FINAL;
+    e = few_rows_fwd(a, dtype);
+  }
+  for (int j = 0; j < n && !f.few && e == cudaSuccess; ++j) {
     a.job = jobs[j];
     a.part0 = two_orders(p) && j == 1 && !f.merge ? f.nsplit : 0;
     a.mode = f.merge ? (j == 0 ? OUT_PARTIAL : OUT_MERGE) : f.nparts ? OUT_PARTIAL : OUT_FINAL;
@@ -247,9 +266,12 @@ BwdPlan plan_bwd(const Geo& g, const st_pattern_desc& p) {
   for (int j = 0; j < n; ++j)
     for (int s = 0; s < jobs[j].nseg; ++s)
       b.kjob[b.njobs++] = Job{jobs[j].hc, jobs[j].qview, 1, {jobs[j].seg[s], jobs[j].seg[s]}};
-  const long long units = ((long long)g.total + 63) / 64 * g.Hkv;
-  long long rows = (long long)p.T * g.G;  // query rows that reach one key, at most
-  b.nsplit = choose_split(units, (int)std::min<long long>((rows + 63) / 64, 1 << 20), 8, sm_count());
+  // key tiles of one longest sequence against the query rows that reach them
+  const long long units = ((long long)p.T + 127) / 128 * g.Hkv;
+  b.nsplit = units < sm_count() ? clamp_int(std::min<long long>((sm_count() + units - 1) / units,
+                                                               (long long)p.T * g.G / 512),
+                                            1, kPartsLimit)
+                                : 1;
   // one part is enough only where every key head has one job over all its keys
   b.parts = b.nsplit > 1 || (b.njobs == 2 && !(g.split && g.G == 1 && b.kjob[1].seg[0].kview != VIEW_SUM));
   const size_t qrows = (size_t)g.total * g.H, krows = (size_t)g.total * g.Hkv;
@@ -270,7 +292,7 @@ st_status st_packed_attn_fwd_workspace(const st_pattern_desc* p, st_dtype dtype,
   if (!bytes) return ST_ERR_INVALID;
   st_status s = fill_geo(p, dtype, x, true, g);
   if (s != ST_OK) return s;
-  *bytes = plan_fwd(g, *p, fwd_split(g, *p)).bytes;
+  *bytes = plan_fwd(g, *p, dtype, p->T, false).bytes;
   return ST_OK;
 }
 
@@ -285,15 +307,13 @@ st_status st_packed_attn_fwd(const st_pattern_desc* p, st_dtype dtype, const st_
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) ||
       !aligned4(cu))
     return ST_ERR_INVALID;
-  const FwdPlan f = plan_fwd(g, *p, fwd_split(g, *p));
+  const FwdPlan f = plan_fwd(g, *p, dtype, p->T, false);
   if (!workspace_ok(ws, ws_bytes, f.bytes)) return ST_ERR_WORKSPACE;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   s = get_status(g, cs);
   if (s != ST_OK) return s;
   g.cu = cu;
-  return run_fwd(*p, dtype, g, scale, f, q, k, v, o, lse, ws,
-                 (int64_t)(g.total - 1) * g.q.tok + g.H, (int64_t)(g.total - 1) * g.k.tok + g.Hkv,
-                 (int64_t)(g.total - 1) * g.v.tok + g.Hkv, cs);
+  return run_fwd(*p, dtype, g, scale, f, q, k, v, o, lse, ws, cs);
 }
 
 st_status st_packed_attn_bwd_workspace(const st_pattern_desc* p, st_dtype dtype,
@@ -349,9 +369,6 @@ st_status st_packed_attn_bwd(const st_pattern_desc* p, st_dtype dtype, const st_
   a.parts = reinterpret_cast<float*>(w + b.delta + b.dq_part);
   a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)g.d);
   a.wait_ns = wait_limit_ns();
-  a.q_rows = (int64_t)(g.total - 1) * g.q.tok + g.H;
-  a.k_rows = (int64_t)(g.total - 1) * g.k.tok + g.Hkv;
-  a.v_rows = (int64_t)(g.total - 1) * g.v.tok + g.Hkv;
   a.stream = cs;
   cudaError_t e = row_delta(g, dtype, o, dout, delta, cs);
   if (e == cudaSuccess) e = simt_ragged_dkv(a, dtype);
@@ -372,7 +389,7 @@ st_status st_paged_attn_workspace(const st_pattern_desc* p, st_dtype dtype,
   st_status s = fill_geo(p, dtype, x, true, g);
   if (s == ST_OK) s = fill_cache(c, g);
   if (s != ST_OK) return s;
-  *bytes = plan_fwd(g, *p, fwd_split(g, *p)).bytes;
+  *bytes = plan_fwd(g, *p, dtype, max_q, true).bytes;
   return ST_OK;
 }
 
@@ -390,7 +407,7 @@ st_status st_paged_attn(const st_pattern_desc* p, st_dtype dtype, const st_packe
   if (!aligned16(q) || !aligned16(kc) || !aligned16(vc) || !aligned16(o) || !aligned16(lse) ||
       !aligned4(cu) || !aligned4(kv_lens) || !aligned4(table))
     return ST_ERR_INVALID;
-  const FwdPlan f = plan_fwd(g, *p, fwd_split(g, *p));
+  const FwdPlan f = plan_fwd(g, *p, dtype, max_q, true);
   if (!workspace_ok(ws, ws_bytes, f.bytes)) return ST_ERR_WORKSPACE;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   s = get_status(g, cs);
@@ -398,8 +415,7 @@ st_status st_paged_attn(const st_pattern_desc* p, st_dtype dtype, const st_packe
   g.cu = cu;
   g.kv_lens = kv_lens;
   g.table = table;
-  return run_fwd(*p, dtype, g, scale, f, q, kc, vc, o, lse, ws,
-                 (int64_t)(g.total - 1) * g.q.tok + g.H, cache_rows(g), cache_rows(g), cs);
+  return run_fwd(*p, dtype, g, scale, f, q, kc, vc, o, lse, ws, cs);
 }
 
 st_status st_cache_append(st_dtype dtype, const st_packed_desc* x, const st_cache_desc* c,

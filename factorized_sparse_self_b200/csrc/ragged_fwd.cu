@@ -7,12 +7,11 @@
 // tile, so a tile brought from L2 serves 256 rows and the two halves' softmax and
 // products alternate. Warp roles:
 //   warp 10      scheduler: decodes the CTA's units into a small ring;
-//   warp 8       producer: Q rows, then K and V tiles of 128 rows in turn into
-//                one ring. Rows are gathered (32 lanes, four rows each) through the
-//                order's index map and the page table; 128 consecutive rows of a
-//                packed sequence come as one box. Rows behind the last key repeat
-//                it: masked entries have weight 0 and must not meet another
-//                sequence's infinities;
+//   warps 8, 11  producers: Q rows, then K and V tiles of 128 rows in turn into
+//                one ring. Rows are gathered through the order's index map and the
+//                page table; 128 consecutive rows of a packed sequence come as a
+//                TMA box. Rows behind the last key repeat it: masked entries have
+//                weight 0 and must not meet another sequence's infinities;
 //   warp 9       MMA issuer: S_h = Q_h K^T (128 x 128 fp32 in TMEM), O_h += P_h V
 //                with P_h read from TMEM; the order S0 S1 | P0V S0' | P1V S1' | ..
 //                keeps one half's products under the other half's softmax;
@@ -29,7 +28,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kRows = 256;  // query rows of a unit
 constexpr int kSched = 3;   // units decoded ahead
-constexpr uint32_t kRegsSoftmax = 224, kRegsIssue = 56;  // 168 at launch: 2 * 224 + 56 = 3 * 168
+constexpr uint32_t kRegsSoftmax = 216, kRegsIssue = 72;  // 168 at launch: 2 * 216 + 72 = 3 * 168
 constexpr float kRescale = 8.f;  // log2
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -56,7 +55,7 @@ struct alignas(1024) Smem {
 };
 
 struct Maps {
-  CUtensorMap q, k, v, kbox, vbox;
+  CUtensorMap kbox, vbox;
 };
 
 template <int D, bool F16>
@@ -73,10 +72,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &S.abort;
   if (threadIdx.x == 0) {
     S.abort = 0;
-    mbar_init(&S.q_full, 1);
+    mbar_init(&S.q_full, 2);  // both producers
     mbar_init(&S.q_empty, 1);
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&S.kv_full[i], 1);
+      mbar_init(&S.kv_full[i], 2);
       mbar_init(&S.kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -86,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kSched; ++i) {
       mbar_init(&S.sched_full[i], 1);
-      mbar_init(&S.sched_empty[i], 10);  // producer, MMA, eight softmax warps
+      mbar_init(&S.sched_empty[i], 11);  // two producers, MMA, eight softmax warps
     }
     mbar_init(&S.fin, 1);
     mbar_init(&S.claim_bar[0], 1);
@@ -121,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = blockIdx.x; n >= 0;) {
         ok = slot_free();
         if (!ok) break;
-        if (decode_unit(g, a.job, a.nsplit, slots, n, kRows, &S.unit[k % kSched])) {
+        if (decode_unit(g, a.job, a.nsplit, a.least, slots, n, kRows, &S.unit[k % kSched])) {
           __threadfence_block();
           if (lane == 0) mbar_arrive(&S.sched_full[k % kSched]);
           ++k;
@@ -142,90 +141,90 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_drain(&S.claim_bar[last & 1], (last >> 1) & 1, limit);
         if (claimed(&S.claim[last & 1]) >= 0) mbar_wait_drain(&S.claim_bar[(last + 1) & 1], ((last + 1) >> 1) & 1, limit);
       }
-    } else if (warp == 8) {
-      // ---------------- producer ----------------
-      if (lane == 0) {
-        tma_prefetch_desc(&maps.q);
-        tma_prefetch_desc(&maps.k);
-        tma_prefetch_desc(&maps.v);
+    } else if (warp != 9) {
+      // ---------------- producers ----------------
+      const int pw = warp == 8 ? 0 : 1;  // loads half pw of the Q rows, rows 64 pw .. of K and V tiles
+      if (pw == 0 && lane == 0) {
+        tma_prefetch_desc(&maps.kbox);
+        tma_prefetch_desc(&maps.vbox);
       }
       int used = 0, kt = 0;  // units with tiles, ring slots filled
       bool ok = true;
+      Gathers gath;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && !__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+          gath.flush();  // what others wait for before they free this
+          ok = __all_sync(0xffffffffu, bar_wait(bar, parity, limit, abort));
+        }
+        return ok;
+      };
       for (int n = 0;; ++n) {
-        ok = __all_sync(0xffffffffu, bar_wait(&S.sched_full[n % kSched], (n / kSched) & 1, limit, abort));
-        if (!ok || !S.unit[n % kSched].live) break;
+        if (!wait(&S.sched_full[n % kSched], (n / kSched) & 1) || !S.unit[n % kSched].live) break;
         const Unit& u = S.unit[n % kSched];
-        if (u.t1 <= u.t0) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
-          continue;
-        }
-        // Q
-        ok = __all_sync(0xffffffffu, used == 0 || bar_wait(&S.q_empty, (used - 1) & 1, limit, abort));
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&S.q_full, 2 * TB);
-        ++used;
-        __syncwarp();
-        const int rows = u.q.nq * u.hs.n;
+        if (u.t1 > u.t0) {
+          if (used > 0 && !wait(&S.q_empty, (used - 1) & 1)) break;
+          ++used;
+          const int rows = u.q.nq * u.hs.n;
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          int r[4];
+          for (int i = 0; i < 2; ++i) {
+            int r[2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            QRow qr;
-            query_at(g, u.q, a.job.qview, u.hs, imin(u.x0 + h * 128 + lane * 4 + i, rows - 1), qr);
-            r[i] = q_row(g, qr.t, qr.h);
+            for (int y = 0; y < 2; ++y) {
+              QRow qr;
+              query_at(g, u.q, a.job.qview, u.hs, imin(u.x0 + pw * 128 + i * 64 + y * 32 + lane, rows - 1), qr);
+              r[y] = q_row(g, qr.t, qr.h);
+            }
+            gather64<D>(smem_u32(S.q[pw]), i * 64, a.q, r[0], r[1]);
           }
+          gath.add(&S.q_full);
+          for (int t = u.t0; t < u.t1 && ok; ++t) {
+            int seg, j;
+            unit_tile(u, t, seg, j);
+            const int view = a.job.seg[seg].kview, nk = n_keys(u.q, view);
+            if (boxes && view == VIEW_NAT && j * 128 + 128 <= nk) {
+              // consecutive tokens: one TMA box per 64 columns
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_gather4(smem_u32(S.q[h]) + c * 16384 + lane * 512, &maps.q, &S.q_full, c * 64, r[0], r[1],
-                        r[2], r[3]);
-        }
-        // K and V
-        for (int t = u.t0; t < u.t1 && ok; ++t) {
-          int seg, j;
-          unit_tile(u, t, seg, j);
-          const int view = a.job.seg[seg].kview, nk = n_keys(u.q, view);
-          const bool box = boxes && view == VIEW_NAT && j * 128 + 128 <= nk;
-          int pos[4];
-          if (!box) {
+              for (int kv = 0; kv < 2; ++kv, ++kt) {
+                const int s = kt % NS;
+                if (kt >= NS && !wait(&S.kv_empty[s], (kt / NS + 1) & 1)) break;
+                gath.flush();
+                if (lane == 0) {
+                  if (pw == 0) {
+                    mbar_arrive_expect_tx(&S.kv_full[s], TB);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              pos[i] = key_pos(g, u.q, view, imin(j * 128 + lane * 4 + i, nk - 1));
-          }
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++kt) {
-            const int s = kt % NS;
-            ok = __all_sync(0xffffffffu,
-                            kt < NS || bar_wait(&S.kv_empty[s], (kt / NS + 1) & 1, limit, abort));
-            if (!ok) break;
-            const uint32_t dst = smem_u32(S.kv[s]);
-            if (lane == 0) mbar_arrive_expect_tx(&S.kv_full[s], TB);
-            __syncwarp();
-            if (box) {
-              if (lane < D / 64)
-                tma_box(dst + lane * 16384, kv ? &maps.vbox : &maps.kbox, &S.kv_full[s], lane * 64, u.kvh,
-                        u.q.qb + j * 128);
+                    for (int c = 0; c < D / 64; ++c)
+                      tma_box(smem_u32(S.kv[s]) + c * 16384, kv ? &maps.vbox : &maps.kbox, &S.kv_full[s],
+                              c * 64, u.kvh, u.q.qb + j * 128);
+                  } else {
+                    mbar_arrive(&S.kv_full[s]);
+                  }
+                }
+              }
             } else {
-              const Rows& rw = kv ? g.v : g.k;
-              int r[4];
+              int pos[2];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) r[i] = kv_row(g, rw, u.q, pos[i], u.kvh);
+              for (int y = 0; y < 2; ++y)
+                pos[y] = key_pos(g, u.q, view, imin(j * 128 + pw * 64 + y * 32 + lane, nk - 1));
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                tma_gather4(dst + c * 16384 + lane * 512, kv ? &maps.v : &maps.k, &S.kv_full[s], c * 64,
-                            r[0], r[1], r[2], r[3]);
+              for (int kv = 0; kv < 2; ++kv, ++kt) {
+                const int s = kt % NS;
+                const Rows& rw = kv ? g.v : g.k;
+                const int ra = kv_row(g, rw, u.q, pos[0], u.kvh), rb = kv_row(g, rw, u.q, pos[1], u.kvh);
+                if (kt >= NS && !wait(&S.kv_empty[s], (kt / NS + 1) & 1)) break;
+                gather64<D>(smem_u32(S.kv[s]), pw * 64, kv ? a.v : a.k, ra, rb);
+                gath.add(&S.kv_full[s]);
+              }
             }
           }
+          if (!ok) break;
         }
-        if (!ok) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
       }
+      gath.flush();
       if (!ok) {
         if (lane == 0) fail();
         // copies in flight land before the CTA may exit
-        if (used > 0) mbar_wait_drain(&S.q_full, (used - 1) & 1, limit);
         for (int i = imax(0, kt - NS); i < kt; ++i)
           mbar_wait_drain(&S.kv_full[i % NS], (i / NS) & 1, limit);
       }
@@ -442,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (the row is worked out again: kept over the tiles it would cost them registers)
       QRow qr;
       const bool have = query_at(g, su.q, a.job.qview, su.hs, su.x0 + h * 128 + row, qr);
-      const int part = su.part;
+      const int part = su.part, parts = su.parts;
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
       if (any) {
@@ -464,10 +463,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (have) {
-        if (a.mode == OUT_PARTIAL)
+        if (a.mode == OUT_PARTIAL) {
           a.parts.lse[(size_t)(a.part0 + part) * g.total * g.H + rr] = L;
-        else
+          if (part == 0)
+            for (int p = parts; p < a.nsplit; ++p)
+              a.parts.lse[(size_t)(a.part0 + p) * g.total * g.H + rr] = -INFINITY;
+        } else {
           a.lse[rr] = L;
+        }
       }
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
@@ -518,12 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, bool F16>
 cudaError_t launch(const FwdLaunch& a) {
   const Geo& g = a.g;
-  Maps m;
-  if (!make_gather_map(&m.q, a.q, F16, a.q_rows, D) || !make_gather_map(&m.k, a.k, F16, a.k_rows, D) ||
-      !make_gather_map(&m.v, a.v, F16, a.v_rows, D))
-    return cudaErrorInvalidValue;
-  m.kbox = m.k;
-  m.vbox = m.v;
+  Maps m = {};
   const bool boxes = !g.kv_lens;
   if (boxes && (!make_box_map(&m.kbox, a.k, F16, g.total, g.Hkv, g.k.tok, D) ||
                 !make_box_map(&m.vbox, a.v, F16, g.total, g.Hkv, g.v.tok, D)))

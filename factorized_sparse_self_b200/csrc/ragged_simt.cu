@@ -144,8 +144,10 @@ __global__ void __launch_bounds__(NT) ragged_fwd_simt(const __grid_constant__ Fw
     cnt[sg] = j1 - j0[sg];
     total += cnt[sg];
   }
-  const int it1 = (int)((long long)total * (part + 1) / a.nsplit);
-  for (int it = (int)((long long)total * part / a.nsplit); it < it1; ++it) {
+  const int parts = parts_of(total, a.nsplit, a.least);
+  if (part >= parts) return;
+  const int it1 = (int)((long long)total * (part + 1) / parts);
+  for (int it = (int)((long long)total * part / parts); it < it1; ++it) {
     const int sg = it >= cnt[0] ? 1 : 0;
     const int kb = (j0[sg] + it - (sg ? cnt[0] : 0)) * BN;
     const int nk = n_keys(q, a.job.seg[sg].kview);
@@ -217,10 +219,14 @@ __global__ void __launch_bounds__(NT) ragged_fwd_simt(const __grid_constant__ Fw
     scl[row] = wp;
     den[row] = wc;
     if (have) {
-      if (a.mode == OUT_PARTIAL)
+      if (a.mode == OUT_PARTIAL) {
         a.parts.lse[(size_t)(a.part0 + part) * g.total * g.H + rr] = out;
-      else
+        if (part == 0)
+          for (int p = parts; p < a.nsplit; ++p)
+            a.parts.lse[(size_t)(a.part0 + p) * g.total * g.H + rr] = -INFINITY;
+      } else {
         a.lse[rr] = out;
+      }
     }
   }
   __syncthreads();

@@ -1,6 +1,6 @@
-// What the tensor-core kernels for ragged sequences share: row-gather TMA
-// loads, the tensor maps behind them, and the units that a scheduler warp
-// decodes for the other warps of its CTA.
+// What the tensor-core kernels for ragged sequences share: the loads of operand
+// tiles, and the units that a scheduler warp decodes for the other warps of its
+// CTA.
 #pragma once
 
 #include "ragged.h"
@@ -43,19 +43,64 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint64_
   }
 }
 
-// Four rows (64 elements from column c on) of a matrix, to 4 x 128 bytes of
-// shared memory. The destination lies on a 512-byte boundary of a buffer that
-// starts on a 1024-byte boundary, so the 128-byte swizzle, which goes by the
-// address, is that of one tile. Row numbers are always in range.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c,
-                                            int r0, int r1, int r2, int r3) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(r0), "r"(r1), "r"(r2),
-      "r"(r3)
-      : "memory");
+// ---- rows gathered into an operand tile -----------------------------------------
+// A tile is 128 rows of D 16-bit elements as D / 64 blocks of [128][64] with the
+// 128-byte swizzle, 16 KB each. A warp copies 64 of its rows, 16 bytes a lane
+// (asynchronously, past L1): lane i knows the row numbers of rows i and 32 + i.
+// (The TMA's row gather moves 4 rows of 128 bytes in about 100 cycles, whatever
+// issues it: with it chunks of 512 tokens behind up to 32 K keys took 1195 us, with these copies 666.)
+template <int D>
+__device__ __forceinline__ void gather64(uint32_t dst, int row0, const void* base, int ra, int rb) {
+  constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte chunks of a row, rows per instruction
+  const int lane = threadIdx.x & 31;
+  const int chunk = lane % CH, sub = lane / CH;
+  const uint32_t col = dst + (chunk >> 3) * 16384;
+#pragma unroll 8
+  for (int i = 0; i < 64 / RPI; ++i) {
+    const int x = i * RPI + sub;
+    const int r = __shfl_sync(0xffffffffu, i * RPI < 32 ? ra : rb, x & 31);
+    const char* src = static_cast<const char*>(base) + (size_t)r * (D * 2) + chunk * 16;
+    const int y = row0 + x;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(col + y * 128 +
+                                                                  (((chunk & 7) ^ (y & 7)) << 4)),
+                 "l"(src)
+                 : "memory");
+  }
 }
+__device__ __forceinline__ void gather_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void gather_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// A warp's gathers that are under way, oldest first: the barrier of each gets one
+// arrival once its copies have landed and are visible to the tensor cores.
+struct Gathers {
+  uint64_t* bar[3];
+  int n = 0;
+  __device__ __forceinline__ void arrive_oldest() {
+    fence_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar[0]);
+    bar[0] = bar[1];
+    bar[1] = bar[2];
+    --n;
+  }
+  __device__ __forceinline__ void add(uint64_t* b) {
+    gather_commit();
+    if (n == 0) bar[0] = b;
+    else if (n == 1) bar[1] = b;
+    else bar[2] = b;
+    if (++n == 3) {
+      gather_wait<2>();
+      arrive_oldest();
+    }
+  }
+  __device__ __forceinline__ void flush() {
+    if (n == 0) return;
+    gather_wait<0>();
+    while (n) arrive_oldest();
+  }
+};
 
 // 64 columns x 128 consecutive tokens of one head.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c,
@@ -121,10 +166,9 @@ __device__ __forceinline__ int claims_take(Claims& c, uint64_t limit, volatile i
   return got;
 }
 
-// Host: the map of a matrix [rows][d] of 16-bit elements for row gathers, and
-// of token rows [tokens][heads][d] (tok rows of d elements from token to token)
-// for boxes of 128 tokens of one head. False when the driver refuses.
-bool make_gather_map(CUtensorMap* out, const void* base, bool f16, int64_t rows, int d);
+// Host: the map of token rows [tokens][heads][d] of 16-bit elements (tok rows of
+// d elements from token to token) for boxes of 128 tokens of one head. False
+// when the driver refuses.
 bool make_box_map(CUtensorMap* out, const void* base, bool f16, int tokens, int heads, int tok, int d);
 
 // One query-major unit: 2 x 128 rows of one (sequence, key/value head, job),
@@ -134,7 +178,7 @@ struct Unit {
   int32_t live;  // 0: no more units
   Seq q;
   Heads3 hs;
-  int32_t kvh, x0, part;
+  int32_t kvh, x0, part, parts;  // parts: how many its keys are cut into
   int32_t t0, t1;          // key tiles of this unit
   int32_t cnt0;            // of segment 0
   int32_t u0[2];           // first tile of each segment
@@ -152,8 +196,8 @@ __device__ __forceinline__ bool half_meets(const Unit& u, int w, int seg, int j)
 // Decodes unit number n into *out (by a whole warp); false if it has no rows.
 // Slots are taken from the last to the first: a sequence's last tiles have the
 // most keys.
-__device__ __forceinline__ bool decode_unit(const Geo& g, const Job& job, int nsplit, int slots,
-                                            int n, int rows, Unit* out) {
+__device__ __forceinline__ bool decode_unit(const Geo& g, const Job& job, int nsplit, int least,
+                                            int slots, int n, int rows, Unit* out) {
   const int lane = threadIdx.x & 31;
   const int part = n % nsplit, m = n / nsplit;
   const int kvh = m % g.Hkv, slot = slots - 1 - m / g.Hkv;
@@ -176,7 +220,9 @@ __device__ __forceinline__ bool decode_unit(const Geo& g, const Job& job, int ns
     b = j1 > j0 ? imax(j1, o1) : o1;
   }
   const int cnt = b - a;
-  const int cnt1 = __shfl_sync(0xffffffffu, cnt, 1);
+  const int total = __shfl_sync(0xffffffffu, cnt, 0) + __shfl_sync(0xffffffffu, cnt, 1);
+  const int parts = parts_of(total, nsplit, least);
+  if (part >= parts) return false;
   if (lane < 4) {
     out->ja[w][sg] = j0;
     out->jb[w][sg] = j1;
@@ -189,9 +235,9 @@ __device__ __forceinline__ bool decode_unit(const Geo& g, const Job& job, int ns
       out->x0 = x0;
       out->part = part;
       out->cnt0 = cnt;
-      const long long total = cnt + cnt1;
-      out->t0 = (int)(total * part / nsplit);
-      out->t1 = (int)(total * (part + 1) / nsplit);
+      out->parts = parts;
+      out->t0 = (int)((long long)total * part / parts);
+      out->t1 = (int)((long long)total * (part + 1) / parts);
     }
   }
   __syncwarp();

@@ -37,13 +37,6 @@ bool encode(CUtensorMap* out, const void* base, bool f16, int rank, const cuuint
 
 }  // namespace
 
-bool make_gather_map(CUtensorMap* out, const void* base, bool f16, int64_t rows, int d) {
-  const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)d * 2};
-  const cuuint32_t box[2] = {64, 1};
-  return encode(out, base, f16, 2, dims, strides, box);
-}
-
 bool make_box_map(CUtensorMap* out, const void* base, bool f16, int tokens, int heads, int tok, int d) {
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)tok * d * 2};
