@@ -13,8 +13,8 @@
 //            the classes that follow one another, not at both ends of the order
 // and in its order every query row's live keys are ONE interval [lo, hi) whose
 // ends never decrease from row to row. A tile of rows therefore meets the keys from its
-// first row's lo to its last row's hi, and, the other way round, key k meets
-// the rows from the first with hi > k up to the first with lo > k.
+// first row's lo to its last row's hi; the rows that a key meets are an interval
+// of the query order in the same way.
 //
 // Grouped heads: the query heads that share a key/value head and have the same
 // index set form the rows of one unit, row x = e * Gc + g being query e of the
@@ -209,28 +209,35 @@ ST_HD void valid_rows(const Seq& q, int view, int& v0, int& v1) {
   v1 = view == VIEW_NAT ? q.nq : q.nqv;
 }
 
-// Query indexes [a, b) of an order whose live interval holds key k.
-ST_HD void live_queries(const Geo& g, const Seq& q, int view, int rule, int k, int& a, int& b) {
-  int v0, v1;
-  valid_rows(q, view, v0, v1);
-  int x = v0, y = v1;
-  while (x < y) {  // first row with hi > k
-    const int m = (x + y) >> 1;
-    int lo, hi;
-    live_keys(g, q, rule, query_row(g, q, view, m) + q.off, lo, hi);
-    if (hi > k) y = m;
-    else x = m + 1;
+// Query indexes [a, b) whose live interval holds key index k, for a packed
+// sequence (as many queries as keys).
+ST_HD void live_queries(const Geo& g, const Seq& q, int rule, int k, int& a, int& b) {
+  a = k;
+  b = q.nq;
+  switch (rule) {
+    case RULE_CAUSAL:
+      return;
+    case RULE_BAND:
+      b = imin(b - k, g.l + 1) + k;
+      return;
+    case RULE_BLOCK:
+      b = k + imin(b - k, g.l - (k - qdiv(k, g.fl, g.l) * g.l));
+      return;
+    case RULE_STRIDE:
+    case RULE_STRIDE_FAR: {
+      // the rest of the key's class, from the key itself or two rows later
+      const int big = q.rem * (q.P + 1);
+      b = k < big ? (k / (q.P + 1) + 1) * (q.P + 1) : big + ((k - big) / imax(q.P, 1) + 1) * q.P;
+      if (rule == RULE_STRIDE_FAR) a = imin(k + 2, b);
+      return;
+    }
+    default: {
+      const int blk = qdiv(k, g.fc, g.c);  // k counts summary positions
+      if (rule == RULE_SUMMARY) a = blk * g.l + (g.l - g.c) + (k - blk * g.c);
+      else a = imin(blk, q.P) * g.l + imin(g.l, q.nq - imin(blk, q.P) * g.l);
+      return;
+    }
   }
-  a = x;
-  y = v1;
-  while (x < y) {  // first row with lo > k
-    const int m = (x + y) >> 1;
-    int lo, hi;
-    live_keys(g, q, rule, query_row(g, q, view, m) + q.off, lo, hi);
-    if (lo > k) y = m;
-    else x = m + 1;
-  }
-  b = x;
 }
 
 // Query heads of a group that belong to a job: head = first + step * g.

@@ -91,6 +91,10 @@ __device__ __forceinline__ bool dkv_direct(const BwdLaunch& a, int kvh) {
 // Tensor-core forward: bf16 / fp16, d = 64 or 128.
 cudaError_t tc_ragged_fwd(const FwdLaunch& a, int dtype);
 
+// Tensor-core backward of packed sequences: dQ of one query order, and dK, dV.
+cudaError_t tc_ragged_dq(const BwdLaunch& a, const Job& job, int mode, int dtype);
+cudaError_t tc_ragged_dkv(const BwdLaunch& a, int dtype);
+
 // Few query rows per key/value head over a paged cache (decoding steps): bf16 /
 // fp16, d = 64 or 128.
 cudaError_t few_rows_fwd(const FwdLaunch& a, int dtype);

@@ -371,13 +371,14 @@ st_status st_packed_attn_bwd(const st_pattern_desc* p, st_dtype dtype, const st_
   a.wait_ns = wait_limit_ns();
   a.stream = cs;
   cudaError_t e = row_delta(g, dtype, o, dout, delta, cs);
-  if (e == cudaSuccess) e = simt_ragged_dkv(a, dtype);
+  if (e == cudaSuccess) e = dtype == ST_F32 ? simt_ragged_dkv(a, dtype) : tc_ragged_dkv(a, dtype);
   if (e == cudaSuccess && b.parts) e = join_dkv(a, dtype);
   Job jobs[2];
   const int n = make_jobs(*p, jobs);
-  for (int j = 0; j < n && e == cudaSuccess; ++j)
-    e = simt_ragged_dq(a, jobs[j],
-                       two_orders(*p) ? (j == 0 ? OUT_PARTIAL : OUT_MERGE) : OUT_FINAL, dtype);
+  for (int j = 0; j < n && e == cudaSuccess; ++j) {
+    const int mode = two_orders(*p) ? (j == 0 ? OUT_PARTIAL : OUT_MERGE) : OUT_FINAL;
+    e = dtype == ST_F32 ? simt_ragged_dq(a, jobs[j], mode, dtype) : tc_ragged_dq(a, jobs[j], mode, dtype);
+  }
   return e == cudaSuccess ? ST_OK : ST_ERR_CUDA;
 }
 

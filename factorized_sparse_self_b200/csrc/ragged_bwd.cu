@@ -1,0 +1,732 @@
+// Backward of attention over packed ragged sequences on the tensor cores (bf16,
+// fp16; d = 64, 128): two kernels of one build.
+//
+// dS = P (dP - D) with P = exp(s - LSE) formed again, dP = dO V^T, D = dO . O.
+//   query-major (dQ):    resident Q, dO of 128 query rows; K, V tiles pass by:
+//                        S = Q K^T, dP = dO V^T, dQ += dS K
+//   key-major (dK, dV):  resident K, V of 128 keys; Q, dO tiles pass by:
+//                        S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q
+// That is seven products where a single kernel needs five, but every gradient
+// row is summed in TMEM by one CTA: no fp32 accumulators in memory, no atomics,
+// and the results are the same in every run. Rows of a unit are (query, head of
+// the group) pairs, so dK and dV of grouped heads are sums over more rows.
+//
+// One CTA per SM (384 threads), units claimed from the grid. Warps 0..7 are two
+// warpgroups that share the 128 rows and take 64 columns each of a 128 x 128
+// tile (thread = row = TMEM lane); P and dS go back to TMEM as 16-bit pairs over
+// the scores they came from and are read from there as the A operand, so they
+// never pass through shared memory. Warp 9 issues the products, warps 8 and 11
+// load rows, warp 10 decodes units.
+// TMEM query-major: S (two buffers, so that S of the next tile is there when a
+// tile's dS is done) 0, 128, dP 256, dQ 384. Key-major: S^T 0, dP^T 128,
+// dV 256, dK 256 + d.
+#include "ragged_tc.cuh"
+
+namespace st {
+namespace rag {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kSched = 2;
+constexpr uint32_t kRegsCompute = 208, kRegsIssue = 88;  // 168 at launch: 2 * 208 + 88 = 3 * 168
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kStages = D == 64 ? 8 : 5;
+};
+
+// 128 rows of one (sequence, key/value head): query rows or keys.
+struct BUnit {
+  int32_t live;
+  Seq q;
+  Heads3 hs;
+  int32_t kvh, job, split;
+  int32_t r0;      // first row (query-major: of the unit's rows; key-major: key index)
+  int32_t t0, t1;  // tiles of the other side
+  int32_t cnt0;    // query-major: tiles of segment 0
+  int32_t u0[2];   // query-major: first tile of each segment
+};
+
+template <int D>
+struct alignas(1024) Smem {
+  uint8_t res[2][Cfg<D>::kTileBytes];  // Q, dO or K, V
+  uint8_t ring[Cfg<D>::kStages][Cfg<D>::kTileBytes];
+  float nlse[2][128], ndel[2][128];    // key-major: -LSE log2(e) and -D of a tile's query rows
+  uint64_t r_full, r_empty;
+  uint64_t full[Cfg<D>::kStages], empty[Cfg<D>::kStages];
+  uint64_t s_full[2], dp_full, p_ready, ds_ready, acc_full;
+  uint64_t row_full[2], row_empty[2];
+  uint64_t sched_full[kSched], sched_empty[kSched];
+  uint64_t fin;
+  alignas(16) uint4 claim[2];
+  uint64_t claim_bar[2];
+  BUnit unit[kSched];
+  uint32_t tmem;
+  int abort;
+};
+
+struct Maps {
+  CUtensorMap k, v;
+};
+
+// Query-major unit n of job a.job[0] (all segments), or key-major unit n.
+template <bool DKV>
+__device__ __forceinline__ bool decode(const BwdLaunch& a, const Job& qjob, int slots, int n, BUnit* out) {
+  const Geo& g = a.g;
+  const int lane = threadIdx.x & 31;
+  int split = 0, jb = 0, m = n;
+  if constexpr (DKV) {
+    split = m % a.nsplit;
+    m /= a.nsplit;
+    jb = m % a.njobs;
+    m /= a.njobs;
+  }
+  const Job& job = DKV ? a.job[jb] : qjob;
+  const int kvh = m % g.Hkv;
+  // query-major: a sequence's last rows see the most keys; key-major: its first
+  // keys are seen by the most rows
+  const int slot = DKV ? m / g.Hkv : slots - 1 - m / g.Hkv;
+  int tile;
+  const int s = find_slot(g, DKV ? 1 : most_heads(g, job.hc), 128, slot, tile);
+  const Seq q = load_seq(g, s);
+  const Heads3 hs = heads_of_group(g, job.hc, kvh);
+  const int r0 = tile * 128;
+  if (hs.n == 0) return false;
+  int t0, t1, cnt0 = 0, u0[2] = {0, 0};
+  if constexpr (DKV) {
+    const int nk = n_keys(q, job.seg[0].kview);
+    if (r0 >= nk) return false;
+    int x0, x1, y;
+    live_queries(g, q, job.seg[0].rule, r0, x0, y);
+    live_queries(g, q, job.seg[0].rule, imin(r0 + 128, nk) - 1, y, x1);
+    t0 = x0 * hs.n / 128;
+    t1 = x1 > x0 ? (x1 * hs.n + 127) / 128 : t0;
+    const int c = t1 - t0;
+    t1 = t0 + (int)((long long)c * (split + 1) / a.nsplit);
+    t0 = t0 + (int)((long long)c * split / a.nsplit);
+  } else {
+    if (r0 >= q.nq * hs.n) return false;
+    int e0, e1, c1 = 0;
+    tile_range(g, q, job, 0, hs, r0, 128, 128, e0, e1);
+    u0[0] = e0;
+    cnt0 = e1 - e0;
+    if (job.nseg > 1) {
+      tile_range(g, q, job, 1, hs, r0, 128, 128, e0, e1);
+      u0[1] = e0;
+      c1 = e1 - e0;
+    }
+    t0 = 0;
+    t1 = cnt0 + c1;
+  }
+  if (lane == 0) {
+    out->live = 1;
+    out->q = q;
+    out->hs = hs;
+    out->kvh = kvh;
+    out->job = jb;
+    out->split = split;
+    out->r0 = r0;
+    out->t0 = t0;
+    out->t1 = t1;
+    out->cnt0 = cnt0;
+    out->u0[0] = u0[0];
+    out->u0[1] = u0[1];
+  }
+  __syncwarp();
+  return true;
+}
+
+template <int D, bool F16, bool DKV>
+__global__ void __launch_bounds__(kThreads, 1)
+    ragged_bwd_tc(const __grid_constant__ BwdLaunch a, const __grid_constant__ Job qjob,
+                  const __grid_constant__ Maps maps, int slots, int mode) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  Smem<D>& S = *reinterpret_cast<Smem<D>*>(raw);
+  constexpr int NS = Cfg<D>::kStages, TB = Cfg<D>::kTileBytes;
+  constexpr uint32_t kDP = DKV ? 128 : 256, kDQ = 384, kDV = 256, kDK = 256 + D;
+  const Geo& g = a.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t limit = a.wait_ns;
+  volatile int* abort = &S.abort;
+  if (smem_u32(raw) & 1023) {  // operand tiles need it; without static shared memory it holds
+    if (threadIdx.x == 0) set_status(g.status, ST_ERR_UNSUPPORTED);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    S.abort = 0;
+    mbar_init(&S.r_full, 2);  // both producers
+    mbar_init(&S.r_empty, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&S.full[i], 2);
+      mbar_init(&S.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.row_full[i], 2);
+      mbar_init(&S.row_empty[i], 8);
+      mbar_init(&S.claim_bar[i], 1);
+    }
+    mbar_init(&S.dp_full, 1);
+    mbar_init(&S.p_ready, 256);
+    mbar_init(&S.ds_ready, 256);
+    mbar_init(&S.acc_full, 1);
+    for (int i = 0; i < kSched; ++i) {
+      mbar_init(&S.sched_full[i], 1);
+      mbar_init(&S.sched_empty[i], 11);  // two producers, MMA, eight compute warps
+    }
+    mbar_init(&S.fin, 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&S.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem;
+  auto fail = [&]() {
+    S.abort = 1;
+    set_status(g.status, ST_ERR_DEVICE_TIMEOUT);
+  };
+
+  if (warp >= 8) {
+    regs_decrease<kRegsIssue>();
+    if (warp == 10) {
+      // ---------------- scheduler ----------------
+      int k = 0;
+      bool ok = true;
+      auto slot_free = [&]() {
+        return k < kSched || __all_sync(0xffffffffu, bar_wait(&S.sched_empty[k % kSched],
+                                                              (k / kSched + 1) & 1, limit, abort));
+      };
+      Claims claims = {S.claim, S.claim_bar, 0};
+      if (lane == 0) claims_issue(claims, 0);
+      for (int n = blockIdx.x; n >= 0;) {
+        ok = slot_free();
+        if (!ok) break;
+        if (decode<DKV>(a, qjob, slots, n, &S.unit[k % kSched])) {
+          __threadfence_block();
+          if (lane == 0) mbar_arrive(&S.sched_full[k % kSched]);
+          ++k;
+        }
+        n = claims_take(claims, limit, abort);
+        ok = n != -2;
+      }
+      if (ok) ok = slot_free();
+      if (ok && lane == 0) {
+        S.unit[k % kSched].live = 0;
+        __threadfence_block();
+        mbar_arrive(&S.sched_full[k % kSched]);
+      }
+      if (!ok) {
+        if (lane == 0) fail();
+        // a claim in flight lands before the CTA may exit
+        const int last = claims.n > 0 ? claims.n - 1 : 0;
+        mbar_wait_drain(&S.claim_bar[last & 1], (last >> 1) & 1, limit);
+        if (claimed(&S.claim[last & 1]) >= 0)
+          mbar_wait_drain(&S.claim_bar[(last + 1) & 1], ((last + 1) >> 1) & 1, limit);
+      }
+    } else if (warp != 9) {
+      // ---------------- producers ----------------
+      const int pw = warp == 8 ? 0 : 1;  // rows 64 pw .. of every tile
+      int used = 0, kt = 0, tt = 0;      // units with tiles, ring slots filled, tiles
+      bool ok = true;
+      Gathers gath;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && !__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+          gath.flush();  // what others wait for before they free this
+          ok = __all_sync(0xffffffffu, bar_wait(bar, parity, limit, abort));
+        }
+        return ok;
+      };
+      for (int n = 0;; ++n) {
+        if (!wait(&S.sched_full[n % kSched], (n / kSched) & 1) || !S.unit[n % kSched].live) break;
+        const BUnit& u = S.unit[n % kSched];
+        if (u.t1 > u.t0) {
+          const Job& job = DKV ? a.job[u.job] : qjob;
+          const int xrows = u.q.nq * u.hs.n;
+          // row numbers of Q (in q) and dO (contiguous) of query row x
+          auto query_rows = [&](int x, int& rq, int& ro) {
+            QRow qr;
+            query_at(g, u.q, job.qview, u.hs, imin(x, xrows - 1), qr);
+            rq = q_row(g, qr.t, qr.h);
+            ro = qr.t * g.H + qr.h;
+          };
+          auto key_rows = [&](int view, int e, int& rk, int& rv) {
+            const int pos = key_pos(g, u.q, view, imin(e, n_keys(u.q, view) - 1));
+            rk = kv_row(g, g.k, u.q, pos, u.kvh);
+            rv = kv_row(g, g.v, u.q, pos, u.kvh);
+          };
+          if (used > 0 && !wait(&S.r_empty, (used - 1) & 1)) break;
+          ++used;
+          {
+            int ra[2], rb[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int e = u.r0 + pw * 64 + y * 32 + lane;
+              if (DKV) key_rows(job.seg[0].kview, e, ra[y], rb[y]);
+              else query_rows(e, ra[y], rb[y]);
+            }
+            gather64<D>(smem_u32(S.res[0]), pw * 64, DKV ? a.k : a.q, ra[0], ra[1]);
+            gather64<D>(smem_u32(S.res[1]), pw * 64, DKV ? a.v : a.dout, rb[0], rb[1]);
+            gath.add(&S.r_full);
+          }
+          for (int t = u.t0; t < u.t1; ++t, ++tt) {
+            int view = 0, j = t, seg = 0;
+            bool box = false;
+            if (!DKV) {
+              seg = t >= u.cnt0 ? 1 : 0;
+              j = u.u0[seg] + t - (seg ? u.cnt0 : 0);
+              view = job.seg[seg].kview;
+              box = view == VIEW_NAT && j * 128 + 128 <= u.q.nk;
+            }
+            if (box) {
+              // consecutive tokens: one TMA box per 64 columns
+#pragma unroll
+              for (int kv = 0; kv < 2; ++kv, ++kt) {
+                const int s = kt % NS;
+                if (kt >= NS && !wait(&S.empty[s], (kt / NS + 1) & 1)) break;
+                gath.flush();
+                if (lane == 0) {
+                  if (pw == 0) {
+                    mbar_arrive_expect_tx(&S.full[s], TB);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                      tma_box(smem_u32(S.ring[s]) + c * 16384, kv ? &maps.v : &maps.k, &S.full[s], c * 64,
+                              u.kvh, u.q.qb + j * 128);
+                  } else {
+                    mbar_arrive(&S.full[s]);
+                  }
+                }
+              }
+              if (!ok) break;
+              continue;
+            }
+            int ra[2], rb[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int e = j * 128 + pw * 64 + y * 32 + lane;
+              if (DKV) query_rows(e, ra[y], rb[y]);
+              else key_rows(view, e, ra[y], rb[y]);
+            }
+            float val[4];
+            if (DKV) {
+              // -LSE log2(e) (producer 0) or -D (producer 1) of the tile's rows;
+              // rows with an empty set have no live entry and get 0
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                int rq, ro;
+                query_rows(j * 128 + y * 32 + lane, rq, ro);
+                const float f = __ldg((pw ? a.delta : a.lse) + ro);
+                val[y] = pw ? -f : f == -INFINITY ? 0.f : -f * kLog2e;
+              }
+            }
+            {
+              const int s = kt % NS;
+              if (kt >= NS && !wait(&S.empty[s], (kt / NS + 1) & 1)) break;
+              gather64<D>(smem_u32(S.ring[s]), pw * 64, DKV ? a.q : a.k, ra[0], ra[1]);
+              gath.add(&S.full[s]);
+              ++kt;
+            }
+            if (DKV) {
+              const int b = tt & 1;
+              if (tt >= 2 && !wait(&S.row_empty[b], (tt / 2 + 1) & 1)) break;
+              float* dst = pw ? S.ndel[b] : S.nlse[b];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) dst[y * 32 + lane] = val[y];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&S.row_full[b]);
+            }
+            {
+              const int s = kt % NS;
+              if (kt >= NS && !wait(&S.empty[s], (kt / NS + 1) & 1)) break;
+              gather64<D>(smem_u32(S.ring[s]), pw * 64, DKV ? a.dout : a.v, rb[0], rb[1]);
+              gath.add(&S.full[s]);
+              ++kt;
+            }
+          }
+          if (!ok) break;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
+      }
+      gath.flush();
+      if (!ok) {
+        if (lane == 0) fail();
+        // copies in flight land before the CTA may exit
+        for (int i = imax(0, kt - NS); i < kt; ++i) mbar_wait_drain(&S.full[i % NS], (i / NS) & 1, limit);
+      }
+    } else {
+      // ---------------- MMA issuer ----------------
+      const uint32_t idS = idesc_16(128, 128, false, false, F16);
+      const uint32_t idA = idesc_16(128, D, false, true, F16);
+      // A lane's failed wait is remembered and agreed on at the end of the unit:
+      // until then the warp goes on (later waits of that lane return at once).
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok) ok = bar_wait(bar, parity, limit, abort);
+        __syncwarp();
+      };
+      const uint64_t a1 = sdesc(smem_u32(S.res[0]), 16, 1024), a2 = sdesc(smem_u32(S.res[1]), 16, 1024);
+      const uint64_t bk = sdesc(smem_u32(S.ring[0]), 16, 1024), bm = sdesc(smem_u32(S.ring[0]), 16384, 1024);
+      int kt = 0, used = 0;  // ring slots of finished units, units with tiles
+      uint32_t ts = 0;       // tiles so far
+      // ring slot i of the unit
+      auto slot = [&](int i) { return (kt + i) % NS; };
+      auto wait_slot = [&](int i) { wait(&S.full[slot(i)], ((kt + i) / NS) & 1); };
+      // scores: resident tile (ad) times ring slot i, transposed operands K-major
+      auto scores = [&](uint64_t ad, int i, uint32_t col, uint64_t* bar) {
+        const uint64_t bd = sdesc_at(bk, slot(i) * TB);
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x)
+            mma_ss(tmem + col, sdesc_at(ad, (x & 3) * 32 + (x >> 2) * 16384),
+                   sdesc_at(bd, (x & 3) * 32 + (x >> 2) * 16384), idS, x > 0);
+          mma_commit(bar);
+        }
+        __syncwarp();
+      };
+      // accumulator (col) += weights (16-bit, 64 keys or rows at columns w and w + 64) times
+      // ring slot i, which is let go
+      auto weigh = [&](uint32_t w, int i, uint32_t col, bool fresh, uint64_t* more) {
+        const uint64_t bd = sdesc_at(bm, slot(i) * TB);
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            mma_ts(tmem + col, tmem + w + (x & 3) * 8 + (x >> 2) * 64, sdesc_at(bd, x * 2048), idA,
+                   !fresh || x > 0);
+          mma_commit(&S.empty[slot(i)]);
+          if (more) mma_commit(more);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) mma_commit(bar);
+        __syncwarp();
+      };
+      for (int n = 0;; ++n) {
+        wait(&S.sched_full[n % kSched], (n / kSched) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const BUnit& u = S.unit[n % kSched];
+        if (!u.live) break;
+        const int T = u.t1 - u.t0;
+        if (T > 0) {
+          wait(&S.r_full, used & 1);
+          ++used;
+          if constexpr (!DKV) {
+            // ring: K0 V0 K1 V1 ...
+            wait_slot(0);
+            scores(a1, 0, (ts & 1) * 128, &S.s_full[ts & 1]);
+            wait_slot(1);
+            scores(a2, 1, kDP, &S.dp_full);
+            commit(&S.empty[slot(1)]);
+            if (T > 1) {
+              wait_slot(2);
+              scores(a1, 2, ((ts + 1) & 1) * 128, &S.s_full[(ts + 1) & 1]);
+            } else {
+              commit(&S.r_empty);
+            }
+            for (int t = 0; t < T; ++t, ++ts) {
+              if (t + 1 < T) wait_slot(2 * t + 3);
+              wait(&S.ds_ready, ts & 1);
+              if (t + 1 < T) {
+                scores(a2, 2 * t + 3, kDP, &S.dp_full);
+                commit(&S.empty[slot(2 * t + 3)]);
+                if (t + 2 == T) commit(&S.r_empty);
+              }
+              weigh((ts & 1) * 128, 2 * t, kDQ, t == 0, t + 1 == T ? &S.acc_full : nullptr);
+              if (t + 2 < T) {
+                wait_slot(2 * t + 4);
+                scores(a1, 2 * t + 4, (ts & 1) * 128, &S.s_full[ts & 1]);
+              }
+            }
+          } else {
+            // ring: Q0 dO0 Q1 dO1 ...
+            wait_slot(0);
+            scores(a1, 0, 0, &S.s_full[0]);
+            wait_slot(1);
+            scores(a2, 1, kDP, &S.dp_full);
+            if (T == 1) commit(&S.r_empty);
+            for (int t = 0; t < T; ++t, ++ts) {
+              if (t + 1 < T) wait_slot(2 * t + 2);
+              wait(&S.p_ready, ts & 1);
+              weigh(0, 2 * t + 1, kDV, t == 0, nullptr);
+              if (t + 1 < T) {
+                scores(a1, 2 * t + 2, 0, &S.s_full[0]);
+                wait_slot(2 * t + 3);
+              }
+              wait(&S.ds_ready, ts & 1);
+              weigh(kDP, 2 * t, kDK, t == 0, t + 1 == T ? &S.acc_full : nullptr);
+              if (t + 1 < T) {
+                scores(a2, 2 * t + 3, kDP, &S.dp_full);
+                if (t + 2 == T) commit(&S.r_empty);
+              }
+            }
+          }
+          kt += 2 * T;
+        }
+        if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
+        __syncwarp();
+      }
+      if (!ok && lane == 0) fail();
+      commit(&S.fin);
+      if (!mbar_wait_drain(&S.fin, 0, limit) && lane == 0) fail();
+      __syncwarp();
+    }
+  } else {
+    regs_increase<kRegsCompute>();
+    // ---------------- compute ----------------
+    const int w = warp >> 2;  // columns 64 w .. 64 w + 63 of every tile
+    const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
+    const int row = (warp & 3) * 32 + lane;
+    const float sc2 = a.scale * kLog2e;
+    bool ok = true;
+    uint32_t ts = 0, us = 0;  // tiles, units with tiles so far
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, bar_wait(bar, parity, limit, abort));
+      return ok;
+    };
+    for (int n = 0;; ++n) {
+      if (!wait(&S.sched_full[n % kSched], (n / kSched) & 1)) break;
+      const BUnit& u = S.unit[n % kSched];
+      if (!u.live) break;
+      const Job& job = DKV ? a.job[u.job] : qjob;
+      const int t0 = u.t0, t1 = u.t1;
+      // live columns of this thread's row, in the unit's tile numbering
+      int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0;
+      float nl = 0.f, nd = 0.f;  // query-major: -LSE log2(e), -D
+      if constexpr (DKV) {
+        if (u.r0 + row < n_keys(u.q, job.seg[0].kview)) {
+          live_queries(g, u.q, job.seg[0].rule, u.r0 + row, lo0, hi0);
+          lo0 *= u.hs.n;
+          hi0 *= u.hs.n;
+        }
+      } else {
+        QRow qr;
+        if (query_at(g, u.q, qjob.qview, u.hs, u.r0 + row, qr)) {
+          live_keys(g, u.q, qjob.seg[0].rule, qr.pos, lo0, hi0);
+          if (qjob.nseg > 1) live_keys(g, u.q, qjob.seg[1].rule, qr.pos, lo1, hi1);
+          const size_t rr = (size_t)qr.t * g.H + qr.h;
+          const float f = a.lse[rr];
+          nl = f == -INFINITY ? 0.f : -f * kLog2e;
+          nd = -a.delta[rr];
+        }
+        lo0 -= u.u0[0] * 128;
+        hi0 -= u.u0[0] * 128;
+        lo1 -= (u.u0[1] - u.cnt0) * 128;
+        hi1 -= (u.u0[1] - u.cnt0) * 128;
+      }
+      const int tsplit = DKV ? t1 : u.cnt0;
+      for (int t = t0; t < t1; ++t, ++ts) {
+        const int buf = DKV ? 0 : (int)(ts & 1);
+        const uint32_t tS = tmem + tl + (DKV ? 0 : buf * 128) + w * 64;
+        const uint32_t tP = tmem + tl + kDP + w * 64;
+        if (!wait(&S.s_full[buf], DKV ? (ts & 1) : ((ts >> 1) & 1))) break;
+        tc_fence_after();
+        float p[64];
+        tmem_ld32(tS, reinterpret_cast<uint32_t*>(p));
+        tmem_ld32(tS + 32, reinterpret_cast<uint32_t*>(p) + 32);
+        tmem_wait_ld();
+        const int kl = (t >= tsplit ? lo1 : lo0) - t * 128 - w * 64;
+        const int kh = (t >= tsplit ? hi1 : hi0) - t * 128 - w * 64;
+        if (!__all_sync(0xffffffffu, kl <= 0 && kh >= 64)) mask_cols<2>(p, 0, kl, kh);
+        if constexpr (DKV) {
+          if (!wait(&S.row_full[ts & 1], (ts >> 1) & 1)) break;
+          const float4* L = reinterpret_cast<const float4*>(S.nlse[ts & 1] + w * 64);
+#pragma unroll
+          for (int x = 0; x < 64; x += 4) {
+            const float4 f = L[x / 4];
+            ffma2(p[x], p[x + 1], p[x], p[x + 1], sc2, sc2, f.x, f.y);
+            ffma2(p[x + 2], p[x + 3], p[x + 2], p[x + 3], sc2, sc2, f.z, f.w);
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 64; x += 2) ffma2(p[x], p[x + 1], p[x], p[x + 1], sc2, sc2, nl, nl);
+        }
+#pragma unroll
+        for (int x = 0; x < 64; ++x) p[x] = fast_exp2(p[x]);
+        if constexpr (DKV) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int x = 0; x < 32; ++x) pk[x] = pack2<F16>(p[2 * x], p[2 * x + 1]);
+          tmem_st32(tS, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&S.p_ready);
+        }
+        if (!wait(&S.dp_full, ts & 1)) break;
+        tc_fence_after();
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float dp[32];
+          tmem_ld32(tP + c * 32, reinterpret_cast<uint32_t*>(dp));
+          tmem_wait_ld();
+          if constexpr (DKV) {
+            const float4* Dl = reinterpret_cast<const float4*>(S.ndel[ts & 1] + w * 64 + c * 32);
+#pragma unroll
+            for (int x = 0; x < 32; x += 4) {
+              const float4 f = Dl[x / 4];
+              float* y = p + c * 32 + x;
+              fadd2(dp[x], dp[x + 1], dp[x], dp[x + 1], f.x, f.y);
+              fadd2(dp[x + 2], dp[x + 3], dp[x + 2], dp[x + 3], f.z, f.w);
+              fmul2(y[0], y[1], y[0], y[1], dp[x], dp[x + 1]);
+              fmul2(y[2], y[3], y[2], y[3], dp[x + 2], dp[x + 3]);
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              float* y = p + c * 32 + x;
+              fadd2(dp[x], dp[x + 1], dp[x], dp[x + 1], nd, nd);
+              fmul2(y[0], y[1], y[0], y[1], dp[x], dp[x + 1]);
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < 16; ++x) pk[c * 16 + x] = pack2<F16>(p[c * 32 + 2 * x], p[c * 32 + 2 * x + 1]);
+        }
+        if (DKV) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.row_empty[ts & 1]);
+        }
+        tmem_st32(DKV ? tP : tS, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&S.ds_ready);
+      }
+      if (!ok) break;
+      // ---- the unit's rows ----
+      if constexpr (!DKV) {
+        QRow qr;
+        const bool have = query_at(g, u.q, qjob.qview, u.hs, u.r0 + row, qr);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
+        if (t1 > t0) {
+          if (!wait(&S.acc_full, us & 1)) break;
+          ++us;
+          tc_fence_after();
+        }
+#pragma unroll 1
+        for (int c = w * (D / 2); c < (w + 1) * (D / 2); c += 32) {
+          float o[32];
+          if (t1 > t0) {
+            tmem_ld32(tmem + tl + kDQ + c, reinterpret_cast<uint32_t*>(o));
+            tmem_wait_ld();
+          }
+          if (!have) continue;
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = t1 > t0 ? o[x] * a.scale : 0.f;
+          float4* part = reinterpret_cast<float4*>(a.dq_part + ((size_t)qr.t * g.H + qr.h) * D + c);
+          if (mode == OUT_PARTIAL) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) part[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            continue;
+          }
+          if (mode == OUT_MERGE) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const float4 f = part[x];
+              o[4 * x] += f.x;
+              o[4 * x + 1] += f.y;
+              o[4 * x + 2] += f.z;
+              o[4 * x + 3] += f.w;
+            }
+          }
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dq) +
+                                                ((size_t)qr.t * a.dq_rows.tok + qr.h * a.dq_rows.head) * D + c);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            dst[x] = make_uint4(pack2<F16>(o[8 * x], o[8 * x + 1]), pack2<F16>(o[8 * x + 2], o[8 * x + 3]),
+                                pack2<F16>(o[8 * x + 4], o[8 * x + 5]), pack2<F16>(o[8 * x + 6], o[8 * x + 7]));
+        }
+        tc_fence_before();
+      } else {
+        const int view = job.seg[0].kview, kvh = u.kvh;
+        const bool have = u.r0 + row < n_keys(u.q, view);
+        const int tok = have ? u.q.qb + key_pos(g, u.q, view, u.r0 + row) : 0;
+        const bool direct = dkv_direct(a, kvh);
+        const int part = u.job * a.nsplit + u.split;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
+        if (t1 > t0) {
+          if (!wait(&S.acc_full, us & 1)) break;
+          ++us;
+          tc_fence_after();
+        }
+        // warpgroup 0 writes dK, warpgroup 1 dV
+        uint16_t* out = w ? static_cast<uint16_t*>(a.dv) + ((size_t)tok * a.dv_rows.tok + kvh * a.dv_rows.head) * D
+                          : static_cast<uint16_t*>(a.dk) + ((size_t)tok * a.dk_rows.tok + kvh * a.dk_rows.head) * D;
+        const float f = w ? 1.f : a.scale;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          if (t1 > t0) {
+            tmem_ld32(tmem + tl + (w ? kDV : kDK) + c, reinterpret_cast<uint32_t*>(o));
+            tmem_wait_ld();
+          }
+          if (!have) continue;
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = t1 > t0 ? o[x] * f : 0.f;
+          if (direct) {
+            uint4* dst = reinterpret_cast<uint4*>(out + c);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              dst[x] = make_uint4(pack2<F16>(o[8 * x], o[8 * x + 1]), pack2<F16>(o[8 * x + 2], o[8 * x + 3]),
+                                  pack2<F16>(o[8 * x + 4], o[8 * x + 5]), pack2<F16>(o[8 * x + 6], o[8 * x + 7]));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(
+                a.parts + (((size_t)part * g.total + tok) * g.Hkv + kvh) * 2 * D + w * D + c);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          }
+        }
+        tc_fence_before();
+      }
+    }
+    if (!ok) fail();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool F16, bool DKV>
+cudaError_t launch(const BwdLaunch& a, const Job& job, int mode) {
+  const Geo& g = a.g;
+  Maps m = {};
+  if (!DKV && (!make_box_map(&m.k, a.k, F16, g.total, g.Hkv, g.k.tok, D) ||
+               !make_box_map(&m.v, a.v, F16, g.total, g.Hkv, g.v.tok, D)))
+    return cudaErrorInvalidValue;
+  const size_t smem = sizeof(Smem<D>);
+  static_assert(sizeof(Smem<D>) <= 232448, "shared memory");
+  cudaError_t e = cudaFuncSetAttribute(ragged_bwd_tc<D, F16, DKV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  const long long slots = slot_count(g, DKV ? 1 : most_heads(g, job.hc), 128);
+  const long long units = slots * g.Hkv * (DKV ? a.njobs * a.nsplit : 1);
+  if (units > 0x7fffffff) return cudaErrorInvalidValue;
+  ragged_bwd_tc<D, F16, DKV><<<(unsigned)units, kThreads, smem, a.stream>>>(a, job, m, (int)slots, mode);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t tc_ragged_dq(const BwdLaunch& a, const Job& job, int mode, int dtype) {
+  if (a.g.d == 64)
+    return dtype == ST_F16 ? launch<64, true, false>(a, job, mode) : launch<64, false, false>(a, job, mode);
+  return dtype == ST_F16 ? launch<128, true, false>(a, job, mode) : launch<128, false, false>(a, job, mode);
+}
+
+cudaError_t tc_ragged_dkv(const BwdLaunch& a, int dtype) {
+  const Job& none = a.job[0];
+  if (a.g.d == 64) return dtype == ST_F16 ? launch<64, true, true>(a, none, 0) : launch<64, false, true>(a, none, 0);
+  return dtype == ST_F16 ? launch<128, true, true>(a, none, 0) : launch<128, false, true>(a, none, 0);
+}
+
+}  // namespace rag
+}  // namespace st

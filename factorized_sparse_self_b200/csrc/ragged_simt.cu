@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(NT) ragged_dkv_simt(const __grid_constant__ Bw
   });
   if (tid < BM) {
     int x = 0, y = 0;
-    if (k0 + tid < nk) live_queries(g, q, job.qview, rule, k0 + tid, x, y);
+    if (k0 + tid < nk) live_queries(g, q, rule, k0 + tid, x, y);
     sa[tid] = x * hs.n;
     sb[tid] = y * hs.n;
     if (tid == 0) lim[0] = x * hs.n;
