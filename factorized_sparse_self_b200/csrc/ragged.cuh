@@ -68,6 +68,7 @@ struct Geo {
   int32_t H, Hkv, G, d;
   int32_t l, c, split;    // split: even / odd heads have different sets
   FastDiv fl, fc;
+  FastDiv fheads[3];      // division by G, (G + 1) / 2, G / 2
   const int32_t* cu;      // [S + 1] first token row of every sequence
   // paged cache (null kv_lens: packed, keys are the sequence's own rows)
   const int32_t* kv_lens; // [S]
@@ -243,17 +244,20 @@ ST_HD void live_queries(const Geo& g, const Seq& q, int rule, int k, int& a, int
 // Query heads of a group that belong to a job: head = first + step * g.
 struct Heads3 {
   int32_t first, step, n;
+  FastDiv f;  // division by n
 };
 ST_HD Heads3 heads_of_group(const Geo& g, int hc, int kvh) {
   Heads3 h;
   h.first = kvh * g.G;
   h.step = 1;
   h.n = g.G;
+  h.f = g.fheads[0];
   if (hc >= 0) {
     h.first += (hc ^ h.first) & 1;
     h.step = 2;
     const int end = kvh * g.G + g.G;
     h.n = h.first < end ? (end - h.first + 1) / 2 : 0;
+    h.f = 2 * h.n > g.G ? g.fheads[1] : g.fheads[2];
   }
   return h;
 }
@@ -323,7 +327,7 @@ struct QRow {
 __device__ __forceinline__ bool query_at(const Geo& g, const Seq& q, int view, const Heads3& hs,
                                          int x, QRow& r) {
   if (x >= q.nq * hs.n) return false;
-  const int e = x / hs.n;
+  const int e = fdiv(x, hs.f);
   const int row = query_row(g, q, view, e);
   r.t = q.qb + row;
   r.pos = row + q.off;
@@ -339,7 +343,7 @@ __device__ __forceinline__ void tile_range(const Geo& g, const Seq& q, const Job
   j0 = j1 = 0;
   int v0, v1;
   valid_rows(q, job.qview, v0, v1);
-  const int e0 = imax(x0 / hs.n, v0), e1 = imin((imin(x0 + rows, q.nq * hs.n) - 1) / hs.n, v1 - 1);
+  const int e0 = imax(fdiv(x0, hs.f), v0), e1 = imin(fdiv(imin(x0 + rows, q.nq * hs.n) - 1, hs.f), v1 - 1);
   if (e0 > e1) return;
   int lo, hi, a, b;
   live_keys(g, q, job.seg[seg].rule, query_row(g, q, job.qview, e0) + q.off, lo, hi);

@@ -94,6 +94,9 @@ st_status fill_geo(const st_pattern_desc* p, st_dtype dtype, const st_packed_des
   g.split = !dense && p->head_mode == ST_HEADS_SPLIT;
   g.fl = make_fastdiv(g.l);
   g.fc = make_fastdiv(g.c);
+  g.fheads[0] = make_fastdiv(g.G);
+  g.fheads[1] = make_fastdiv((g.G + 1) / 2);
+  g.fheads[2] = make_fastdiv(g.G / 2);
   if (!stride_rows(x->q_stride, x->H, x->d, &g.q.tok) ||
       !stride_rows(x->k_stride, x->Hkv, x->d, &g.k.tok) ||
       !stride_rows(x->v_stride, x->Hkv, x->d, &g.v.tok))

@@ -67,8 +67,9 @@ struct alignas(1024) Smem {
   int abort;
 };
 
+// Boxes of the streamed operands: K, V of one head, or Q, dO of a group's heads.
 struct Maps {
-  CUtensorMap k, v;
+  CUtensorMap b1, b2;
 };
 
 // Query-major unit n of job a.job[0] (all segments), or key-major unit n.
@@ -141,7 +142,7 @@ __device__ __forceinline__ bool decode(const BwdLaunch& a, const Job& qjob, int 
 template <int D, bool F16, bool DKV>
 __global__ void __launch_bounds__(kThreads, 1)
     ragged_bwd_tc(const __grid_constant__ BwdLaunch a, const __grid_constant__ Job qjob,
-                  const __grid_constant__ Maps maps, int slots, int mode) {
+                  const __grid_constant__ Maps maps, int slots, int mode, int boxes) {
   extern __shared__ __align__(1024) uint8_t raw[];
   Smem<D>& S = *reinterpret_cast<Smem<D>*>(raw);
   constexpr int NS = Cfg<D>::kStages, TB = Cfg<D>::kTileBytes;
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       Gathers gath;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok && !__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+        if (ok && !__all_sync(0xffffffffu, bar_test(bar, parity))) {
           gath.flush();  // what others wait for before they free this
           ok = __all_sync(0xffffffffu, bar_wait(bar, parity, limit, abort));
         }
@@ -275,78 +276,75 @@ __global__ void __launch_bounds__(kThreads, 1)
             gath.add(&S.r_full);
           }
           for (int t = u.t0; t < u.t1; ++t, ++tt) {
-            int view = 0, j = t, seg = 0;
-            bool box = false;
-            if (!DKV) {
-              seg = t >= u.cnt0 ? 1 : 0;
+            int view = 0, j = t, bh, bt;
+            bool box;
+            if constexpr (DKV) {
+              // rows (query, head of the group) in natural order: 128 / G tokens
+              box = boxes && job.qview == VIEW_NAT && j * 128 + 128 <= xrows;
+              bh = u.hs.first;
+              bt = u.q.qb + j * boxes;
+            } else {
+              const int seg = t >= u.cnt0 ? 1 : 0;
               j = u.u0[seg] + t - (seg ? u.cnt0 : 0);
               view = job.seg[seg].kview;
               box = view == VIEW_NAT && j * 128 + 128 <= u.q.nk;
+              bh = u.kvh;
+              bt = u.q.qb + j * 128;
             }
-            if (box) {
-              // consecutive tokens: one TMA box per 64 columns
+            int ra[2], rb[2];
+            float vl[2], vd[2];
+            if (DKV || !box) {
 #pragma unroll
-              for (int kv = 0; kv < 2; ++kv, ++kt) {
-                const int s = kt % NS;
-                if (kt >= NS && !wait(&S.empty[s], (kt / NS + 1) & 1)) break;
+              for (int y = 0; y < 2; ++y) {
+                const int e = j * 128 + pw * 64 + y * 32 + lane;
+                if (DKV) query_rows(e, ra[y], rb[y]);
+                else key_rows(view, e, ra[y], rb[y]);
+              }
+            }
+            if (DKV) {
+              // -LSE log2(e) and -D of the tile's rows 64 pw ..; rows with an
+              // empty set have no live entry and get 0
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const float f = __ldg(a.lse + rb[y]);
+                vl[y] = f == -INFINITY ? 0.f : -f * kLog2e;
+                vd[y] = -__ldg(a.delta + rb[y]);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i, ++kt) {
+              const int s = kt % NS;
+              if (kt >= NS && !wait(&S.empty[s], (kt / NS + 1) & 1)) break;
+              if (box) {
                 gath.flush();
                 if (lane == 0) {
                   if (pw == 0) {
                     mbar_arrive_expect_tx(&S.full[s], TB);
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c)
-                      tma_box(smem_u32(S.ring[s]) + c * 16384, kv ? &maps.v : &maps.k, &S.full[s], c * 64,
-                              u.kvh, u.q.qb + j * 128);
+                      tma_box(smem_u32(S.ring[s]) + c * 16384, i ? &maps.b2 : &maps.b1, &S.full[s], c * 64, bh, bt);
                   } else {
                     mbar_arrive(&S.full[s]);
                   }
                 }
+              } else {
+                gather64<D>(smem_u32(S.ring[s]), pw * 64, DKV ? (i ? a.dout : a.q) : (i ? a.v : a.k),
+                            i ? rb[0] : ra[0], i ? rb[1] : ra[1]);
+                gath.add(&S.full[s]);
               }
-              if (!ok) break;
-              continue;
-            }
-            int ra[2], rb[2];
+              if (DKV && i == 0) {
+                const int b = tt & 1;
+                if (tt >= 2 && !wait(&S.row_empty[b], (tt / 2 + 1) & 1)) break;
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int e = j * 128 + pw * 64 + y * 32 + lane;
-              if (DKV) query_rows(e, ra[y], rb[y]);
-              else key_rows(view, e, ra[y], rb[y]);
-            }
-            float val[4];
-            if (DKV) {
-              // -LSE log2(e) (producer 0) or -D (producer 1) of the tile's rows;
-              // rows with an empty set have no live entry and get 0
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                int rq, ro;
-                query_rows(j * 128 + y * 32 + lane, rq, ro);
-                const float f = __ldg((pw ? a.delta : a.lse) + ro);
-                val[y] = pw ? -f : f == -INFINITY ? 0.f : -f * kLog2e;
+                for (int y = 0; y < 2; ++y) {
+                  S.nlse[b][pw * 64 + y * 32 + lane] = vl[y];
+                  S.ndel[b][pw * 64 + y * 32 + lane] = vd[y];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.row_full[b]);
               }
             }
-            {
-              const int s = kt % NS;
-              if (kt >= NS && !wait(&S.empty[s], (kt / NS + 1) & 1)) break;
-              gather64<D>(smem_u32(S.ring[s]), pw * 64, DKV ? a.q : a.k, ra[0], ra[1]);
-              gath.add(&S.full[s]);
-              ++kt;
-            }
-            if (DKV) {
-              const int b = tt & 1;
-              if (tt >= 2 && !wait(&S.row_empty[b], (tt / 2 + 1) & 1)) break;
-              float* dst = pw ? S.ndel[b] : S.nlse[b];
-#pragma unroll
-              for (int y = 0; y < 4; ++y) dst[y * 32 + lane] = val[y];
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&S.row_full[b]);
-            }
-            {
-              const int s = kt % NS;
-              if (kt >= NS && !wait(&S.empty[s], (kt / NS + 1) & 1)) break;
-              gather64<D>(smem_u32(S.ring[s]), pw * 64, DKV ? a.dout : a.v, rb[0], rb[1]);
-              gath.add(&S.full[s]);
-              ++kt;
-            }
+            if (!ok) break;
           }
           if (!ok) break;
         }
@@ -699,9 +697,20 @@ template <int D, bool F16, bool DKV>
 cudaError_t launch(const BwdLaunch& a, const Job& job, int mode) {
   const Geo& g = a.g;
   Maps m = {};
-  if (!DKV && (!make_box_map(&m.k, a.k, F16, g.total, g.Hkv, g.k.tok, D) ||
-               !make_box_map(&m.v, a.v, F16, g.total, g.Hkv, g.v.tok, D)))
-    return cudaErrorInvalidValue;
+  int boxes = 0;  // tokens of a box
+  if (DKV) {
+    if (!g.split && 128 % g.G == 0) {
+      boxes = 128 / g.G;
+      if (!make_box_map(&m.b1, a.q, F16, g.total, g.H, g.q.tok, D, g.G) ||
+          !make_box_map(&m.b2, a.dout, F16, g.total, g.H, g.H, D, g.G))
+        return cudaErrorInvalidValue;
+    }
+  } else {
+    boxes = 128;
+    if (!make_box_map(&m.b1, a.k, F16, g.total, g.Hkv, g.k.tok, D) ||
+        !make_box_map(&m.b2, a.v, F16, g.total, g.Hkv, g.v.tok, D))
+      return cudaErrorInvalidValue;
+  }
   const size_t smem = sizeof(Smem<D>);
   static_assert(sizeof(Smem<D>) <= 232448, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(ragged_bwd_tc<D, F16, DKV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -710,7 +719,7 @@ cudaError_t launch(const BwdLaunch& a, const Job& job, int mode) {
   const long long slots = slot_count(g, DKV ? 1 : most_heads(g, job.hc), 128);
   const long long units = slots * g.Hkv * (DKV ? a.njobs * a.nsplit : 1);
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
-  ragged_bwd_tc<D, F16, DKV><<<(unsigned)units, kThreads, smem, a.stream>>>(a, job, m, (int)slots, mode);
+  ragged_bwd_tc<D, F16, DKV><<<(unsigned)units, kThreads, smem, a.stream>>>(a, job, m, (int)slots, mode, boxes);
   return cudaGetLastError();
 }
 

@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       Gathers gath;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok && !__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+        if (ok && !__all_sync(0xffffffffu, bar_test(bar, parity))) {
           gath.flush();  // what others wait for before they free this
           ok = __all_sync(0xffffffffu, bar_wait(bar, parity, limit, abort));
         }

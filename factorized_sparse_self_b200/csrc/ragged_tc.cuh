@@ -26,6 +26,20 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Whether a phase is complete, at once (try_wait may hold the thread for
+// microseconds first).
+__device__ __forceinline__ bool bar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Waits for a phase; gives up after limit_ns or when another role raised
 // `abort`. The clock and the flag are looked at after every 64 attempts only:
 // read in every attempt, they delay the waking thread.
@@ -102,7 +116,7 @@ struct Gathers {
   }
 };
 
-// 64 columns x 128 consecutive tokens of one head.
+// 64 columns x the map's box of heads and tokens (128 rows).
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c,
                                         int head, int tok) {
   asm volatile(
@@ -167,9 +181,10 @@ __device__ __forceinline__ int claims_take(Claims& c, uint64_t limit, volatile i
 }
 
 // Host: the map of token rows [tokens][heads][d] of 16-bit elements (tok rows of
-// d elements from token to token) for boxes of 128 tokens of one head. False
+// d elements from token to token) for boxes of `n` heads, 128 / n tokens. False
 // when the driver refuses.
-bool make_box_map(CUtensorMap* out, const void* base, bool f16, int tokens, int heads, int tok, int d);
+bool make_box_map(CUtensorMap* out, const void* base, bool f16, int tokens, int heads, int tok, int d,
+                  int n = 1);
 
 // One query-major unit: 2 x 128 rows of one (sequence, key/value head, job),
 // against the key tiles it meets. Key tiles are numbered through the job's

@@ -37,10 +37,11 @@ bool encode(CUtensorMap* out, const void* base, bool f16, int rank, const cuuint
 
 }  // namespace
 
-bool make_box_map(CUtensorMap* out, const void* base, bool f16, int tokens, int heads, int tok, int d) {
+bool make_box_map(CUtensorMap* out, const void* base, bool f16, int tokens, int heads, int tok, int d,
+                  int n) {
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)tok * d * 2};
-  const cuuint32_t box[3] = {64, 1, 128};
+  const cuuint32_t box[3] = {64, (cuuint32_t)n, (cuuint32_t)(128 / n)};
   return encode(out, base, f16, 3, dims, strides, box);
 }
 
