@@ -341,89 +341,83 @@ def st_pattern(kind, mode="merged", l=1, c=1) -> Pattern:
     return Pattern(kind, mode, l, c)
 
 
-def _tokens(t, name, d=None, like=None, heads=None, rows=None):
-    """Address and token stride of token rows [total, heads, d]: the heads of a token lie d apart,
-    tokens any multiple of d."""
+def _tokens(t, name, q=None, heads=None):
+    """Token stride of token rows [total, heads, d] (like q: its d, dtype, device and rows): the
+    heads of a token lie d apart, tokens any multiple of d."""
     if t.dim() != 3 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, d]")
-    d = t.shape[2] if d is None else d
-    if t.shape[2] != d or (heads is not None and t.shape[1] != heads) or \
-            (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} has the wrong shape {tuple(t.shape)}")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must match q in dtype and device")
-    if d > 1 and t.stride(2) != 1 or t.shape[1] > 1 and t.stride(1) != d:
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if q is not None:
+        if t.dtype != q.dtype or t.device != q.device:
+            raise ValueError(f"{name} must match q in dtype and device")
+        if d != q.shape[2] or n != q.shape[0] or (heads is not None and h != heads):
+            raise ValueError(f"{name} has the wrong shape {tuple(t.shape)}")
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         raise ValueError(f"{name} must have the heads of a token contiguous")
-    stride = t.stride(0) if t.shape[0] > 1 else t.shape[1] * d
-    if stride < t.shape[1] * d or stride % d:
+    if n <= 1:
+        return h * d
+    if s0 < h * d or s0 % d:
         raise ValueError(f"{name}: tokens must be a multiple of d = {d} elements apart")
-    return ctypes.c_void_p(t.data_ptr()), stride
+    return s0
 
 
 def _ints(t, name, n, like):
     import torch
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.device != like.device or t.numel() != n:
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n or t.device != like.device:
         raise ValueError(f"{name} must be a contiguous int32 tensor of {n} values on {like.device}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _rows_out(t, name, shape, dtype, like):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != like.device or \
-            not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != like.device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {like.device}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-class _On:
-    """The stream of a call. What the call allocates belongs to that stream, so its memory is not
-    handed out again before the call's work is done."""
+def _call_stream(stream, like):
+    """The CUDA stream of a call, and a context in which what the call allocates belongs to that
+    stream, so that the memory is not handed out again before the call's work is done."""
+    import contextlib
 
-    def __init__(self, stream, like):
-        import torch
-        if torch.cuda.current_device() != like.device.index:
-            raise ValueError(f"tensors are on {like.device}, which is not the current device")
-        self.stream = stream if stream is not None else torch.cuda.current_stream()
-        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
-        self.ctx = torch.cuda.stream(stream) if stream is not None else None
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self
-
-    def __exit__(self, *a):
-        if self.ctx is not None:
-            self.ctx.__exit__(*a)
+    import torch
+    if torch.cuda.current_device() != like.device.index:
+        raise ValueError(f"tensors are on {like.device}, which is not the current device")
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream, contextlib.nullcontext()
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
 def _work(workspace, nbytes, like):
+    """(tensor to keep, address, bytes) of a workspace."""
     import torch
     if workspace is None:
         if nbytes == 0:
-            return None, ctypes.c_void_p(0), 0
+            return None, None, 0
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
     elif workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the tensors' device")
-    return workspace, ctypes.c_void_p(workspace.data_ptr()), \
-        workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _packed_desc(q, k, v, cu_seqlens):
-    total, H, d = q.shape if q.dim() == 3 else (0, 0, 0)
-    qp, qs = _tokens(q, "q")
-    kp, ks = _tokens(k, "k", d, q, rows=total)
-    vp, vs = _tokens(v, "v", d, q, heads=k.shape[1], rows=total)
-    x = _PackedDesc(cu_seqlens.numel() - 1, total, H, k.shape[1], d, qs, ks, vs, 0, 0, 0)
-    return x, qp, kp, vp
+    qs = _tokens(q, "q")
+    ks = _tokens(k, "k", q)
+    total, H, d = q.shape
+    Hkv = k.shape[1]
+    return _PackedDesc(cu_seqlens.numel() - 1, total, H, Hkv, d, qs, ks, _tokens(v, "v", q, Hkv), 0,
+                       0, 0)
+
+
+def _packed_workspace(name, pat, code, x):
+    n = ctypes.c_size_t()
+    _check(getattr(lib(), name)(ctypes.byref(pat), code, ctypes.byref(x), ctypes.byref(n)), name)
+    return n.value
 
 
 def st_packed_attn_fwd_workspace(pattern: Pattern, q, k, v, cu_seqlens, max_len) -> int:
-    x = _packed_desc(q, k, v, cu_seqlens)[0]
-    n = ctypes.c_size_t()
-    _check(lib().st_packed_attn_fwd_workspace(ctypes.byref(pattern._desc(max_len)), _dtype_code(q),
-                                              ctypes.byref(x), ctypes.byref(n)),
-           "st_packed_attn_fwd_workspace")
-    return n.value
+    return _packed_workspace("st_packed_attn_fwd_workspace", pattern._desc(max_len), _dtype_code(q),
+                             _packed_desc(q, k, v, cu_seqlens))
 
 
 def st_packed_attn_fwd(pattern: Pattern, q, k, v, cu_seqlens, max_len, scale=None, o=None, lse=None,
@@ -434,28 +428,28 @@ def st_packed_attn_fwd(pattern: Pattern, q, k, v, cu_seqlens, max_len, scale=Non
     split). Returns o [total, H, d] and lse float32 [total, H] (natural log); token rows of no
     sequence are not written."""
     import torch
-    x, qp, kp, vp = _packed_desc(q, k, v, cu_seqlens)
+    x = _packed_desc(q, k, v, cu_seqlens)
     cu = _ints(cu_seqlens, "cu_seqlens", x.n_seqs + 1, q)
-    nb = st_packed_attn_fwd_workspace(pattern, q, k, v, cu_seqlens, max_len)
-    with _On(stream, q) as on:
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if lse is None else lse
-        op = _rows_out(o, "o", q.shape, q.dtype, q)
-        lp = _rows_out(lse, "lse", q.shape[:2], torch.float32, q)
+    code, pat = _dtype_code(q), pattern._desc(max_len)
+    nb = _packed_workspace("st_packed_attn_fwd_workspace", pat, code, x)
+    sp, ctx = _call_stream(stream, q)
+    with ctx:
+        if o is None:
+            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
         keep, ws, wn = _work(workspace, nb, q)
-        _check(lib().st_packed_attn_fwd(ctypes.byref(pattern._desc(max_len)), _dtype_code(q),
-                                        ctypes.byref(x), float(scale) if scale else 0.0, qp, kp, vp,
-                                        cu, op, lp, ws, wn, on.ptr), "st_packed_attn_fwd")
+        _check(lib().st_packed_attn_fwd(ctypes.byref(pat), code, ctypes.byref(x),
+                                        float(scale) if scale else 0.0, q.data_ptr(), k.data_ptr(),
+                                        v.data_ptr(), cu, _rows_out(o, "o", q.shape, q.dtype, q),
+                                        _rows_out(lse, "lse", q.shape[:2], torch.float32, q), ws, wn,
+                                        sp), "st_packed_attn_fwd")
     return o, lse
 
 
 def st_packed_attn_bwd_workspace(pattern: Pattern, q, k, v, cu_seqlens, max_len) -> int:
-    x = _packed_desc(q, k, v, cu_seqlens)[0]
-    n = ctypes.c_size_t()
-    _check(lib().st_packed_attn_bwd_workspace(ctypes.byref(pattern._desc(max_len)), _dtype_code(q),
-                                              ctypes.byref(x), ctypes.byref(n)),
-           "st_packed_attn_bwd_workspace")
-    return n.value
+    return _packed_workspace("st_packed_attn_bwd_workspace", pattern._desc(max_len), _dtype_code(q),
+                             _packed_desc(q, k, v, cu_seqlens))
 
 
 def st_packed_attn_bwd(pattern: Pattern, q, k, v, o, lse, dout, cu_seqlens, max_len, scale=None,
@@ -463,61 +457,69 @@ def st_packed_attn_bwd(pattern: Pattern, q, k, v, o, lse, dout, cu_seqlens, max_
     """dq [total, H, d], dk, dv [total, Hkv, d] of st_packed_attn_fwd (dtype of q; given tensors may
     be slices of a fused gradient). Rows of no sequence are not written."""
     import torch
-    x, qp, kp, vp = _packed_desc(q, k, v, cu_seqlens)
+    x = _packed_desc(q, k, v, cu_seqlens)
     cu = _ints(cu_seqlens, "cu_seqlens", x.n_seqs + 1, q)
-    op = _rows_out(o, "o", q.shape, q.dtype, q)
-    lp = _rows_out(lse, "lse", q.shape[:2], torch.float32, q)
-    gp = _rows_out(dout, "dout", q.shape, q.dtype, q)
-    nb = st_packed_attn_bwd_workspace(pattern, q, k, v, cu_seqlens, max_len)
-    with _On(stream, q) as on:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device) if dk is None else dk
-        dv = torch.empty(k.shape, dtype=q.dtype, device=q.device) if dv is None else dv
-        dqp, x.dq_stride = _tokens(dq, "dq", x.d, q, x.H, x.total)
-        dkp, x.dk_stride = _tokens(dk, "dk", x.d, q, x.Hkv, x.total)
-        dvp, x.dv_stride = _tokens(dv, "dv", x.d, q, x.Hkv, x.total)
+    code, pat = _dtype_code(q), pattern._desc(max_len)
+    nb = _packed_workspace("st_packed_attn_bwd_workspace", pat, code, x)
+    sp, ctx = _call_stream(stream, q)
+    with ctx:
+        if dq is None:
+            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if dk is None:
+            dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        if dv is None:
+            dv = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        x.dq_stride = _tokens(dq, "dq", q, x.H)
+        x.dk_stride = _tokens(dk, "dk", q, x.Hkv)
+        x.dv_stride = _tokens(dv, "dv", q, x.Hkv)
         keep, ws, wn = _work(workspace, nb, q)
-        _check(lib().st_packed_attn_bwd(ctypes.byref(pattern._desc(max_len)), _dtype_code(q),
-                                        ctypes.byref(x), float(scale) if scale else 0.0, qp, kp, vp,
-                                        op, lp, gp, cu, dqp, dkp, dvp, ws, wn, on.ptr),
+        _check(lib().st_packed_attn_bwd(ctypes.byref(pat), code, ctypes.byref(x),
+                                        float(scale) if scale else 0.0, q.data_ptr(), k.data_ptr(),
+                                        v.data_ptr(), _rows_out(o, "o", q.shape, q.dtype, q),
+                                        _rows_out(lse, "lse", q.shape[:2], torch.float32, q),
+                                        _rows_out(dout, "dout", q.shape, q.dtype, q), cu,
+                                        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws, wn, sp),
                "st_packed_attn_bwd")
     return dq, dk, dv
 
 
-def _cache_desc(k_cache, v_cache, page_table, d, like):
+def _cache_desc(k_cache, v_cache, page_table, like):
+    d = like.shape[2]
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if t.dim() != 4 or t.shape[3] != d or t.dtype != like.dtype or t.device != like.device:
             raise ValueError(f"{name} must be [pages, page_size, Hkv, {d}], of {like.dtype} on "
                              f"{like.device}")
-        if t.stride(3) != 1 and d > 1:
-            raise ValueError(f"{name} must be contiguous in its last dimension")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+    n, size, Hkv, _ = k_cache.shape
+    s = k_cache.stride()
+    if k_cache.shape != v_cache.shape or s != v_cache.stride():
         raise ValueError("k_cache and v_cache must have the same shape and strides")
+    if s[3] != 1 and d > 1:
+        raise ValueError("the caches must be contiguous in their last dimension")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [sequences, pages]")
-    n, size, _, _ = k_cache.shape
-    sp, ss, sh, _ = k_cache.stride()
-    return _CacheDesc(n, size, page_table.shape[1], sp, ss, sh)
+    return _CacheDesc(n, size, page_table.shape[1], s[0], s[1], s[2]), Hkv
 
 
 def _paged_args(q, k_cache, v_cache, page_table, cu_q, kv_lens):
-    qp, qs = _tokens(q, "q")
+    qs = _tokens(q, "q")
     S = cu_q.numel() - 1
-    c = _cache_desc(k_cache, v_cache, page_table, q.shape[2], q)
-    x = _PackedDesc(S, q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2], qs, 0, 0, 0, 0, 0)
-    ints = (_ints(page_table, "page_table", S * c.max_pages, q), _ints(cu_q, "cu_q", S + 1, q),
-            _ints(kv_lens, "kv_lens", S, q))
-    return x, c, qp, ints
+    c, Hkv = _cache_desc(k_cache, v_cache, page_table, q)
+    x = _PackedDesc(S, q.shape[0], q.shape[1], Hkv, q.shape[2], qs, 0, 0, 0, 0, 0)
+    return x, c, (_ints(page_table, "page_table", S * c.max_pages, q), _ints(cu_q, "cu_q", S + 1, q),
+                  _ints(kv_lens, "kv_lens", S, q))
+
+
+def _paged_workspace(pat, code, x, c, max_q):
+    n = ctypes.c_size_t()
+    _check(lib().st_paged_attn_workspace(ctypes.byref(pat), code, ctypes.byref(x), ctypes.byref(c),
+                                         max_q, ctypes.byref(n)), "st_paged_attn_workspace")
+    return n.value
 
 
 def st_paged_attn_workspace(pattern: Pattern, q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q,
                             max_kv) -> int:
-    x, c, _, _ = _paged_args(q, k_cache, v_cache, page_table, cu_q, kv_lens)
-    n = ctypes.c_size_t()
-    _check(lib().st_paged_attn_workspace(ctypes.byref(pattern._desc(max_kv)), _dtype_code(q),
-                                         ctypes.byref(x), ctypes.byref(c), int(max_q),
-                                         ctypes.byref(n)), "st_paged_attn_workspace")
-    return n.value
+    x, c, _ = _paged_args(q, k_cache, v_cache, page_table, cu_q, kv_lens)
+    return _paged_workspace(pattern._desc(max_kv), _dtype_code(q), x, c, int(max_q))
 
 
 def st_paged_attn(pattern: Pattern, q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q, max_kv,
@@ -528,43 +530,42 @@ def st_paged_attn(pattern: Pattern, q, k_cache, v_cache, page_table, cu_q, kv_le
     int32 [n], the new tokens included. max_q and max_kv, the most new tokens and keys of a sequence
     expected, only steer how work is split. Returns o [total, H, d], lse float32 [total, H]."""
     import torch
-    x, c, qp, ints = _paged_args(q, k_cache, v_cache, page_table, cu_q, kv_lens)
-    pat = pattern._desc(max_kv)
-    n = ctypes.c_size_t()
-    _check(lib().st_paged_attn_workspace(ctypes.byref(pat), _dtype_code(q), ctypes.byref(x),
-                                         ctypes.byref(c), int(max_q), ctypes.byref(n)),
-           "st_paged_attn_workspace")
-    with _On(stream, q) as on:
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if lse is None else lse
-        op = _rows_out(o, "o", q.shape, q.dtype, q)
-        lp = _rows_out(lse, "lse", q.shape[:2], torch.float32, q)
-        keep, ws, wn = _work(workspace, n.value, q)
-        _check(lib().st_paged_attn(ctypes.byref(pat), _dtype_code(q), ctypes.byref(x),
-                                   ctypes.byref(c), int(max_q), float(scale) if scale else 0.0, qp,
-                                   ctypes.c_void_p(k_cache.data_ptr()),
-                                   ctypes.c_void_p(v_cache.data_ptr()), *ints, op, lp, ws, wn,
-                                   on.ptr), "st_paged_attn")
+    x, c, (pt, cu, kv) = _paged_args(q, k_cache, v_cache, page_table, cu_q, kv_lens)
+    code, pat, max_q = _dtype_code(q), pattern._desc(max_kv), int(max_q)
+    nb = _paged_workspace(pat, code, x, c, max_q)
+    sp, ctx = _call_stream(stream, q)
+    with ctx:
+        if o is None:
+            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        keep, ws, wn = _work(workspace, nb, q)
+        _check(lib().st_paged_attn(ctypes.byref(pat), code, ctypes.byref(x), ctypes.byref(c), max_q,
+                                   float(scale) if scale else 0.0, q.data_ptr(), k_cache.data_ptr(),
+                                   v_cache.data_ptr(), pt, cu, kv,
+                                   _rows_out(o, "o", q.shape, q.dtype, q),
+                                   _rows_out(lse, "lse", q.shape[:2], torch.float32, q), ws, wn, sp),
+               "st_paged_attn")
     return o, lse
 
 
 def st_cache_append(k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens, stream=None):
     """Writes new keys and values k, v [total, Hkv, d] into the pages of the cache: new token t of n
     of sequence s goes to position kv_lens[s] - n + t (kv_lens counts the new tokens)."""
-    kp, ks = _tokens(k, "k")
-    vp, vs = _tokens(v, "v", k.shape[2], k, k.shape[1], k.shape[0])
+    ks = _tokens(k, "k")
+    total, Hkv, d = k.shape
+    vs = _tokens(v, "v", k, Hkv)
     S = cu_seqlens.numel() - 1
-    c = _cache_desc(k_cache, v_cache, page_table, k.shape[2], k)
-    if k_cache.shape[2] != k.shape[1]:
+    c, cache_heads = _cache_desc(k_cache, v_cache, page_table, k)
+    if cache_heads != Hkv:
         raise ValueError("k and the cache differ in their number of heads")
-    x = _PackedDesc(S, k.shape[0], k.shape[1], k.shape[1], k.shape[2], 0, ks, vs, 0, 0, 0)
-    with _On(stream, k) as on:
-        _check(lib().st_cache_append(_dtype_code(k), ctypes.byref(x), ctypes.byref(c), kp, vp,
-                                     ctypes.c_void_p(k_cache.data_ptr()),
-                                     ctypes.c_void_p(v_cache.data_ptr()),
-                                     _ints(page_table, "page_table", S * c.max_pages, k),
-                                     _ints(cu_seqlens, "cu_seqlens", S + 1, k),
-                                     _ints(kv_lens, "kv_lens", S, k), on.ptr), "st_cache_append")
+    x = _PackedDesc(S, total, Hkv, Hkv, d, 0, ks, vs, 0, 0, 0)
+    sp, _ = _call_stream(stream, k)
+    _check(lib().st_cache_append(_dtype_code(k), ctypes.byref(x), ctypes.byref(c), k.data_ptr(),
+                                 v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                 _ints(page_table, "page_table", S * c.max_pages, k),
+                                 _ints(cu_seqlens, "cu_seqlens", S + 1, k),
+                                 _ints(kv_lens, "kv_lens", S, k), sp), "st_cache_append")
 
 
 def st_last_device_status(stream=None) -> int:

@@ -288,17 +288,30 @@ __device__ __forceinline__ Seq load_seq(const Geo& g, int s) {
   return make_seq(g, s, a, b - a, nk);
 }
 
-// Sequence and tile of a slot (the tile may be past the sequence's rows).
-__device__ __forceinline__ int find_slot(const Geo& g, int mult, int BM, int slot, int& tile) {
-  int a = 0, b = g.S - 1;
-  while (a < b) {
-    const int m = (a + b + 1) >> 1;
-    const int first = (int)((long long)cu_at(g, m) * mult / BM) + m;
-    if (first <= slot) a = m;
-    else b = m - 1;
+// The last of 0 .. n-1 for which pred holds (true up to some index, which
+// includes 0, then false), by a whole warp: 32 probes a round instead of one, for
+// each round waits for memory.
+template <class P>
+__device__ __forceinline__ int last_true(int n, P pred) {
+  const int lane = threadIdx.x & 31;
+  int a = 0;
+  while (n > 1) {
+    const int step = (n + 31) >> 5, x = a + lane * step;
+    const unsigned yes = __ballot_sync(0xffffffffu, lane * step < n && pred(x));
+    const int c = imax(__popc(yes), 1) - 1;
+    a += c * step;
+    n = imin(step, n - c * step);
   }
-  tile = slot - ((int)((long long)cu_at(g, a) * mult / BM) + a);
   return a;
+}
+
+// Sequence and tile of a slot (the tile may be past the sequence's rows), by a
+// whole warp.
+__device__ __forceinline__ int find_slot(const Geo& g, int mult, int BM, int slot, int& tile) {
+  auto first = [&](int s) { return (int)((long long)cu_at(g, s) * mult / BM) + s; };
+  const int s = last_true(g.S, [&](int x) { return first(x) <= slot; });
+  tile = slot - first(s);
+  return s;
 }
 
 // Row (in units of d elements) of key position j, key/value head kvh, of k or v

@@ -29,19 +29,17 @@ ST_HD int parts_of(int tiles, int nsplit, int least) {
   return imax(1, imin(nsplit, (tiles + least - 1) / least));
 }
 
-// One launch of a forward kernel: one job (the few-row kernel: all jobs at
-// once), its keys cut into up to nsplit parts.
+// One launch of a forward kernel: one or two jobs, each unit's keys cut into up
+// to nsplit parts.
 struct FwdLaunch {
   Geo g;
-  Job job;
-  Job job1;          // few-row kernel: the second job
+  Job job, job1;
   int32_t njobs;
   const void *q, *k, *v;
   void* o;
   float* lse;
   Parts parts;
-  int32_t part0;   // first part of this job
-  int32_t part1;   // few-row kernel: of the second job
+  int32_t part0, part1;  // first part of each job
   int32_t nsplit;  // OUT_PARTIAL: most key ranges of a unit
   int32_t least;   // fewest key tiles of a range
   int32_t mode;    // OutMode
@@ -56,6 +54,8 @@ struct BwdLaunch {
   Geo g;
   Job job[2];        // key jobs: one segment each
   int32_t njobs;
+  Job qjob[2];       // query jobs of this launch
+  int32_t nqjobs, mode;
   const void *q, *k, *v, *dout;
   const float *lse, *delta;
   void *dq, *dk, *dv;
@@ -92,17 +92,17 @@ __device__ __forceinline__ bool dkv_direct(const BwdLaunch& a, int kvh) {
 cudaError_t tc_ragged_fwd(const FwdLaunch& a, int dtype);
 
 // Tensor-core backward of packed sequences: dQ of one query order, and dK, dV.
-cudaError_t tc_ragged_dq(const BwdLaunch& a, const Job& job, int mode, int dtype);
+cudaError_t tc_ragged_dq(const BwdLaunch& a, int dtype);
 cudaError_t tc_ragged_dkv(const BwdLaunch& a, int dtype);
 
 // Few query rows per key/value head over a paged cache (decoding steps): bf16 /
 // fp16, d = 64 or 128.
 cudaError_t few_rows_fwd(const FwdLaunch& a, int dtype);
 
-// CUDA-core kernels in fp32 arithmetic.
-cudaError_t simt_ragged_fwd(const FwdLaunch& a, int dtype);
-cudaError_t simt_ragged_dq(const BwdLaunch& a, const Job& job, int mode, int dtype);
-cudaError_t simt_ragged_dkv(const BwdLaunch& a, int dtype);
+// CUDA-core kernels for float32 tensors.
+cudaError_t simt_ragged_fwd(const FwdLaunch& a);
+cudaError_t simt_ragged_dq(const BwdLaunch& a);
+cudaError_t simt_ragged_dkv(const BwdLaunch& a);
 
 // Joins nparts parts of every query row (rows of no sequence are skipped).
 cudaError_t join_parts(const Geo& g, int dtype, const Parts& parts, int nparts,

@@ -233,20 +233,25 @@ st_status run_fwd(const st_pattern_desc& p, st_dtype dtype, Geo& g, float scale,
   a.stream = stream;
   Job jobs[2];
   const int n = make_jobs(p, jobs);
+  auto go = [&]() {
+    return f.few ? few_rows_fwd(a, dtype) : dtype == ST_F32 ? simt_ragged_fwd(a) : tc_ragged_fwd(a, dtype);
+  };
   cudaError_t e = cudaSuccess;
-  if (f.few) {
+  if (f.merge) {
+    // the second order reads what the first left
+    a.njobs = 1;
+    for (int j = 0; j < n && e == cudaSuccess; ++j) {
+      a.job = jobs[j];
+      a.mode = j == 0 ? OUT_PARTIAL : OUT_MERGE;
+      e = go();
+    }
+  } else {
     a.job = jobs[0];
     a.job1 = jobs[n - 1];
     a.njobs = n;
     a.part1 = two_orders(p) ? f.nsplit : 0;
     a.mode = f.nparts ? OUT_PARTIAL : OUT_FINAL;
-    e = few_rows_fwd(a, dtype);
-  }
-  for (int j = 0; j < n && !f.few && e == cudaSuccess; ++j) {
-    a.job = jobs[j];
-    a.part0 = two_orders(p) && j == 1 && !f.merge ? f.nsplit : 0;
-    a.mode = f.merge ? (j == 0 ? OUT_PARTIAL : OUT_MERGE) : f.nparts ? OUT_PARTIAL : OUT_FINAL;
-    e = dtype == ST_F32 ? simt_ragged_fwd(a, dtype) : tc_ragged_fwd(a, dtype);
+    e = go();
   }
   if (e == cudaSuccess && f.nparts && !f.merge)
     e = join_parts(g, dtype, a.parts, f.nparts, o, lse, stream);
@@ -374,13 +379,24 @@ st_status st_packed_attn_bwd(const st_pattern_desc* p, st_dtype dtype, const st_
   a.wait_ns = wait_limit_ns();
   a.stream = cs;
   cudaError_t e = row_delta(g, dtype, o, dout, delta, cs);
-  if (e == cudaSuccess) e = dtype == ST_F32 ? simt_ragged_dkv(a, dtype) : tc_ragged_dkv(a, dtype);
+  if (e == cudaSuccess) e = dtype == ST_F32 ? simt_ragged_dkv(a) : tc_ragged_dkv(a, dtype);
   if (e == cudaSuccess && b.parts) e = join_dkv(a, dtype);
   Job jobs[2];
   const int n = make_jobs(*p, jobs);
-  for (int j = 0; j < n && e == cudaSuccess; ++j) {
-    const int mode = two_orders(*p) ? (j == 0 ? OUT_PARTIAL : OUT_MERGE) : OUT_FINAL;
-    e = dtype == ST_F32 ? simt_ragged_dq(a, jobs[j], mode, dtype) : tc_ragged_dq(a, jobs[j], mode, dtype);
+  auto go_dq = [&]() { return dtype == ST_F32 ? simt_ragged_dq(a) : tc_ragged_dq(a, dtype); };
+  if (two_orders(*p)) {
+    a.nqjobs = 1;
+    for (int j = 0; j < n && e == cudaSuccess; ++j) {
+      a.qjob[0] = jobs[j];
+      a.mode = j == 0 ? OUT_PARTIAL : OUT_MERGE;
+      e = go_dq();
+    }
+  } else if (e == cudaSuccess) {
+    a.qjob[0] = jobs[0];
+    a.qjob[1] = jobs[n - 1];
+    a.nqjobs = n;
+    a.mode = OUT_FINAL;
+    e = go_dq();
   }
   return e == cudaSuccess ? ST_OK : ST_ERR_CUDA;
 }

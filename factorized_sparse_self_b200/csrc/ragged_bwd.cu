@@ -72,19 +72,20 @@ struct Maps {
   CUtensorMap b1, b2;
 };
 
-// Query-major unit n of job a.job[0] (all segments), or key-major unit n.
+// Query-major unit n of the query jobs (all segments), or key-major unit n.
 template <bool DKV>
-__device__ __forceinline__ bool decode(const BwdLaunch& a, const Job& qjob, int slots, int n, BUnit* out) {
+__device__ __forceinline__ bool decode(const BwdLaunch& a, int slots, int n, BUnit* out) {
   const Geo& g = a.g;
   const int lane = threadIdx.x & 31;
   int split = 0, jb = 0, m = n;
   if constexpr (DKV) {
     split = m % a.nsplit;
     m /= a.nsplit;
-    jb = m % a.njobs;
-    m /= a.njobs;
   }
-  const Job& job = DKV ? a.job[jb] : qjob;
+  const int nj = DKV ? a.njobs : a.nqjobs;
+  jb = m % nj;
+  m /= nj;
+  const Job& job = DKV ? a.job[jb] : a.qjob[jb];
   const int kvh = m % g.Hkv;
   // query-major: a sequence's last rows see the most keys; key-major: its first
   // keys are seen by the most rows
@@ -141,8 +142,7 @@ __device__ __forceinline__ bool decode(const BwdLaunch& a, const Job& qjob, int 
 
 template <int D, bool F16, bool DKV>
 __global__ void __launch_bounds__(kThreads, 1)
-    ragged_bwd_tc(const __grid_constant__ BwdLaunch a, const __grid_constant__ Job qjob,
-                  const __grid_constant__ Maps maps, int slots, int mode, int boxes) {
+    ragged_bwd_tc(const __grid_constant__ BwdLaunch a, const __grid_constant__ Maps maps, int slots, int boxes) {
   extern __shared__ __align__(1024) uint8_t raw[];
   Smem<D>& S = *reinterpret_cast<Smem<D>*>(raw);
   constexpr int NS = Cfg<D>::kStages, TB = Cfg<D>::kTileBytes;
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = blockIdx.x; n >= 0;) {
         ok = slot_free();
         if (!ok) break;
-        if (decode<DKV>(a, qjob, slots, n, &S.unit[k % kSched])) {
+        if (decode<DKV>(a, slots, n, &S.unit[k % kSched])) {
           __threadfence_block();
           if (lane == 0) mbar_arrive(&S.sched_full[k % kSched]);
           ++k;
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&S.sched_full[n % kSched], (n / kSched) & 1) || !S.unit[n % kSched].live) break;
         const BUnit& u = S.unit[n % kSched];
         if (u.t1 > u.t0) {
-          const Job& job = DKV ? a.job[u.job] : qjob;
+          const Job& job = DKV ? a.job[u.job] : a.qjob[u.job];
           const int xrows = u.q.nq * u.hs.n;
           // row numbers of Q (in q) and dO (contiguous) of query row x
           auto query_rows = [&](int x, int& rq, int& ro) {
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(&S.sched_full[n % kSched], (n / kSched) & 1)) break;
       const BUnit& u = S.unit[n % kSched];
       if (!u.live) break;
-      const Job& job = DKV ? a.job[u.job] : qjob;
+      const Job& job = DKV ? a.job[u.job] : a.qjob[u.job];
       const int t0 = u.t0, t1 = u.t1;
       // live columns of this thread's row, in the unit's tile numbering
       int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0;
@@ -507,9 +507,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         QRow qr;
-        if (query_at(g, u.q, qjob.qview, u.hs, u.r0 + row, qr)) {
-          live_keys(g, u.q, qjob.seg[0].rule, qr.pos, lo0, hi0);
-          if (qjob.nseg > 1) live_keys(g, u.q, qjob.seg[1].rule, qr.pos, lo1, hi1);
+        if (query_at(g, u.q, job.qview, u.hs, u.r0 + row, qr)) {
+          live_keys(g, u.q, job.seg[0].rule, qr.pos, lo0, hi0);
+          if (job.nseg > 1) live_keys(g, u.q, job.seg[1].rule, qr.pos, lo1, hi1);
           const size_t rr = (size_t)qr.t * g.H + qr.h;
           const float f = a.lse[rr];
           nl = f == -INFINITY ? 0.f : -f * kLog2e;
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the unit's rows ----
       if constexpr (!DKV) {
         QRow qr;
-        const bool have = query_at(g, u.q, qjob.qview, u.hs, u.r0 + row, qr);
+        const bool have = query_at(g, u.q, job.qview, u.hs, u.r0 + row, qr);
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
         if (t1 > t0) {
@@ -620,12 +620,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 32; ++x) o[x] = t1 > t0 ? o[x] * a.scale : 0.f;
           float4* part = reinterpret_cast<float4*>(a.dq_part + ((size_t)qr.t * g.H + qr.h) * D + c);
-          if (mode == OUT_PARTIAL) {
+          if (a.mode == OUT_PARTIAL) {
 #pragma unroll
             for (int x = 0; x < 8; ++x) part[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
             continue;
           }
-          if (mode == OUT_MERGE) {
+          if (a.mode == OUT_MERGE) {
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
               const float4 f = part[x];
@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, bool F16, bool DKV>
-cudaError_t launch(const BwdLaunch& a, const Job& job, int mode) {
+cudaError_t launch(const BwdLaunch& a) {
   const Geo& g = a.g;
   Maps m = {};
   int boxes = 0;  // tokens of a box
@@ -716,25 +716,23 @@ cudaError_t launch(const BwdLaunch& a, const Job& job, int mode) {
   cudaError_t e = cudaFuncSetAttribute(ragged_bwd_tc<D, F16, DKV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
-  const long long slots = slot_count(g, DKV ? 1 : most_heads(g, job.hc), 128);
-  const long long units = slots * g.Hkv * (DKV ? a.njobs * a.nsplit : 1);
+  const long long slots = slot_count(g, DKV ? 1 : most_heads(g, a.qjob[0].hc), 128);
+  const long long units = slots * g.Hkv * (DKV ? a.njobs * a.nsplit : a.nqjobs);
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
-  ragged_bwd_tc<D, F16, DKV><<<(unsigned)units, kThreads, smem, a.stream>>>(a, job, m, (int)slots, mode, boxes);
+  ragged_bwd_tc<D, F16, DKV><<<(unsigned)units, kThreads, smem, a.stream>>>(a, m, (int)slots, boxes);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t tc_ragged_dq(const BwdLaunch& a, const Job& job, int mode, int dtype) {
-  if (a.g.d == 64)
-    return dtype == ST_F16 ? launch<64, true, false>(a, job, mode) : launch<64, false, false>(a, job, mode);
-  return dtype == ST_F16 ? launch<128, true, false>(a, job, mode) : launch<128, false, false>(a, job, mode);
+cudaError_t tc_ragged_dq(const BwdLaunch& a, int dtype) {
+  if (a.g.d == 64) return dtype == ST_F16 ? launch<64, true, false>(a) : launch<64, false, false>(a);
+  return dtype == ST_F16 ? launch<128, true, false>(a) : launch<128, false, false>(a);
 }
 
 cudaError_t tc_ragged_dkv(const BwdLaunch& a, int dtype) {
-  const Job& none = a.job[0];
-  if (a.g.d == 64) return dtype == ST_F16 ? launch<64, true, true>(a, none, 0) : launch<64, false, true>(a, none, 0);
-  return dtype == ST_F16 ? launch<128, true, true>(a, none, 0) : launch<128, false, true>(a, none, 0);
+  if (a.g.d == 64) return dtype == ST_F16 ? launch<64, true, true>(a) : launch<64, false, true>(a);
+  return dtype == ST_F16 ? launch<128, true, true>(a) : launch<128, false, true>(a);
 }
 
 }  // namespace rag

@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = blockIdx.x; n >= 0;) {
         ok = slot_free();
         if (!ok) break;
-        if (decode_unit(g, a.job, a.nsplit, a.least, slots, n, kRows, &S.unit[k % kSched])) {
+        if (decode_unit(a, slots, n, kRows, &S.unit[k % kSched])) {
           __threadfence_block();
           if (lane == 0) mbar_arrive(&S.sched_full[k % kSched]);
           ++k;
@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&S.sched_full[n % kSched], (n / kSched) & 1) || !S.unit[n % kSched].live) break;
         const Unit& u = S.unit[n % kSched];
         if (u.t1 > u.t0) {
+          const Job& job = u.job ? a.job1 : a.job;
           if (used > 0 && !wait(&S.q_empty, (used - 1) & 1)) break;
           ++used;
           const int rows = u.q.nq * u.hs.n;
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               QRow qr;
-              query_at(g, u.q, a.job.qview, u.hs, imin(u.x0 + pw * 128 + i * 64 + y * 32 + lane, rows - 1), qr);
+              query_at(g, u.q, job.qview, u.hs, imin(u.x0 + pw * 128 + i * 64 + y * 32 + lane, rows - 1), qr);
               r[y] = q_row(g, qr.t, qr.h);
             }
             gather64<D>(smem_u32(S.q[pw]), i * 64, a.q, r[0], r[1]);
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = u.t0; t < u.t1 && ok; ++t) {
             int seg, j;
             unit_tile(u, t, seg, j);
-            const int view = a.job.seg[seg].kview, nk = n_keys(u.q, view);
+            const int view = job.seg[seg].kview, nk = n_keys(u.q, view);
             if (boxes && view == VIEW_NAT && j * 128 + 128 <= nk) {
               // consecutive tokens: one TMA box per 64 columns
 #pragma unroll
@@ -360,12 +361,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const Unit& su = S.unit[n % kSched];
       if (!su.live) break;
+      const Job& job = su.job ? a.job1 : a.job;
       int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0;
       {
         QRow qr;
-        if (query_at(g, su.q, a.job.qview, su.hs, su.x0 + h * 128 + row, qr) && qr.pos >= 0) {
-          live_keys(g, su.q, a.job.seg[0].rule, qr.pos, lo0, hi0);
-          if (a.job.nseg > 1) live_keys(g, su.q, a.job.seg[1].rule, qr.pos, lo1, hi1);
+        if (query_at(g, su.q, job.qview, su.hs, su.x0 + h * 128 + row, qr) && qr.pos >= 0) {
+          live_keys(g, su.q, job.seg[0].rule, qr.pos, lo0, hi0);
+          if (job.nseg > 1) live_keys(g, su.q, job.seg[1].rule, qr.pos, lo1, hi1);
         }
       }
       const int t1 = su.t1;
@@ -440,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the unit's rows ----
       // (the row is worked out again: kept over the tiles it would cost them registers)
       QRow qr;
-      const bool have = query_at(g, su.q, a.job.qview, su.hs, su.x0 + h * 128 + row, qr);
-      const int part = su.part, parts = su.parts;
+      const bool have = query_at(g, su.q, job.qview, su.hs, su.x0 + h * 128 + row, qr);
+      const int part = su.part, parts = su.parts, part0 = su.job ? a.part1 : a.part0;
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
       if (any) {
@@ -464,10 +466,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (have) {
         if (a.mode == OUT_PARTIAL) {
-          a.parts.lse[(size_t)(a.part0 + part) * g.total * g.H + rr] = L;
+          a.parts.lse[(size_t)(part0 + part) * g.total * g.H + rr] = L;
           if (part == 0)
             for (int p = parts; p < a.nsplit; ++p)
-              a.parts.lse[(size_t)(a.part0 + p) * g.total * g.H + rr] = -INFINITY;
+              a.parts.lse[(size_t)(part0 + p) * g.total * g.H + rr] = -INFINITY;
         } else {
           a.lse[rr] = L;
         }
@@ -485,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (a.mode == OUT_PARTIAL) {
           if (wc > 0.f) {  // a part without weight is not read
             float4* dst = reinterpret_cast<float4*>(
-                a.parts.o + ((size_t)(a.part0 + part) * g.total * g.H + rr) * D + c);
+                a.parts.o + ((size_t)(part0 + part) * g.total * g.H + rr) * D + c);
 #pragma unroll
             for (int x = 0; x < 8; ++x)
               dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
@@ -532,7 +534,7 @@ cudaError_t launch(const FwdLaunch& a) {
                                        (int)smem);
   if (e != cudaSuccess) return e;
   const long long slots = slot_count(g, most_heads(g, a.job.hc), kRows);
-  const long long units = slots * g.Hkv * a.nsplit;
+  const long long units = slots * g.Hkv * a.njobs * a.nsplit;
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
   ragged_fwd_tc<D, F16><<<(unsigned)units, kThreads, smem, a.stream>>>(a, m, (int)slots, boxes);
   return cudaGetLastError();

@@ -54,10 +54,10 @@ __device__ __forceinline__ __half round_to<__half>(float x) {
   return __float2half_rn(x);
 }
 
-// Copies 64 rows of D elements into dst [64][D + 4] as fp32; row(i) gives the
+// Copies 64 rows of D elements into dst [64][D + 4]; row(i) gives the
 // row index of tile row i, or -1 for a row of zeros.
-template <int D, class T, class F>
-__device__ __forceinline__ void load_rows(float* dst, const T* base, F row) {
+template <int D, class F>
+__device__ __forceinline__ void load_rows(float* dst, const float* base, F row) {
   constexpr int C4 = D / 4;
   for (int x = threadIdx.x; x < BM * C4; x += NT) {
     const int i = x / C4, c = x - i * C4;
@@ -107,7 +107,7 @@ __device__ __forceinline__ void weigh_tile(const float* W, const float* B, int t
   }
 }
 
-template <int D, class T>
+template <int D>
 __global__ void __launch_bounds__(NT) ragged_fwd_simt(const __grid_constant__ FwdLaunch a) {
   extern __shared__ float sm[];
   float* A = sm;
@@ -116,31 +116,33 @@ __global__ void __launch_bounds__(NT) ragged_fwd_simt(const __grid_constant__ Fw
   float* scl = W + BM * SP;  // per row: factor of the old accumulator
   float* den = scl + BM;     // per row: 1 / sum, at the end
   const Geo& g = a.g;
-  const int kvh = blockIdx.y, part = blockIdx.z;
+  const int kvh = blockIdx.y, jb = blockIdx.z / a.nsplit, part = blockIdx.z - jb * a.nsplit;
+  const Job& job = jb ? a.job1 : a.job;
+  const int part0 = jb ? a.part1 : a.part0;
   int tile;
-  const int s = find_slot(g, most_heads(g, a.job.hc), BM, gridDim.x - 1 - blockIdx.x, tile);
+  const int s = find_slot(g, most_heads(g, job.hc), BM, gridDim.x - 1 - blockIdx.x, tile);
   const Seq q = load_seq(g, s);
-  const Heads3 hs = heads_of_group(g, a.job.hc, kvh);
+  const Heads3 hs = heads_of_group(g, job.hc, kvh);
   const int x0 = tile * BM;
   if (hs.n == 0 || x0 >= q.nq * hs.n) return;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const T* qp = static_cast<const T*>(a.q);
-  const T* kp = static_cast<const T*>(a.k);
-  const T* vp = static_cast<const T*>(a.v);
+  const float* qp = static_cast<const float*>(a.q);
+  const float* kp = static_cast<const float*>(a.k);
+  const float* vp = static_cast<const float*>(a.v);
   load_rows<D>(A, qp, [&](int i) {
     QRow r;
-    return query_at(g, q, a.job.qview, hs, x0 + i, r) ? q_row(g, r.t, r.h) : -1;
+    return query_at(g, q, job.qview, hs, x0 + i, r) ? q_row(g, r.t, r.h) : -1;
   });
   float acc[4][D / 16] = {};
   // softmax state of row tid / 4, kept by four threads
   const int row = tid >> 2;
   QRow qr;
-  const bool have = query_at(g, q, a.job.qview, hs, x0 + row, qr);
+  const bool have = query_at(g, q, job.qview, hs, x0 + row, qr);
   float m = -INFINITY, sum = 0.f;
   int cnt[2] = {0, 0}, j0[2] = {0, 0}, total = 0;
-  for (int sg = 0; sg < a.job.nseg; ++sg) {
+  for (int sg = 0; sg < job.nseg; ++sg) {
     int j1;
-    tile_range(g, q, a.job, sg, hs, x0, BM, BN, j0[sg], j1);
+    tile_range(g, q, job, sg, hs, x0, BM, BN, j0[sg], j1);
     cnt[sg] = j1 - j0[sg];
     total += cnt[sg];
   }
@@ -150,10 +152,10 @@ __global__ void __launch_bounds__(NT) ragged_fwd_simt(const __grid_constant__ Fw
   for (int it = (int)((long long)total * part / parts); it < it1; ++it) {
     const int sg = it >= cnt[0] ? 1 : 0;
     const int kb = (j0[sg] + it - (sg ? cnt[0] : 0)) * BN;
-    const int nk = n_keys(q, a.job.seg[sg].kview);
+    const int nk = n_keys(q, job.seg[sg].kview);
     __syncthreads();
     load_rows<D>(B, kp, [&](int i) {
-      return kb + i < nk ? kv_row(g, g.k, q, key_pos(g, q, a.job.seg[sg].kview, kb + i), kvh) : -1;
+      return kb + i < nk ? kv_row(g, g.k, q, key_pos(g, q, job.seg[sg].kview, kb + i), kvh) : -1;
     });
     __syncthreads();
     float sc[4][4] = {};
@@ -164,10 +166,10 @@ __global__ void __launch_bounds__(NT) ragged_fwd_simt(const __grid_constant__ Fw
       for (int j = 0; j < 4; ++j) W[(4 * ty + i) * SP + tx + 16 * j] = sc[i][j] * a.scale_log2;
     __syncthreads();
     load_rows<D>(B, vp, [&](int i) {
-      return kb + i < nk ? kv_row(g, g.v, q, key_pos(g, q, a.job.seg[sg].kview, kb + i), kvh) : -1;
+      return kb + i < nk ? kv_row(g, g.v, q, key_pos(g, q, job.seg[sg].kview, kb + i), kvh) : -1;
     });
     int lo = 0, hi = 0;
-    if (have && qr.pos >= 0) live_keys(g, q, a.job.seg[sg].rule, qr.pos, lo, hi);
+    if (have && qr.pos >= 0) live_keys(g, q, job.seg[sg].rule, qr.pos, lo, hi);
     float mt = -INFINITY;
     for (int x = tid & 3; x < BN; x += 4) {
       const int k = kb + x;
@@ -220,10 +222,10 @@ __global__ void __launch_bounds__(NT) ragged_fwd_simt(const __grid_constant__ Fw
     den[row] = wc;
     if (have) {
       if (a.mode == OUT_PARTIAL) {
-        a.parts.lse[(size_t)(a.part0 + part) * g.total * g.H + rr] = out;
+        a.parts.lse[(size_t)(part0 + part) * g.total * g.H + rr] = out;
         if (part == 0)
           for (int p = parts; p < a.nsplit; ++p)
-            a.parts.lse[(size_t)(a.part0 + p) * g.total * g.H + rr] = -INFINITY;
+            a.parts.lse[(size_t)(part0 + p) * g.total * g.H + rr] = -INFINITY;
       } else {
         a.lse[rr] = out;
       }
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(NT) ragged_fwd_simt(const __grid_constant__ Fw
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     QRow r;
-    if (!query_at(g, q, a.job.qview, hs, x0 + 4 * ty + i, r)) continue;
+    if (!query_at(g, q, job.qview, hs, x0 + 4 * ty + i, r)) continue;
     const size_t o = ((size_t)r.t * g.H + r.h) * D;
     const float f = den[4 * ty + i], fp = scl[4 * ty + i];
 #pragma unroll
@@ -241,19 +243,18 @@ __global__ void __launch_bounds__(NT) ragged_fwd_simt(const __grid_constant__ Fw
       const int c = tx + 16 * j;
       float v = acc[i][j] * f;
       if (a.mode == OUT_PARTIAL) {
-        a.parts.o[(size_t)(a.part0 + part) * g.total * g.H * D + o + c] = v;
+        a.parts.o[(size_t)(part0 + part) * g.total * g.H * D + o + c] = v;
       } else {
         if (a.mode == OUT_MERGE && fp > 0.f) v = fmaf(fp, a.parts.o[o + c], v);
-        static_cast<T*>(a.o)[o + c] = round_to<T>(v);
+        static_cast<float*>(a.o)[o + c] = v;
       }
     }
   }
 }
 
 // dQ of 64 query rows: S and dP = dO V^T again, dS = P (dP - delta), dQ += dS K.
-template <int D, class T>
-__global__ void __launch_bounds__(NT) ragged_dq_simt(const __grid_constant__ BwdLaunch a,
-                                                     const __grid_constant__ Job job, int mode) {
+template <int D>
+__global__ void __launch_bounds__(NT) ragged_dq_simt(const __grid_constant__ BwdLaunch a) {
   extern __shared__ float sm[];
   float* A = sm;
   float* A2 = A + BM * (D + 4);
@@ -264,6 +265,7 @@ __global__ void __launch_bounds__(NT) ragged_dq_simt(const __grid_constant__ Bwd
   __shared__ int slo[BM], shi[BM];
   const Geo& g = a.g;
   const int kvh = blockIdx.y;
+  const Job& job = a.qjob[blockIdx.z];
   int tile;
   const int s = find_slot(g, most_heads(g, job.hc), BM, gridDim.x - 1 - blockIdx.x, tile);
   const Seq q = load_seq(g, s);
@@ -271,12 +273,12 @@ __global__ void __launch_bounds__(NT) ragged_dq_simt(const __grid_constant__ Bwd
   const int x0 = tile * BM;
   if (hs.n == 0 || x0 >= q.nq * hs.n) return;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const T *kp = static_cast<const T*>(a.k), *vp = static_cast<const T*>(a.v);
-  load_rows<D>(A, static_cast<const T*>(a.q), [&](int i) {
+  const float *kp = static_cast<const float*>(a.k), *vp = static_cast<const float*>(a.v);
+  load_rows<D>(A, static_cast<const float*>(a.q), [&](int i) {
     QRow r;
     return query_at(g, q, job.qview, hs, x0 + i, r) ? q_row(g, r.t, r.h) : -1;
   });
-  load_rows<D>(A2, static_cast<const T*>(a.dout), [&](int i) {
+  load_rows<D>(A2, static_cast<const float*>(a.dout), [&](int i) {
     QRow r;
     return query_at(g, q, job.qview, hs, x0 + i, r) ? r.t * g.H + r.h : -1;
   });
@@ -336,18 +338,18 @@ __global__ void __launch_bounds__(NT) ragged_dq_simt(const __grid_constant__ Bwd
     for (int j = 0; j < D / 16; ++j) {
       const int c = tx + 16 * j;
       float v = acc[i][j] * a.scale;
-      if (mode == OUT_PARTIAL) {
+      if (a.mode == OUT_PARTIAL) {
         a.dq_part[po + c] = v;
       } else {
-        if (mode == OUT_MERGE) v += a.dq_part[po + c];
-        static_cast<T*>(a.dq)[o + c] = round_to<T>(v);
+        if (a.mode == OUT_MERGE) v += a.dq_part[po + c];
+        static_cast<float*>(a.dq)[o + c] = v;
       }
     }
   }
 }
 
 // dK, dV of 64 keys: S^T, dP^T = V dO^T, P^T and dS^T, dV += P^T dO, dK += dS^T Q.
-template <int D, class T>
+template <int D>
 __global__ void __launch_bounds__(NT) ragged_dkv_simt(const __grid_constant__ BwdLaunch a) {
   extern __shared__ float sm[];
   float* A = sm;
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(NT) ragged_dkv_simt(const __grid_constant__ Bw
   const int k0 = tile * BM, nk = n_keys(q, view);
   if (hs.n == 0 || k0 >= nk) return;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const T *kp = static_cast<const T*>(a.k), *vp = static_cast<const T*>(a.v);
+  const float *kp = static_cast<const float*>(a.k), *vp = static_cast<const float*>(a.v);
   load_rows<D>(A, kp, [&](int i) {
     return k0 + i < nk ? kv_row(g, g.k, q, key_pos(g, q, view, k0 + i), kvh) : -1;
   });
@@ -394,11 +396,11 @@ __global__ void __launch_bounds__(NT) ragged_dkv_simt(const __grid_constant__ Bw
   for (int t = tb; t < te; ++t) {
     const int xb = t * BN;
     __syncthreads();
-    load_rows<D>(B, static_cast<const T*>(a.q), [&](int i) {
+    load_rows<D>(B, static_cast<const float*>(a.q), [&](int i) {
       QRow r;
       return query_at(g, q, job.qview, hs, xb + i, r) ? q_row(g, r.t, r.h) : -1;
     });
-    load_rows<D>(B2, static_cast<const T*>(a.dout), [&](int i) {
+    load_rows<D>(B2, static_cast<const float*>(a.dout), [&](int i) {
       QRow r;
       return query_at(g, q, job.qview, hs, xb + i, r) ? r.t * g.H + r.h : -1;
     });
@@ -436,10 +438,9 @@ __global__ void __launch_bounds__(NT) ragged_dkv_simt(const __grid_constant__ Bw
     for (int j = 0; j < D / 16; ++j) {
       const int c = tx + 16 * j;
       if (direct) {
-        static_cast<T*>(a.dk)[((size_t)t * a.dk_rows.tok + kvh * a.dk_rows.head) * D + c] =
-            round_to<T>(dk[i][j] * a.scale);
-        static_cast<T*>(a.dv)[((size_t)t * a.dv_rows.tok + kvh * a.dv_rows.head) * D + c] =
-            round_to<T>(dv[i][j]);
+        static_cast<float*>(a.dk)[((size_t)t * a.dk_rows.tok + kvh * a.dk_rows.head) * D + c] =
+            dk[i][j] * a.scale;
+        static_cast<float*>(a.dv)[((size_t)t * a.dv_rows.tok + kvh * a.dv_rows.head) * D + c] = dv[i][j];
       } else {
         float* p = a.parts + (((size_t)blockIdx.z * g.total + t) * g.Hkv + kvh) * 2 * D;
         p[c] = dk[i][j] * a.scale;
@@ -449,17 +450,11 @@ __global__ void __launch_bounds__(NT) ragged_dkv_simt(const __grid_constant__ Bw
   }
 }
 
-// Sequence of token row t, or false for a row of no sequence.
+// Sequence of token row t (the warp's), or false for a row of no sequence.
 __device__ __forceinline__ bool seq_of_token(const Geo& g, int t, int& s) {
-  if (t < cu_at(g, 0) || t >= cu_at(g, g.S)) return false;
-  int a = 0, b = g.S - 1;
-  while (a < b) {  // last sequence that starts at or before t
-    const int m = (a + b + 1) >> 1;
-    if (cu_at(g, m) <= t) a = m;
-    else b = m - 1;
-  }
-  s = a;
-  return t < cu_at(g, a + 1);
+  // the last sequence that starts at or before t
+  s = last_true(g.S, [&](int x) { return cu_at(g, x) <= t; });
+  return t >= cu_at(g, s) && t < cu_at(g, s + 1);
 }
 
 constexpr int kJoinRows = 8;  // rows (warps) of a block of the streaming kernels
@@ -548,17 +543,18 @@ __global__ void __launch_bounds__(32 * kJoinRows) join_dkv_kernel(const __grid_c
   }
 }
 
-// One warp per new token and key/value head: 16-byte chunks of the key row and
-// of the value row go to the slot of the token's position. Tokens at negative
-// positions, positions past the page table and pages outside the cache are
-// dropped (the last two are reported).
+// One warp per new token: the 16-byte chunks of its key and value rows, head by
+// head, go to the slot of its position, eight in flight a lane. Tokens at negative
+// positions are dropped; so are positions past the page table and pages outside
+// the cache, which are reported. Bound by the copy itself: 36.8 k tokens of 4 KB
+// (302 MB moved) take 53 us, 5.7 TB/s (a warp per token and head: 111 us, each
+// looking its sequence and page up for 512 bytes).
 __global__ void __launch_bounds__(32 * kJoinRows)
-    cache_append_kernel(const __grid_constant__ Geo g, const Rows kin, const Rows vin,
-                        int row_chunks, const uint4* k, const uint4* v, uint4* kc, uint4* vc) {
-  const long long row = (long long)blockIdx.x * kJoinRows + (threadIdx.x >> 5);
+    cache_append_kernel(const __grid_constant__ Geo g, const Rows kin, const Rows vin, int row_chunks,
+                        FastDiv frow, const uint4* k, const uint4* v, uint4* kc, uint4* vc) {
+  const int t = blockIdx.x * kJoinRows + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (row >= (long long)g.total * g.Hkv) return;
-  const int t = (int)(row / g.Hkv), h = (int)(row - (long long)t * g.Hkv);
+  if (t >= g.total) return;
   int s;
   if (!seq_of_token(g, t, s)) return;
   const int pos = __ldg(g.kv_lens + s) - (cu_at(g, s + 1) - t);
@@ -569,14 +565,28 @@ __global__ void __launch_bounds__(32 * kJoinRows)
     set_status(g.status, ST_ERR_INVALID);
     return;
   }
-  const size_t dst = (size_t)page * g.k.page + (size_t)(pos - pg * g.page_size) * g.k.tok +
-                     (size_t)h * g.k.head;
-  const size_t ks = (size_t)t * kin.tok + h, vs = (size_t)t * vin.tok + h;
-  for (int c = lane; c < 2 * row_chunks; c += 32) {
-    if (c < row_chunks)
-      kc[dst * row_chunks + c] = __ldg(k + ks * row_chunks + c);
-    else
-      vc[dst * row_chunks + c - row_chunks] = __ldg(v + vs * row_chunks + c - row_chunks);
+  const size_t slot = (size_t)page * g.k.page + (size_t)(pos - pg * g.page_size) * g.k.tok;
+  const int n = g.Hkv * row_chunks;  // of K, and of V
+  const uint4* ks = k + (size_t)t * kin.tok * row_chunks;
+  const uint4* vs = v + (size_t)t * vin.tok * row_chunks;
+  for (int c0 = lane; c0 < n; c0 += 128) {
+    uint4 a[4], b[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (c0 + 32 * x < n) {
+        a[x] = __ldg(ks + c0 + 32 * x);
+        b[x] = __ldg(vs + c0 + 32 * x);
+      }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int c = c0 + 32 * x;
+      if (c < n) {
+        const int h = fdiv(c, frow);
+        const size_t dst = (slot + (size_t)h * g.k.head) * row_chunks + (c - h * row_chunks);
+        kc[dst] = a[x];
+        vc[dst] = b[x];
+      }
+    }
   }
 }
 
@@ -585,85 +595,73 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <int D, class T>
+template <int D>
 cudaError_t fwd_t(const FwdLaunch& a) {
   const size_t smem = sizeof(float) * (2 * BM * (D + 4) + BM * SP + 2 * BM);
-  cudaError_t e = allow_smem(ragged_fwd_simt<D, T>, smem);
+  cudaError_t e = allow_smem(ragged_fwd_simt<D>, smem);
   if (e != cudaSuccess) return e;
   const long long slots = slot_count(a.g, most_heads(a.g, a.job.hc), BM);
-  ragged_fwd_simt<D, T><<<dim3((unsigned)slots, a.g.Hkv, a.nsplit), NT, smem, a.stream>>>(a);
+  ragged_fwd_simt<D><<<dim3((unsigned)slots, a.g.Hkv, a.njobs * a.nsplit), NT, smem, a.stream>>>(a);
   return cudaGetLastError();
 }
 
-template <int D, class T>
-cudaError_t dq_t(const BwdLaunch& a, const Job& job, int mode) {
+template <int D>
+cudaError_t dq_t(const BwdLaunch& a) {
   const size_t smem = sizeof(float) * (4 * BM * (D + 4) + BM * SP);
-  cudaError_t e = allow_smem(ragged_dq_simt<D, T>, smem);
+  cudaError_t e = allow_smem(ragged_dq_simt<D>, smem);
   if (e != cudaSuccess) return e;
-  const long long slots = slot_count(a.g, most_heads(a.g, job.hc), BM);
-  ragged_dq_simt<D, T><<<dim3((unsigned)slots, a.g.Hkv), NT, smem, a.stream>>>(a, job, mode);
+  const long long slots = slot_count(a.g, most_heads(a.g, a.qjob[0].hc), BM);
+  ragged_dq_simt<D><<<dim3((unsigned)slots, a.g.Hkv, a.nqjobs), NT, smem, a.stream>>>(a);
   return cudaGetLastError();
 }
 
-template <int D, class T>
+template <int D>
 cudaError_t dkv_t(const BwdLaunch& a) {
   const size_t smem = sizeof(float) * (4 * BM * (D + 4) + 2 * BM * SP);
-  cudaError_t e = allow_smem(ragged_dkv_simt<D, T>, smem);
+  cudaError_t e = allow_smem(ragged_dkv_simt<D>, smem);
   if (e != cudaSuccess) return e;
   const long long slots = slot_count(a.g, 1, BM);
-  ragged_dkv_simt<D, T>
+  ragged_dkv_simt<D>
       <<<dim3((unsigned)slots, a.g.Hkv, a.njobs * a.nsplit), NT, smem, a.stream>>>(a);
   return cudaGetLastError();
 }
 
-// f(std::integral_constant-like D, T tag) for the element type and head size
 template <class F>
-cudaError_t pick(int dtype, int d, F f) {
-#define ST_PICK(T)                                      \
-  switch (d) {                                          \
-    case 32: return f.template run<32, T>();            \
-    case 64: return f.template run<64, T>();            \
-    case 128: return f.template run<128, T>();          \
+cudaError_t pick(int d, F f) {
+  switch (d) {
+    case 32: return f.template run<32>();
+    case 64: return f.template run<64>();
+    case 128: return f.template run<128>();
   }
-  if (dtype == ST_F32) {
-    ST_PICK(float)
-  } else if (dtype == ST_BF16) {
-    ST_PICK(__nv_bfloat16)
-  } else {
-    ST_PICK(__half)
-  }
-#undef ST_PICK
   return cudaErrorInvalidValue;
 }
 
 struct RunFwd {
   const FwdLaunch& a;
-  template <int D, class T>
-  cudaError_t run() { return fwd_t<D, T>(a); }
+  template <int D>
+  cudaError_t run() { return fwd_t<D>(a); }
 };
 struct RunDq {
   const BwdLaunch& a;
-  const Job& job;
-  int mode;
-  template <int D, class T>
-  cudaError_t run() { return dq_t<D, T>(a, job, mode); }
+  template <int D>
+  cudaError_t run() { return dq_t<D>(a); }
 };
 struct RunDkv {
   const BwdLaunch& a;
-  template <int D, class T>
-  cudaError_t run() { return dkv_t<D, T>(a); }
+  template <int D>
+  cudaError_t run() { return dkv_t<D>(a); }
 };
 
 unsigned join_blocks(long long rows) { return (unsigned)((rows + kJoinRows - 1) / kJoinRows); }
 
 }  // namespace
 
-cudaError_t simt_ragged_fwd(const FwdLaunch& a, int dtype) { return pick(dtype, a.g.d, RunFwd{a}); }
-cudaError_t simt_ragged_dq(const BwdLaunch& a, const Job& job, int mode, int dtype) {
-  return pick(dtype, a.g.d, RunDq{a, job, mode});
+cudaError_t simt_ragged_fwd(const FwdLaunch& a) { return pick(a.g.d, RunFwd{a}); }
+cudaError_t simt_ragged_dq(const BwdLaunch& a) {
+  return pick(a.g.d, RunDq{a});
 }
-cudaError_t simt_ragged_dkv(const BwdLaunch& a, int dtype) {
-  return pick(dtype, a.g.d, RunDkv{a});
+cudaError_t simt_ragged_dkv(const BwdLaunch& a) {
+  return pick(a.g.d, RunDkv{a});
 }
 
 cudaError_t join_parts(const Geo& g, int dtype, const Parts& parts, int nparts, void* o,
@@ -712,9 +710,9 @@ cudaError_t join_dkv(const BwdLaunch& a, int dtype) {
 
 cudaError_t cache_append(const Geo& g, const Rows& kin, const Rows& vin, int elem_bytes,
                          const void* k, const void* v, void* kc, void* vc, cudaStream_t s) {
-  const unsigned nb = join_blocks((long long)g.total * g.Hkv);
-  cache_append_kernel<<<nb, 32 * kJoinRows, 0, s>>>(
-      g, kin, vin, g.d * elem_bytes / 16, static_cast<const uint4*>(k),
+  const int row_chunks = g.d * elem_bytes / 16;
+  cache_append_kernel<<<join_blocks(g.total), 32 * kJoinRows, 0, s>>>(
+      g, kin, vin, row_chunks, make_fastdiv(row_chunks), static_cast<const uint4*>(k),
       static_cast<const uint4*>(v), static_cast<uint4*>(kc), static_cast<uint4*>(vc));
   return cudaGetLastError();
 }

@@ -193,7 +193,7 @@ struct Unit {
   int32_t live;  // 0: no more units
   Seq q;
   Heads3 hs;
-  int32_t kvh, x0, part, parts;  // parts: how many its keys are cut into
+  int32_t kvh, job, x0, part, parts;  // parts: how many its keys are cut into
   int32_t t0, t1;          // key tiles of this unit
   int32_t cnt0;            // of segment 0
   int32_t u0[2];           // first tile of each segment
@@ -211,10 +211,15 @@ __device__ __forceinline__ bool half_meets(const Unit& u, int w, int seg, int j)
 // Decodes unit number n into *out (by a whole warp); false if it has no rows.
 // Slots are taken from the last to the first: a sequence's last tiles have the
 // most keys.
-__device__ __forceinline__ bool decode_unit(const Geo& g, const Job& job, int nsplit, int least,
-                                            int slots, int n, int rows, Unit* out) {
+__device__ __forceinline__ bool decode_unit(const FwdLaunch& a, int slots, int n, int rows, Unit* out) {
+  const Geo& g = a.g;
+  const int nsplit = a.nsplit, least = a.least;
   const int lane = threadIdx.x & 31;
-  const int part = n % nsplit, m = n / nsplit;
+  const int part = n % nsplit;
+  int m = n / nsplit;
+  const int jb = m % a.njobs;
+  m /= a.njobs;
+  const Job& job = jb ? a.job1 : a.job;
   const int kvh = m % g.Hkv, slot = slots - 1 - m / g.Hkv;
   int tile;
   const int s = find_slot(g, most_heads(g, job.hc), rows, slot, tile);
@@ -229,24 +234,25 @@ __device__ __forceinline__ bool decode_unit(const Geo& g, const Job& job, int ns
     tile_range(g, q, job, sg, hs, x0 + w * kNeed, kNeed, kNeed, j0, j1);
   // both halves together: rows follow one another, and so do their intervals
   const int o0 = __shfl_xor_sync(0xffffffffu, j0, 2), o1 = __shfl_xor_sync(0xffffffffu, j1, 2);
-  int a = j0, b = j1;
+  int u0 = j0, u1 = j1;
   if (o1 > o0) {
-    a = j1 > j0 ? imin(j0, o0) : o0;
-    b = j1 > j0 ? imax(j1, o1) : o1;
+    u0 = j1 > j0 ? imin(j0, o0) : o0;
+    u1 = j1 > j0 ? imax(j1, o1) : o1;
   }
-  const int cnt = b - a;
+  const int cnt = u1 - u0;
   const int total = __shfl_sync(0xffffffffu, cnt, 0) + __shfl_sync(0xffffffffu, cnt, 1);
   const int parts = parts_of(total, nsplit, least);
   if (part >= parts) return false;
   if (lane < 4) {
     out->ja[w][sg] = j0;
     out->jb[w][sg] = j1;
-    if (lane < 2) out->u0[sg] = a;
+    if (lane < 2) out->u0[sg] = u0;
     if (lane == 0) {
       out->live = 1;
       out->q = q;
       out->hs = hs;
       out->kvh = kvh;
+      out->job = jb;
       out->x0 = x0;
       out->part = part;
       out->cnt0 = cnt;
