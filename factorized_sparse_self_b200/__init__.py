@@ -376,28 +376,51 @@ def _rows_out(t, name, shape, dtype, like):
 
 
 def _call_stream(stream, like):
-    """The CUDA stream of a call, and a context in which what the call allocates belongs to that
-    stream, so that the memory is not handed out again before the call's work is done."""
-    import contextlib
-
+    """The CUDA stream of a call (an integer)."""
     import torch
-    if torch.cuda.current_device() != like.device.index:
+    dev = like.device.index
+    if torch.cuda.current_device() != dev:
         raise ValueError(f"tensors are on {like.device}, which is not the current device")
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream, contextlib.nullcontext()
-    return stream.cuda_stream, torch.cuda.stream(stream)
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _raw_stream(dev):
+    # the current stream without the object around it (a fifth of the binding's time)
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _on(stream):
+    """What a call allocates for itself belongs to its stream: the memory is not handed out again
+    before the call's work is done."""
+    import torch
+    return torch.cuda.stream(stream)
+
+
+def _outputs(q, o, lse):
+    import torch
+    if o is None:
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if lse is None:
+        lse = q.new_empty(q.shape[:2], dtype=torch.float32)
+    return o, lse
 
 
 def _work(workspace, nbytes, like):
-    """(tensor to keep, address, bytes) of a workspace."""
+    """A workspace of nbytes, the caller's if given (None: none needed)."""
     import torch
     if workspace is None:
-        if nbytes == 0:
-            return None, None, 0
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    elif workspace.device != like.device or not workspace.is_contiguous():
+        return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+    if workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the tensors' device")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace
+
+
+def _work_args(workspace):
+    if workspace is None:
+        return None, 0
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _packed_desc(q, k, v, cu_seqlens):
@@ -432,18 +455,17 @@ def st_packed_attn_fwd(pattern: Pattern, q, k, v, cu_seqlens, max_len, scale=Non
     cu = _ints(cu_seqlens, "cu_seqlens", x.n_seqs + 1, q)
     code, pat = _dtype_code(q), pattern._desc(max_len)
     nb = _packed_workspace("st_packed_attn_fwd_workspace", pat, code, x)
-    sp, ctx = _call_stream(stream, q)
-    with ctx:
-        if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        keep, ws, wn = _work(workspace, nb, q)
-        _check(lib().st_packed_attn_fwd(ctypes.byref(pat), code, ctypes.byref(x),
-                                        float(scale) if scale else 0.0, q.data_ptr(), k.data_ptr(),
-                                        v.data_ptr(), cu, _rows_out(o, "o", q.shape, q.dtype, q),
-                                        _rows_out(lse, "lse", q.shape[:2], torch.float32, q), ws, wn,
-                                        sp), "st_packed_attn_fwd")
+    sp = _call_stream(stream, q)
+    if stream is None:
+        (o, lse), work = _outputs(q, o, lse), _work(workspace, nb, q)
+    else:
+        with _on(stream):
+            (o, lse), work = _outputs(q, o, lse), _work(workspace, nb, q)
+    _check(lib().st_packed_attn_fwd(ctypes.byref(pat), code, ctypes.byref(x),
+                                    float(scale) if scale else 0.0, q.data_ptr(), k.data_ptr(),
+                                    v.data_ptr(), cu, _rows_out(o, "o", q.shape, q.dtype, q),
+                                    _rows_out(lse, "lse", q.shape[:2], torch.float32, q),
+                                    *_work_args(work), sp), "st_packed_attn_fwd")
     return o, lse
 
 
@@ -461,25 +483,28 @@ def st_packed_attn_bwd(pattern: Pattern, q, k, v, o, lse, dout, cu_seqlens, max_
     cu = _ints(cu_seqlens, "cu_seqlens", x.n_seqs + 1, q)
     code, pat = _dtype_code(q), pattern._desc(max_len)
     nb = _packed_workspace("st_packed_attn_bwd_workspace", pat, code, x)
-    sp, ctx = _call_stream(stream, q)
-    with ctx:
-        if dq is None:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if dk is None:
-            dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-        if dv is None:
-            dv = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-        x.dq_stride = _tokens(dq, "dq", q, x.H)
-        x.dk_stride = _tokens(dk, "dk", q, x.Hkv)
-        x.dv_stride = _tokens(dv, "dv", q, x.Hkv)
-        keep, ws, wn = _work(workspace, nb, q)
-        _check(lib().st_packed_attn_bwd(ctypes.byref(pat), code, ctypes.byref(x),
-                                        float(scale) if scale else 0.0, q.data_ptr(), k.data_ptr(),
-                                        v.data_ptr(), _rows_out(o, "o", q.shape, q.dtype, q),
-                                        _rows_out(lse, "lse", q.shape[:2], torch.float32, q),
-                                        _rows_out(dout, "dout", q.shape, q.dtype, q), cu,
-                                        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws, wn, sp),
-               "st_packed_attn_bwd")
+    sp = _call_stream(stream, q)
+
+    def buffers():
+        like = [torch.empty_like(t, memory_format=torch.contiguous_format) if g is None else g
+                for t, g in ((q, dq), (k, dk), (v, dv))]
+        return like, _work(workspace, nb, q)
+
+    if stream is None:
+        (dq, dk, dv), work = buffers()
+    else:
+        with _on(stream):
+            (dq, dk, dv), work = buffers()
+    x.dq_stride = _tokens(dq, "dq", q, x.H)
+    x.dk_stride = _tokens(dk, "dk", q, x.Hkv)
+    x.dv_stride = _tokens(dv, "dv", q, x.Hkv)
+    _check(lib().st_packed_attn_bwd(ctypes.byref(pat), code, ctypes.byref(x),
+                                    float(scale) if scale else 0.0, q.data_ptr(), k.data_ptr(),
+                                    v.data_ptr(), _rows_out(o, "o", q.shape, q.dtype, q),
+                                    _rows_out(lse, "lse", q.shape[:2], torch.float32, q),
+                                    _rows_out(dout, "dout", q.shape, q.dtype, q), cu,
+                                    dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *_work_args(work),
+                                    sp), "st_packed_attn_bwd")
     return dq, dk, dv
 
 
@@ -533,19 +558,18 @@ def st_paged_attn(pattern: Pattern, q, k_cache, v_cache, page_table, cu_q, kv_le
     x, c, (pt, cu, kv) = _paged_args(q, k_cache, v_cache, page_table, cu_q, kv_lens)
     code, pat, max_q = _dtype_code(q), pattern._desc(max_kv), int(max_q)
     nb = _paged_workspace(pat, code, x, c, max_q)
-    sp, ctx = _call_stream(stream, q)
-    with ctx:
-        if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        keep, ws, wn = _work(workspace, nb, q)
-        _check(lib().st_paged_attn(ctypes.byref(pat), code, ctypes.byref(x), ctypes.byref(c), max_q,
-                                   float(scale) if scale else 0.0, q.data_ptr(), k_cache.data_ptr(),
-                                   v_cache.data_ptr(), pt, cu, kv,
-                                   _rows_out(o, "o", q.shape, q.dtype, q),
-                                   _rows_out(lse, "lse", q.shape[:2], torch.float32, q), ws, wn, sp),
-               "st_paged_attn")
+    sp = _call_stream(stream, q)
+    if stream is None:
+        (o, lse), work = _outputs(q, o, lse), _work(workspace, nb, q)
+    else:
+        with _on(stream):
+            (o, lse), work = _outputs(q, o, lse), _work(workspace, nb, q)
+    _check(lib().st_paged_attn(ctypes.byref(pat), code, ctypes.byref(x), ctypes.byref(c), max_q,
+                               float(scale) if scale else 0.0, q.data_ptr(), k_cache.data_ptr(),
+                               v_cache.data_ptr(), pt, cu, kv,
+                               _rows_out(o, "o", q.shape, q.dtype, q),
+                               _rows_out(lse, "lse", q.shape[:2], torch.float32, q),
+                               *_work_args(work), sp), "st_paged_attn")
     return o, lse
 
 
@@ -560,7 +584,7 @@ def st_cache_append(k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens, str
     if cache_heads != Hkv:
         raise ValueError("k and the cache differ in their number of heads")
     x = _PackedDesc(S, total, Hkv, Hkv, d, 0, ks, vs, 0, 0, 0)
-    sp, _ = _call_stream(stream, k)
+    sp = _call_stream(stream, k)
     _check(lib().st_cache_append(_dtype_code(k), ctypes.byref(x), ctypes.byref(c), k.data_ptr(),
                                  v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                  _ints(page_table, "page_table", S * c.max_pages, k),
