@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 ? 3 : 2)
       // rows behind the last key repeat it (their weights are 0, and 0 times an
       // infinity in an unused slot would not be)
       const int e = imin(j * kKeys + (lane & 15), n_keys(q, view) - 1);
-      const int r = kv_row(g, g.k, q, key_pos(g, q, view, e), kvh);
+      const int r = k_row(g, q, key_pos(g, q, view, e), kvh);
       const uint32_t dst = ring + (i % NS) * (2 * TB);
       const int chunk = lane % CH, sub = lane / CH;
 #pragma unroll

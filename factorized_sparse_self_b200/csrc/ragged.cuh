@@ -314,18 +314,36 @@ __device__ __forceinline__ int find_slot(const Geo& g, int mult, int BM, int slo
   return s;
 }
 
-// Row (in units of d elements) of key position j, key/value head kvh, of k or v
-// (r = g.k or g.v). A page number outside the cache is reported and read as
+// Page number pg of a sequence; one outside the cache is reported and read as
 // page 0.
-__device__ __forceinline__ int kv_row(const Geo& g, const Rows& r, const Seq& q, int j, int kvh) {
-  if (!g.kv_lens) return (q.qb + j) * r.tok + kvh * r.head;
-  const int pg = fdiv(j, g.fpage);
+__device__ __forceinline__ int page_of(const Geo& g, const Seq& q, int pg) {
   int page = __ldg(g.table + (size_t)q.s * g.max_pages + pg);
   if ((unsigned)page >= (unsigned)g.num_pages) {
     set_status(g.status, ST_ERR_INVALID);
     page = 0;
   }
-  return page * r.page + (j - pg * g.page_size) * r.tok + kvh * r.head;
+  return page;
+}
+
+// Rows (in units of d elements) of key position j, key/value head kvh, of k and v.
+__device__ __forceinline__ void kv_rows(const Geo& g, const Seq& q, int j, int kvh, int& rk, int& rv) {
+  if (!g.kv_lens) {
+    rk = (q.qb + j) * g.k.tok + kvh * g.k.head;
+    rv = (q.qb + j) * g.v.tok + kvh * g.v.head;
+    return;
+  }
+  const int pg = fdiv(j, g.fpage);
+  rk = rv = page_of(g, q, pg) * g.k.page + (j - pg * g.page_size) * g.k.tok + kvh * g.k.head;
+}
+__device__ __forceinline__ int k_row(const Geo& g, const Seq& q, int j, int kvh) {
+  int rk, rv;
+  kv_rows(g, q, j, kvh, rk, rv);
+  return rk;
+}
+__device__ __forceinline__ int v_row(const Geo& g, const Seq& q, int j, int kvh) {
+  int rk, rv;
+  kv_rows(g, q, j, kvh, rk, rv);
+  return rv;
 }
 
 // Row of token t (absolute), query head h.

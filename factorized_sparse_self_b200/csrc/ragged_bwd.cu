@@ -28,13 +28,15 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kSched = 2;
-constexpr uint32_t kRegsCompute = 208, kRegsIssue = 88;  // 168 at launch: 2 * 208 + 88 = 3 * 168
+constexpr uint32_t kRegsCompute = 200, kRegsIssue = 104;  // 168 at launch: 2 * 200 + 104 = 3 * 168
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
 struct Cfg {
   static constexpr int kTileBytes = 128 * D * 2;
-  static constexpr int kStages = D == 64 ? 8 : 5;
+  // ring slots of the first streamed operand (K or Q, held until the tile's last
+  // product) and of the second (V or dO, let go earlier)
+  static constexpr int kA = D == 64 ? 4 : 3, kB = D == 64 ? 4 : 2;
 };
 
 // 128 rows of one (sequence, key/value head): query rows or keys.
@@ -52,10 +54,10 @@ struct BUnit {
 template <int D>
 struct alignas(1024) Smem {
   uint8_t res[2][Cfg<D>::kTileBytes];  // Q, dO or K, V
-  uint8_t ring[Cfg<D>::kStages][Cfg<D>::kTileBytes];
+  uint8_t ring[Cfg<D>::kA + Cfg<D>::kB][Cfg<D>::kTileBytes];
   float nlse[2][128], ndel[2][128];    // key-major: -LSE log2(e) and -D of a tile's query rows
   uint64_t r_full, r_empty;
-  uint64_t full[Cfg<D>::kStages], empty[Cfg<D>::kStages];
+  uint64_t full[Cfg<D>::kA + Cfg<D>::kB], empty[Cfg<D>::kA + Cfg<D>::kB];
   uint64_t s_full[2], dp_full, p_ready, ds_ready, acc_full;
   uint64_t row_full[2], row_empty[2];
   uint64_t sched_full[kSched], sched_empty[kSched];
@@ -65,11 +67,6 @@ struct alignas(1024) Smem {
   BUnit unit[kSched];
   uint32_t tmem;
   int abort;
-};
-
-// Boxes of the streamed operands: K, V of one head, or Q, dO of a group's heads.
-struct Maps {
-  CUtensorMap b1, b2;
 };
 
 // Query-major unit n of the query jobs (all segments), or key-major unit n.
@@ -142,10 +139,10 @@ __device__ __forceinline__ bool decode(const BwdLaunch& a, int slots, int n, BUn
 
 template <int D, bool F16, bool DKV>
 __global__ void __launch_bounds__(kThreads, 1)
-    ragged_bwd_tc(const __grid_constant__ BwdLaunch a, const __grid_constant__ Maps maps, int slots, int boxes) {
+    ragged_bwd_tc(const __grid_constant__ BwdLaunch a, const __grid_constant__ TileMaps maps, int slots) {
   extern __shared__ __align__(1024) uint8_t raw[];
   Smem<D>& S = *reinterpret_cast<Smem<D>*>(raw);
-  constexpr int NS = Cfg<D>::kStages, TB = Cfg<D>::kTileBytes;
+  constexpr int NA = Cfg<D>::kA, NB = Cfg<D>::kB, NS = NA + NB, TB = Cfg<D>::kTileBytes;
   constexpr uint32_t kDP = DKV ? 128 : 256, kDQ = 384, kDV = 256, kDK = 256 + D;
   const Geo& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -233,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp != 9) {
       // ---------------- producers ----------------
       const int pw = warp == 8 ? 0 : 1;  // rows 64 pw .. of every tile
-      int used = 0, kt = 0, tt = 0;      // units with tiles, ring slots filled, tiles
+      int used = 0, tt = 0;              // units with tiles, tiles
       bool ok = true;
       Gathers gath;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -258,8 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           auto key_rows = [&](int view, int e, int& rk, int& rv) {
             const int pos = key_pos(g, u.q, view, imin(e, n_keys(u.q, view) - 1));
-            rk = kv_row(g, g.k, u.q, pos, u.kvh);
-            rv = kv_row(g, g.v, u.q, pos, u.kvh);
+            kv_rows(g, u.q, pos, u.kvh, rk, rv);
           };
           if (used > 0 && !wait(&S.r_empty, (used - 1) & 1)) break;
           ++used;
@@ -276,24 +272,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             gath.add(&S.r_full);
           }
           for (int t = u.t0; t < u.t1; ++t, ++tt) {
-            int view = 0, j = t, bh, bt;
-            bool box;
+            int view = 0, j = t, R;
             if constexpr (DKV) {
-              // rows (query, head of the group) in natural order: 128 / G tokens
-              box = boxes && job.qview == VIEW_NAT && j * 128 + 128 <= xrows;
-              bh = u.hs.first;
-              bt = u.q.qb + j * boxes;
+              R = job.qview == VIEW_NAT && j * 128 + 128 <= xrows ? maps.q_tokens : 0;
             } else {
               const int seg = t >= u.cnt0 ? 1 : 0;
               j = u.u0[seg] + t - (seg ? u.cnt0 : 0);
               view = job.seg[seg].kview;
-              box = view == VIEW_NAT && j * 128 + 128 <= u.q.nk;
-              bh = u.kvh;
-              bt = u.q.qb + j * 128;
+              R = box_rows(maps, g, u.q, view, j);
             }
             int ra[2], rb[2];
             float vl[2], vd[2];
-            if (DKV || !box) {
+            if (DKV || !R) {
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 const int e = j * 128 + pw * 64 + y * 32 + lane;
@@ -312,25 +302,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i, ++kt) {
-              const int s = kt % NS;
-              if (kt >= NS && !wait(&S.empty[s], (kt / NS + 1) & 1)) break;
-              if (box) {
-                gath.flush();
-                if (lane == 0) {
-                  if (pw == 0) {
-                    mbar_arrive_expect_tx(&S.full[s], TB);
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                      tma_box(smem_u32(S.ring[s]) + c * 16384, i ? &maps.b2 : &maps.b1, &S.full[s], c * 64, bh, bt);
-                  } else {
-                    mbar_arrive(&S.full[s]);
-                  }
-                }
-              } else {
+            for (int i = 0; i < 2; ++i) {
+              const int NR = i ? NB : NA, s = (i ? NA : 0) + tt % NR;
+              if (tt >= NR && !wait(&S.empty[s], (tt / NR + 1) & 1)) break;
+              if (!R) {
                 gather64<D>(smem_u32(S.ring[s]), pw * 64, DKV ? (i ? a.dout : a.q) : (i ? a.v : a.k),
                             i ? rb[0] : ra[0], i ? rb[1] : ra[1]);
                 gath.add(&S.full[s]);
+              } else {
+                gath.flush();
+                if (pw == 1) {
+                  if (lane == 0) mbar_arrive(&S.full[s]);
+                } else if (DKV) {
+                  load_query_boxes<D>(smem_u32(S.ring[s]), i ? &maps.dout : &maps.q, &S.full[s], maps, u.q, u.hs,
+                                      j * 128);
+                } else {
+                  load_boxes<D>(smem_u32(S.ring[s]), maps, i, &S.full[s], g, u.q, view, j, u.kvh, R);
+                }
               }
               if (DKV && i == 0) {
                 const int b = tt & 1;
@@ -355,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) {
         if (lane == 0) fail();
         // copies in flight land before the CTA may exit
-        for (int i = imax(0, kt - NS); i < kt; ++i) mbar_wait_drain(&S.full[i % NS], (i / NS) & 1, limit);
+        for (int i = imax(0, tt - NA); i <= tt; ++i) mbar_wait_drain(&S.full[i % NA], (i / NA) & 1, limit);
+        for (int i = imax(0, tt - NB); i <= tt; ++i) mbar_wait_drain(&S.full[NA + i % NB], (i / NB) & 1, limit);
       }
     } else {
       // ---------------- MMA issuer ----------------
@@ -370,14 +359,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       const uint64_t a1 = sdesc(smem_u32(S.res[0]), 16, 1024), a2 = sdesc(smem_u32(S.res[1]), 16, 1024);
       const uint64_t bk = sdesc(smem_u32(S.ring[0]), 16, 1024), bm = sdesc(smem_u32(S.ring[0]), 16384, 1024);
-      int kt = 0, used = 0;  // ring slots of finished units, units with tiles
-      uint32_t ts = 0;       // tiles so far
-      // ring slot i of the unit
-      auto slot = [&](int i) { return (kt + i) % NS; };
-      auto wait_slot = [&](int i) { wait(&S.full[slot(i)], ((kt + i) / NS) & 1); };
-      // scores: resident tile (ad) times ring slot i, transposed operands K-major
+      int used = 0;     // units with tiles
+      uint32_t ts = 0;  // tiles so far
+      // ring slots of tile t (counted from the first): its first operand, its second
+      auto slot_a = [&](uint32_t t) { return (int)(t % NA); };
+      auto slot_b = [&](uint32_t t) { return NA + (int)(t % NB); };
+      auto wait_a = [&](uint32_t t) { wait(&S.full[slot_a(t)], (t / NA) & 1); };
+      auto wait_b = [&](uint32_t t) { wait(&S.full[slot_b(t)], (t / NB) & 1); };
+      // scores: resident tile (ad) times ring slot i, both K-major
       auto scores = [&](uint64_t ad, int i, uint32_t col, uint64_t* bar) {
-        const uint64_t bd = sdesc_at(bk, slot(i) * TB);
+        const uint64_t bd = sdesc_at(bk, i * TB);
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -391,14 +382,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // accumulator (col) += weights (16-bit, 64 keys or rows at columns w and w + 64) times
       // ring slot i, which is let go
       auto weigh = [&](uint32_t w, int i, uint32_t col, bool fresh, uint64_t* more) {
-        const uint64_t bd = sdesc_at(bm, slot(i) * TB);
+        const uint64_t bd = sdesc_at(bm, i * TB);
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int x = 0; x < 8; ++x)
             mma_ts(tmem + col, tmem + w + (x & 3) * 8 + (x >> 2) * 64, sdesc_at(bd, x * 2048), idA,
                    !fresh || x > 0);
-          mma_commit(&S.empty[slot(i)]);
+          mma_commit(&S.empty[i]);
           if (more) mma_commit(more);
         }
         __syncwarp();
@@ -418,56 +409,53 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(&S.r_full, used & 1);
           ++used;
           if constexpr (!DKV) {
-            // ring: K0 V0 K1 V1 ...
-            wait_slot(0);
-            scores(a1, 0, (ts & 1) * 128, &S.s_full[ts & 1]);
-            wait_slot(1);
-            scores(a2, 1, kDP, &S.dp_full);
-            commit(&S.empty[slot(1)]);
+            wait_a(ts);
+            scores(a1, slot_a(ts), (ts & 1) * 128, &S.s_full[ts & 1]);
+            wait_b(ts);
+            scores(a2, slot_b(ts), kDP, &S.dp_full);
+            commit(&S.empty[slot_b(ts)]);
             if (T > 1) {
-              wait_slot(2);
-              scores(a1, 2, ((ts + 1) & 1) * 128, &S.s_full[(ts + 1) & 1]);
+              wait_a(ts + 1);
+              scores(a1, slot_a(ts + 1), ((ts + 1) & 1) * 128, &S.s_full[(ts + 1) & 1]);
             } else {
               commit(&S.r_empty);
             }
             for (int t = 0; t < T; ++t, ++ts) {
-              if (t + 1 < T) wait_slot(2 * t + 3);
+              if (t + 1 < T) wait_b(ts + 1);
               wait(&S.ds_ready, ts & 1);
               if (t + 1 < T) {
-                scores(a2, 2 * t + 3, kDP, &S.dp_full);
-                commit(&S.empty[slot(2 * t + 3)]);
+                scores(a2, slot_b(ts + 1), kDP, &S.dp_full);
+                commit(&S.empty[slot_b(ts + 1)]);
                 if (t + 2 == T) commit(&S.r_empty);
               }
-              weigh((ts & 1) * 128, 2 * t, kDQ, t == 0, t + 1 == T ? &S.acc_full : nullptr);
+              weigh((ts & 1) * 128, slot_a(ts), kDQ, t == 0, t + 1 == T ? &S.acc_full : nullptr);
               if (t + 2 < T) {
-                wait_slot(2 * t + 4);
-                scores(a1, 2 * t + 4, (ts & 1) * 128, &S.s_full[ts & 1]);
+                wait_a(ts + 2);
+                scores(a1, slot_a(ts + 2), (ts & 1) * 128, &S.s_full[ts & 1]);
               }
             }
           } else {
-            // ring: Q0 dO0 Q1 dO1 ...
-            wait_slot(0);
-            scores(a1, 0, 0, &S.s_full[0]);
-            wait_slot(1);
-            scores(a2, 1, kDP, &S.dp_full);
+            wait_a(ts);
+            scores(a1, slot_a(ts), 0, &S.s_full[0]);
+            wait_b(ts);
+            scores(a2, slot_b(ts), kDP, &S.dp_full);
             if (T == 1) commit(&S.r_empty);
             for (int t = 0; t < T; ++t, ++ts) {
-              if (t + 1 < T) wait_slot(2 * t + 2);
+              if (t + 1 < T) wait_a(ts + 1);
               wait(&S.p_ready, ts & 1);
-              weigh(0, 2 * t + 1, kDV, t == 0, nullptr);
+              weigh(0, slot_b(ts), kDV, t == 0, nullptr);
               if (t + 1 < T) {
-                scores(a1, 2 * t + 2, 0, &S.s_full[0]);
-                wait_slot(2 * t + 3);
+                scores(a1, slot_a(ts + 1), 0, &S.s_full[0]);
+                wait_b(ts + 1);
               }
               wait(&S.ds_ready, ts & 1);
-              weigh(kDP, 2 * t, kDK, t == 0, t + 1 == T ? &S.acc_full : nullptr);
+              weigh(kDP, slot_a(ts), kDK, t == 0, t + 1 == T ? &S.acc_full : nullptr);
               if (t + 1 < T) {
-                scores(a2, 2 * t + 3, kDP, &S.dp_full);
+                scores(a2, slot_b(ts + 1), kDP, &S.dp_full);
                 if (t + 2 == T) commit(&S.r_empty);
               }
             }
           }
-          kt += 2 * T;
         }
         if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
         __syncwarp();
@@ -696,21 +684,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, bool F16, bool DKV>
 cudaError_t launch(const BwdLaunch& a) {
   const Geo& g = a.g;
-  Maps m = {};
-  int boxes = 0;  // tokens of a box
-  if (DKV) {
-    if (!g.split && 128 % g.G == 0) {
-      boxes = 128 / g.G;
-      if (!make_box_map(&m.b1, a.q, F16, g.total, g.H, g.q.tok, D, g.G) ||
-          !make_box_map(&m.b2, a.dout, F16, g.total, g.H, g.H, D, g.G))
-        return cudaErrorInvalidValue;
-    }
-  } else {
-    boxes = 128;
-    if (!make_box_map(&m.b1, a.k, F16, g.total, g.Hkv, g.k.tok, D) ||
-        !make_box_map(&m.b2, a.v, F16, g.total, g.Hkv, g.v.tok, D))
-      return cudaErrorInvalidValue;
-  }
+  TileMaps m = {};
+  const Rows whole = {g.H, 1, 0};
+  if (DKV ? !make_query_map(&m.q, m, g, g.q, a.q, F16) || !make_query_map(&m.dout, m, g, whole, a.dout, F16)
+          : !make_key_maps(m, g, a.k, a.v, F16))
+    return cudaErrorInvalidValue;
   const size_t smem = sizeof(Smem<D>);
   static_assert(sizeof(Smem<D>) <= 232448, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(ragged_bwd_tc<D, F16, DKV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -719,7 +697,7 @@ cudaError_t launch(const BwdLaunch& a) {
   const long long slots = slot_count(g, DKV ? 1 : most_heads(g, a.qjob[0].hc), 128);
   const long long units = slots * g.Hkv * (DKV ? a.njobs * a.nsplit : a.nqjobs);
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
-  ragged_bwd_tc<D, F16, DKV><<<(unsigned)units, kThreads, smem, a.stream>>>(a, m, (int)slots, boxes);
+  ragged_bwd_tc<D, F16, DKV><<<(unsigned)units, kThreads, smem, a.stream>>>(a, m, (int)slots);
   return cudaGetLastError();
 }
 

@@ -9,8 +9,7 @@
 //   warp 10      scheduler: decodes the CTA's units into a small ring;
 //   warps 8, 11  producers: Q rows, then K and V tiles of 128 rows in turn into
 //                one ring. Rows are gathered through the order's index map and the
-//                page table; 128 consecutive rows of a packed sequence come as a
-//                TMA box. Rows behind the last key repeat it: masked entries have
+//                page table, or come as TMA boxes where they lie evenly. Rows behind the last key repeat it: masked entries have
 //                weight 0 and must not meet another sequence's infinities;
 //   warp 9       MMA issuer: S_h = Q_h K^T (128 x 128 fp32 in TMEM), O_h += P_h V
 //                with P_h read from TMEM; the order S0 S1 | P0V S0' | P1V S1' | ..
@@ -28,7 +27,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kRows = 256;  // query rows of a unit
 constexpr int kSched = 3;   // units decoded ahead
-constexpr uint32_t kRegsSoftmax = 216, kRegsIssue = 72;  // 168 at launch: 2 * 216 + 72 = 3 * 168
+constexpr uint32_t kRegsSoftmax = 208, kRegsIssue = 88;  // 168 at launch: 2 * 208 + 88 = 3 * 168
 constexpr float kRescale = 8.f;  // log2
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -36,13 +35,14 @@ template <int D>
 struct Cfg {
   static constexpr int kTileBytes = 128 * D * 2;
   static constexpr int kStages = D == 64 ? 8 : 5;
+  static constexpr int kQ = D == 64 ? 2 : 1;  // Q buffers (d = 128 has no room for a second)
 };
 
 template <int D>
 struct alignas(1024) Smem {
-  uint8_t q[2][Cfg<D>::kTileBytes];
+  uint8_t q[Cfg<D>::kQ][2][Cfg<D>::kTileBytes];
   uint8_t kv[Cfg<D>::kStages][Cfg<D>::kTileBytes];
-  uint64_t q_full, q_empty;
+  uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[Cfg<D>::kStages], kv_empty[Cfg<D>::kStages];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t sched_full[kSched], sched_empty[kSched];
@@ -54,17 +54,12 @@ struct alignas(1024) Smem {
   int abort;
 };
 
-struct Maps {
-  CUtensorMap kbox, vbox;
-};
-
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
-    ragged_fwd_tc(const __grid_constant__ FwdLaunch a, const __grid_constant__ Maps maps, int slots,
-                  int boxes) {
+    ragged_fwd_tc(const __grid_constant__ FwdLaunch a, const __grid_constant__ TileMaps maps, int slots) {
   extern __shared__ uint8_t raw[];
   Smem<D>& S = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  constexpr int NS = Cfg<D>::kStages, TB = Cfg<D>::kTileBytes;
+  constexpr int NS = Cfg<D>::kStages, TB = Cfg<D>::kTileBytes, QB = Cfg<D>::kQ;
   constexpr uint32_t kColO = 256;
   const Geo& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -72,13 +67,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &S.abort;
   if (threadIdx.x == 0) {
     S.abort = 0;
-    mbar_init(&S.q_full, 2);  // both producers
-    mbar_init(&S.q_empty, 1);
     for (int i = 0; i < NS; ++i) {
       mbar_init(&S.kv_full[i], 2);
       mbar_init(&S.kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.q_full[i], 2);  // both producers
+      mbar_init(&S.q_empty[i], 1);
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.p_full[i], 128);
       mbar_init(&S.o_full[i], 1);
@@ -144,9 +139,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp != 9) {
       // ---------------- producers ----------------
       const int pw = warp == 8 ? 0 : 1;  // loads half pw of the Q rows, rows 64 pw .. of K and V tiles
-      if (pw == 0 && lane == 0) {
-        tma_prefetch_desc(&maps.kbox);
-        tma_prefetch_desc(&maps.vbox);
+      if (pw == 0 && lane == 0 && maps.nat_rows) {
+        tma_prefetch_desc(&maps.k);
+        tma_prefetch_desc(&maps.v);
       }
       int used = 0, kt = 0;  // units with tiles, ring slots filled
       bool ok = true;
@@ -163,57 +158,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Unit& u = S.unit[n % kSched];
         if (u.t1 > u.t0) {
           const Job& job = u.job ? a.job1 : a.job;
-          if (used > 0 && !wait(&S.q_empty, (used - 1) & 1)) break;
+          const int qb = used % QB;
+          if (used >= QB && !wait(&S.q_empty[qb], (used / QB + 1) & 1)) break;
           ++used;
-          const int rows = u.q.nq * u.hs.n;
+          const int rows = u.q.nq * u.hs.n, x0 = u.x0 + pw * 128;
+          if (maps.q_tokens && job.qview == VIEW_NAT && x0 + 128 <= rows) {
+            load_query_boxes<D>(smem_u32(S.q[qb][pw]), &maps.q, &S.q_full[qb], maps, u.q, u.hs, x0);
+          } else {
 #pragma unroll 1
-          for (int i = 0; i < 2; ++i) {
-            int r[2];
+            for (int i = 0; i < 2; ++i) {
+              int r[2];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              QRow qr;
-              query_at(g, u.q, job.qview, u.hs, imin(u.x0 + pw * 128 + i * 64 + y * 32 + lane, rows - 1), qr);
-              r[y] = q_row(g, qr.t, qr.h);
+              for (int y = 0; y < 2; ++y) {
+                QRow qr;
+                query_at(g, u.q, job.qview, u.hs, imin(x0 + i * 64 + y * 32 + lane, rows - 1), qr);
+                r[y] = q_row(g, qr.t, qr.h);
+              }
+              gather64<D>(smem_u32(S.q[qb][pw]), i * 64, a.q, r[0], r[1]);
             }
-            gather64<D>(smem_u32(S.q[pw]), i * 64, a.q, r[0], r[1]);
+            gath.add(&S.q_full[qb]);
           }
-          gath.add(&S.q_full);
           for (int t = u.t0; t < u.t1 && ok; ++t) {
             int seg, j;
             unit_tile(u, t, seg, j);
-            const int view = job.seg[seg].kview, nk = n_keys(u.q, view);
-            if (boxes && view == VIEW_NAT && j * 128 + 128 <= nk) {
-              // consecutive tokens: one TMA box per 64 columns
+            const int view = job.seg[seg].kview, R = box_rows(maps, g, u.q, view, j);
+            int rk[2], rv[2];
+            if (!R) {
 #pragma unroll
-              for (int kv = 0; kv < 2; ++kv, ++kt) {
-                const int s = kt % NS;
-                if (kt >= NS && !wait(&S.kv_empty[s], (kt / NS + 1) & 1)) break;
-                gath.flush();
-                if (lane == 0) {
-                  if (pw == 0) {
-                    mbar_arrive_expect_tx(&S.kv_full[s], TB);
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                      tma_box(smem_u32(S.kv[s]) + c * 16384, kv ? &maps.vbox : &maps.kbox, &S.kv_full[s],
-                              c * 64, u.kvh, u.q.qb + j * 128);
-                  } else {
-                    mbar_arrive(&S.kv_full[s]);
-                  }
-                }
+              for (int y = 0; y < 2; ++y) {
+                const int e = imin(j * 128 + pw * 64 + y * 32 + lane, n_keys(u.q, view) - 1);
+                kv_rows(g, u.q, key_pos(g, u.q, view, e), u.kvh, rk[y], rv[y]);
               }
-            } else {
-              int pos[2];
+            }
 #pragma unroll
-              for (int y = 0; y < 2; ++y)
-                pos[y] = key_pos(g, u.q, view, imin(j * 128 + pw * 64 + y * 32 + lane, nk - 1));
-#pragma unroll
-              for (int kv = 0; kv < 2; ++kv, ++kt) {
-                const int s = kt % NS;
-                const Rows& rw = kv ? g.v : g.k;
-                const int ra = kv_row(g, rw, u.q, pos[0], u.kvh), rb = kv_row(g, rw, u.q, pos[1], u.kvh);
-                if (kt >= NS && !wait(&S.kv_empty[s], (kt / NS + 1) & 1)) break;
-                gather64<D>(smem_u32(S.kv[s]), pw * 64, kv ? a.v : a.k, ra, rb);
+            for (int kv = 0; kv < 2; ++kv, ++kt) {
+              const int s = kt % NS;
+              if (kt >= NS && !wait(&S.kv_empty[s], (kt / NS + 1) & 1)) break;
+              if (!R) {
+                gather64<D>(smem_u32(S.kv[s]), pw * 64, kv ? a.v : a.k, kv ? rv[0] : rk[0], kv ? rv[1] : rk[1]);
                 gath.add(&S.kv_full[s]);
+              } else {
+                gath.flush();
+                if (pw == 0) load_boxes<D>(smem_u32(S.kv[s]), maps, kv, &S.kv_full[s], g, u.q, view, j, u.kvh, R);
+                else if (lane == 0) mbar_arrive(&S.kv_full[s]);
               }
             }
           }
@@ -226,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) {
         if (lane == 0) fail();
         // copies in flight land before the CTA may exit
+        for (int i = imax(0, used - QB); i < used; ++i) mbar_wait_drain(&S.q_full[i % QB], (i / QB) & 1, limit);
         for (int i = imax(0, kt - NS); i < kt; ++i)
           mbar_wait_drain(&S.kv_full[i % NS], (i / NS) & 1, limit);
       }
@@ -242,11 +230,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ok = bar_wait(bar, parity, limit, abort);
         __syncwarp();
       };
-      const uint64_t qd0 = sdesc(smem_u32(S.q[0]), 16, 1024);
+      const uint64_t qd0 = sdesc(smem_u32(S.q[0][0]), 16, 1024);
       const uint64_t kd0 = sdesc(smem_u32(S.kv[0]), 16, 1024);
       const uint64_t vd0 = sdesc(smem_u32(S.kv[0]), 16384, 1024);
-      auto issue_s = [&](int h, int stage) {
-        const uint64_t qd = sdesc_at(qd0, h * TB), kd = sdesc_at(kd0, stage * TB);
+      auto issue_s = [&](int h, int stage, int qb) {
+        const uint64_t qd = sdesc_at(qd0, (2 * qb + h) * TB), kd = sdesc_at(kd0, stage * TB);
         if (elect_one()) {
 #pragma unroll
           for (int x = 0; x < D / 16; ++x)
@@ -281,7 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto meets = [&](int h, int t) {
             return t < t1 && (t < cnt0 ? t >= a0[h] && t < b0[h] : t >= a1[h] && t < b1[h]);
           };
-          wait(&S.q_full, used & 1);
+          const int qb = used % QB;
+          wait(&S.q_full[qb], (used / QB) & 1);
           ++used;
           bool fresh[2] = {true, true};
           bool act[2] = {meets(0, t0), meets(1, t0)};
@@ -289,9 +278,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            if (act[h]) issue_s(h, kt % NS);
+            if (act[h]) issue_s(h, kt % NS, qb);
           commit(&S.kv_empty[kt % NS]);
-          if (t0 + 1 == t1) commit(&S.q_empty);
+          if (t0 + 1 == t1) commit(&S.q_empty[qb]);
           int sv = (kt + 1) % NS, pv = ((kt + 1) / NS) & 1;
           for (int t = t0; t < t1; ++t, kt += 2) {
             int sk = sv + 1, pk = pv;
@@ -322,12 +311,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 fresh[h] = false;
               }
-              if (nact[h]) issue_s(h, sk);
+              if (nact[h]) issue_s(h, sk, qb);
             }
             commit(&S.kv_empty[sv]);
             if (more) {
               commit(&S.kv_empty[sk]);
-              if (t + 2 == t1) commit(&S.q_empty);
+              if (t + 2 == t1) commit(&S.q_empty[qb]);
             }
             act[0] = nact[0];
             act[1] = nact[1];
@@ -523,10 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, bool F16>
 cudaError_t launch(const FwdLaunch& a) {
   const Geo& g = a.g;
-  Maps m = {};
-  const bool boxes = !g.kv_lens;
-  if (boxes && (!make_box_map(&m.kbox, a.k, F16, g.total, g.Hkv, g.k.tok, D) ||
-                !make_box_map(&m.vbox, a.v, F16, g.total, g.Hkv, g.v.tok, D)))
+  TileMaps m = {};
+  if (!make_key_maps(m, g, a.k, a.v, F16) || !make_query_map(&m.q, m, g, g.q, a.q, F16))
     return cudaErrorInvalidValue;
   const size_t smem = sizeof(Smem<D>) + 1024;
   static_assert(sizeof(Smem<D>) + 1024 <= 232448, "shared memory");
@@ -536,7 +523,7 @@ cudaError_t launch(const FwdLaunch& a) {
   const long long slots = slot_count(g, most_heads(g, a.job.hc), kRows);
   const long long units = slots * g.Hkv * a.njobs * a.nsplit;
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
-  ragged_fwd_tc<D, F16><<<(unsigned)units, kThreads, smem, a.stream>>>(a, m, (int)slots, boxes);
+  ragged_fwd_tc<D, F16><<<(unsigned)units, kThreads, smem, a.stream>>>(a, m, (int)slots);
   return cudaGetLastError();
 }
 

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(NT) ragged_fwd_simt(const __grid_constant__ Fw
     const int nk = n_keys(q, job.seg[sg].kview);
     __syncthreads();
     load_rows<D>(B, kp, [&](int i) {
-      return kb + i < nk ? kv_row(g, g.k, q, key_pos(g, q, job.seg[sg].kview, kb + i), kvh) : -1;
+      return kb + i < nk ? k_row(g, q, key_pos(g, q, job.seg[sg].kview, kb + i), kvh) : -1;
     });
     __syncthreads();
     float sc[4][4] = {};
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(NT) ragged_fwd_simt(const __grid_constant__ Fw
       for (int j = 0; j < 4; ++j) W[(4 * ty + i) * SP + tx + 16 * j] = sc[i][j] * a.scale_log2;
     __syncthreads();
     load_rows<D>(B, vp, [&](int i) {
-      return kb + i < nk ? kv_row(g, g.v, q, key_pos(g, q, job.seg[sg].kview, kb + i), kvh) : -1;
+      return kb + i < nk ? v_row(g, q, key_pos(g, q, job.seg[sg].kview, kb + i), kvh) : -1;
     });
     int lo = 0, hi = 0;
     if (have && qr.pos >= 0) live_keys(g, q, job.seg[sg].rule, qr.pos, lo, hi);
@@ -306,10 +306,10 @@ __global__ void __launch_bounds__(NT) ragged_dq_simt(const __grid_constant__ Bwd
       const int kb = j * BN;
       __syncthreads();
       load_rows<D>(B, kp, [&](int i) {
-        return kb + i < nk ? kv_row(g, g.k, q, key_pos(g, q, job.seg[sg].kview, kb + i), kvh) : -1;
+        return kb + i < nk ? k_row(g, q, key_pos(g, q, job.seg[sg].kview, kb + i), kvh) : -1;
       });
       load_rows<D>(B2, vp, [&](int i) {
-        return kb + i < nk ? kv_row(g, g.v, q, key_pos(g, q, job.seg[sg].kview, kb + i), kvh) : -1;
+        return kb + i < nk ? v_row(g, q, key_pos(g, q, job.seg[sg].kview, kb + i), kvh) : -1;
       });
       __syncthreads();
       float sc[4][4] = {}, dp[4][4] = {};
@@ -374,10 +374,10 @@ __global__ void __launch_bounds__(NT) ragged_dkv_simt(const __grid_constant__ Bw
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const float *kp = static_cast<const float*>(a.k), *vp = static_cast<const float*>(a.v);
   load_rows<D>(A, kp, [&](int i) {
-    return k0 + i < nk ? kv_row(g, g.k, q, key_pos(g, q, view, k0 + i), kvh) : -1;
+    return k0 + i < nk ? k_row(g, q, key_pos(g, q, view, k0 + i), kvh) : -1;
   });
   load_rows<D>(A2, vp, [&](int i) {
-    return k0 + i < nk ? kv_row(g, g.v, q, key_pos(g, q, view, k0 + i), kvh) : -1;
+    return k0 + i < nk ? v_row(g, q, key_pos(g, q, view, k0 + i), kvh) : -1;
   });
   if (tid < BM) {
     int x = 0, y = 0;

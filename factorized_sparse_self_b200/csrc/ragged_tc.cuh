@@ -69,16 +69,21 @@ __device__ __forceinline__ void gather64(uint32_t dst, int row0, const void* bas
   const int lane = threadIdx.x & 31;
   const int chunk = lane % CH, sub = lane / CH;
   const uint32_t col = dst + (chunk >> 3) * 16384;
-#pragma unroll 8
-  for (int i = 0; i < 64 / RPI; ++i) {
-    const int x = i * RPI + sub;
-    const int r = __shfl_sync(0xffffffffu, i * RPI < 32 ? ra : rb, x & 31);
-    const char* src = static_cast<const char*>(base) + (size_t)r * (D * 2) + chunk * 16;
-    const int y = row0 + x;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(col + y * 128 +
-                                                                  (((chunk & 7) ^ (y & 7)) << 4)),
-                 "l"(src)
-                 : "memory");
+#pragma unroll 1
+  for (int i0 = 0; i0 < 64 / RPI; i0 += 8) {
+    int r[8];  // eight lookups, then eight copies: one by one each waits for its shuffle
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      r[i] = __shfl_sync(0xffffffffu, (i0 + i) * RPI < 32 ? ra : rb, ((i0 + i) * RPI + sub) & 31);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int y = row0 + (i0 + i) * RPI + sub;
+      const char* src = static_cast<const char*>(base) + (size_t)r[i] * (D * 2) + chunk * 16;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(col + y * 128 +
+                                                                    (((chunk & 7) ^ (y & 7)) << 4)),
+                   "l"(src)
+                   : "memory");
+    }
   }
 }
 __device__ __forceinline__ void gather_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -116,14 +121,72 @@ struct Gathers {
   }
 };
 
-// 64 columns x the map's box of heads and tokens (128 rows).
+// ---- boxes ---------------------------------------------------------------------
+// Rows that lie evenly in memory come as TMA boxes of 64 columns: 128 / R boxes of
+// R rows (a multiple of 8, so each starts on a swizzle boundary).
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c,
-                                        int head, int tok) {
+                                        int head, int row, int outer) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(head), "r"(tok)
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(head), "r"(row),
+      "r"(outer)
       : "memory");
+}
+
+// Maps of one launch. Keys and values: boxes of nat_rows consecutive positions
+// (packed: 128 tokens; paged: within a page) and of the sum_rows = c summary
+// positions of a block (packed only); 0: none. Query-side tensors: boxes of the G
+// heads of q_tokens = 128 / G tokens.
+struct TileMaps {
+  CUtensorMap k, v, ksum, vsum, q, dout;
+  int32_t nat_rows, sum_rows, q_tokens;
+};
+
+// Whether key tile j of an order is made of whole boxes, and their rows.
+__device__ __forceinline__ int box_rows(const TileMaps& m, const Geo& g, const Seq& q, int view, int j) {
+  if (view == VIEW_NAT) return (j + 1) * 128 <= q.nk ? m.nat_rows : 0;
+  if (view == VIEW_SUM) return (j + 1) * 128 <= q.P * g.c ? m.sum_rows : 0;
+  return 0;
+}
+// Loads the tile (one warp; R = box_rows(...) > 0); the barrier gets one arrival.
+template <int D>
+__device__ __forceinline__ void load_boxes(uint32_t dst, const TileMaps& m, bool value, uint64_t* bar,
+                                           const Geo& g, const Seq& q, int view, int j, int kvh, int R) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) mbar_arrive_expect_tx(bar, 128 * D * 2);
+  __syncwarp();
+  if (lane * R < 128) {
+    int row, outer = 0;
+    const CUtensorMap* map = value ? &m.v : &m.k;
+    if (view == VIEW_SUM) {
+      map = value ? &m.vsum : &m.ksum;
+      row = q.qb + (fdiv(j * 128, g.fc) + lane + 1) * g.l - g.c;
+    } else if (!g.kv_lens) {
+      row = q.qb + j * 128;
+    } else {
+      const int pos = j * 128 + lane * R, pg = fdiv(pos, g.fpage);
+      row = pos - pg * g.page_size;
+      outer = page_of(g, q, pg);
+    }
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      tma_box(dst + c * 16384 + lane * R * 128, map, bar, c * 64, kvh, row, outer);
+  }
+  __syncwarp();
+}
+// 128 rows (query, head of the group) from row x0 of a query-side tensor.
+template <int D>
+__device__ __forceinline__ void load_query_boxes(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                                 const TileMaps& m, const Seq& q, const Heads3& hs, int x0) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) {
+    mbar_arrive_expect_tx(bar, 128 * D * 2);
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      tma_box(dst + c * 16384, map, bar, c * 64, hs.first, q.qb + x0 / 128 * m.q_tokens, 0);
+  }
+  __syncwarp();
 }
 
 // ---- work claimed from the grid ------------------------------------------------
@@ -180,11 +243,9 @@ __device__ __forceinline__ int claims_take(Claims& c, uint64_t limit, volatile i
   return got;
 }
 
-// Host: the map of token rows [tokens][heads][d] of 16-bit elements (tok rows of
-// d elements from token to token) for boxes of `n` heads, 128 / n tokens. False
-// when the driver refuses.
-bool make_box_map(CUtensorMap* out, const void* base, bool f16, int tokens, int heads, int tok, int d,
-                  int n = 1);
+// Host: the boxes of a launch. False when the driver refuses one.
+bool make_key_maps(TileMaps& m, const Geo& g, const void* k, const void* v, bool f16);
+bool make_query_map(CUtensorMap* out, TileMaps& m, const Geo& g, const Rows& rows, const void* base, bool f16);
 
 // One query-major unit: 2 x 128 rows of one (sequence, key/value head, job),
 // against the key tiles it meets. Key tiles are numbered through the job's
