@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         const int kl = (t >= tsplit ? lo1 : lo0) - t * 128 - w * 64;
         const int kh = (t >= tsplit ? hi1 : hi0) - t * 128 - w * 64;
-        if (!__all_sync(0xffffffffu, kl <= 0 && kh >= 64)) mask_cols<2>(p, 0, kl, kh);
+        if (!__all_sync(0xffffffffu, kl <= 0 && kh >= 64)) mask_bits<2>(p, kl, kh);
         if constexpr (DKV) {
           if (!wait(&S.row_full[ts & 1], (ts >> 1) & 1)) break;
           const float4* L = reinterpret_cast<const float4*>(S.nlse[ts & 1] + w * 64);

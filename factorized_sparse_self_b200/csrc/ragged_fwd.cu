@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tl = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + tl + h * 128, tO = tmem + tl + kColO + h * D;
     const int row = (warp & 3) * 32 + lane;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.o) & 31) == 0;
     bool ok = true;
     int ns = 0, no = 0;  // tiles of this half so far, units with tiles
     for (int n = 0;; ++n) {
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, reinterpret_cast<uint32_t*>(s) + c * 32);
         tmem_wait_ld();
         const int kl = (seg ? lo1 : lo0) - j * 128, kh = (seg ? hi1 : hi0) - j * 128;
-        if (!__all_sync(0xffffffffu, kl <= 0 && kh >= 128)) mask_cols<4>(s, 0, kl, kh);
+        if (!__all_sync(0xffffffffu, kl <= 0 && kh >= 128)) mask_bits<4>(s, kl, kh);
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int x = 0; x < 128; x += 8) {
@@ -475,11 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 32; ++x) o[x] = any ? o[x] * wc : 0.f;
         if (a.mode == OUT_PARTIAL) {
           if (wc > 0.f) {  // a part without weight is not read
-            float4* dst = reinterpret_cast<float4*>(
-                a.parts.o + ((size_t)(part0 + part) * g.total * g.H + rr) * D + c);
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            store_row32(a.parts.o + ((size_t)(part0 + part) * g.total * g.H + rr) * D + c, o);
           }
           continue;
         }
@@ -494,11 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[4 * x + 3] = fmaf(wp, f.w, o[4 * x + 3]);
           }
         }
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + rr * D + c);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          dst[x] = make_uint4(pack2<F16>(o[8 * x], o[8 * x + 1]), pack2<F16>(o[8 * x + 2], o[8 * x + 3]),
-                              pack2<F16>(o[8 * x + 4], o[8 * x + 5]), pack2<F16>(o[8 * x + 6], o[8 * x + 7]));
+        store_row16<F16>(static_cast<uint16_t*>(a.o) + rr * D + c, o, wide);
       }
       tc_fence_before();
     }

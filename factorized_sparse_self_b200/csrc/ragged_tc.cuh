@@ -57,6 +57,43 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint64_
   }
 }
 
+// Sets v[x] = -inf for the columns x (< 32 * N) outside [lo, hi). The live columns
+// of 32 form a word whose bits become predicates several at a time; chunks that
+// every row of the warp keeps are left alone.
+template <int N>
+__device__ __forceinline__ void mask_bits(float* v, int lo, int hi) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const int a = imin(imax(lo - c * 32, 0), 32), b = imin(imax(hi - c * 32, 0), 32);
+    const uint32_t bits = (uint32_t)((1ull << b) - 1) & ~(uint32_t)((1ull << a) - 1);
+    if (!__all_sync(0xffffffffu, bits == 0xffffffffu)) {
+#pragma unroll
+      for (int x = 0; x < 32; ++x) v[c * 32 + x] = (bits & (1u << x)) ? v[c * 32 + x] : -INFINITY;
+    }
+  }
+}
+
+// Stores 32 values of a row in 16 bits, 32 bytes at a time where the row allows it.
+template <bool F16>
+__device__ __forceinline__ void store_row16(void* dst, const float* o, bool wide) {
+  uint32_t w[16];
+#pragma unroll
+  for (int x = 0; x < 16; ++x) w[x] = pack2<F16>(o[2 * x], o[2 * x + 1]);
+  uint4* p = static_cast<uint4*>(dst);
+  if (wide) {
+    st_global_v8(p, w);
+    st_global_v8(p + 2, w + 8);
+  } else {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) p[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+  }
+}
+// 32 fp32 values (parts of a workspace, whose rows lie on 32-byte boundaries).
+__device__ __forceinline__ void store_row32(float* dst, const float* o) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x) st_global_v8(dst + 8 * x, reinterpret_cast<const uint32_t*>(o) + 8 * x);
+}
+
 // ---- rows gathered into an operand tile -----------------------------------------
 // A tile is 128 rows of D 16-bit elements as D / 64 blocks of [128][64] with the
 // 128-byte swizzle, 16 KB each. A warp copies 64 of its rows, 16 bytes a lane
