@@ -7,6 +7,7 @@
 // products do 16 FMAs for 2 float4 loads, so the kernels are bound by shared
 // memory and the FMA pipe together.
 #include "ragged.h"
+#include "tc_common.cuh"
 
 namespace st {
 namespace rag {
@@ -19,40 +20,11 @@ constexpr int SP = BN + 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
-template <class T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-  return __ldg(reinterpret_cast<const float4*>(p));
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
-template <>
-__device__ __forceinline__ float4 load4<__half>(const __half* p) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
-template <class T>
-__device__ __forceinline__ T round_to(float x);
-template <>
-__device__ __forceinline__ float round_to<float>(float x) {
-  return x;
-}
-template <>
-__device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) {
-  return __float2bfloat16_rn(x);
-}
-template <>
-__device__ __forceinline__ __half round_to<__half>(float x) {
-  return __float2half_rn(x);
-}
+__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+
+__device__ __forceinline__ float value(float x) { return x; }
+__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float value(__half x) { return __half2float(x); }
 
 // Copies 64 rows of D elements into dst [64][D + 4]; row(i) gives the
 // row index of tile row i, or -1 for a row of zeros.
@@ -459,88 +431,136 @@ __device__ __forceinline__ bool seq_of_token(const Geo& g, int t, int& s) {
 
 constexpr int kJoinRows = 8;  // rows (warps) of a block of the streaming kernels
 
-// One warp per query row: o = sum_p exp(lse_p - lse) o_p.
-template <class T>
-__global__ void __launch_bounds__(32 * kJoinRows)
-    join_parts_kernel(const __grid_constant__ Geo g, const Parts parts, int nparts, T* o,
-                      float* lse) {
-  const long long row = (long long)blockIdx.x * kJoinRows + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const long long rows = (long long)g.total * g.H;
-  if (row >= rows) return;
-  int s;
-  if (!seq_of_token(g, (int)(row / g.H), s)) return;
-  float m = -INFINITY;
-  for (int p = lane; p < nparts; p += 32) m = fmaxf(m, parts.lse[p * rows + row]);
-#pragma unroll
-  for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-  float sum = 0.f;
-  if (m > -INFINITY)
-    for (int p = lane; p < nparts; p += 32) sum += expf(parts.lse[p * rows + row] - m);
-#pragma unroll
-  for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-  const float L = m > -INFINITY ? m + logf(sum) : -INFINITY;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  if (m > -INFINITY)
-    for (int p = 0; p < nparts; ++p) {
-      const float w = expf(parts.lse[p * rows + row] - L);
-      if (w == 0.f) continue;
-      const float* src = parts.o + (p * rows + row) * g.d;
-      for (int x = 0, c = lane; c < g.d; ++x, c += 32) acc[x] = fmaf(w, src[c], acc[x]);
-    }
-  for (int x = 0, c = lane; c < g.d; ++x, c += 32) o[row * g.d + c] = round_to<T>(acc[x]);
-  if (lane == 0) lse[row] = L;
+// Whether token row t belongs to a sequence (they follow one another).
+__device__ __forceinline__ bool in_sequence(const Geo& g, int t) {
+  return t >= cu_at(g, 0) && t < cu_at(g, g.S);
+}
+
+// Position of a token row in its sequence, by one thread.
+__device__ __forceinline__ int token_pos(const Geo& g, int t) {
+  int a = 0, b = g.S - 1;
+  while (a < b) {
+    const int m = (a + b + 1) >> 1;
+    if (cu_at(g, m) <= t) a = m;
+    else b = m - 1;
+  }
+  return t - cu_at(g, a);
 }
 
 template <class T>
-__global__ void __launch_bounds__(32 * kJoinRows)
-    row_delta_kernel(long long rows, int d, const T* o, const T* dout, float* delta) {
-  const long long row = (long long)blockIdx.x * kJoinRows + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  float acc = 0.f;
-  for (int c = lane * 4; c < d; c += 128) {
-    const float4 x = load4(o + row * d + c), y = load4(dout + row * d + c);
-    acc = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, acc))));
+__device__ __forceinline__ void store4(T* p, float4 v);
+template <>
+__device__ __forceinline__ void store4<float>(float* p, float4 v) {
+  *reinterpret_cast<float4*>(p) = v;
+}
+template <>
+__device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(tc::pack2<false>(v.x, v.y), tc::pack2<false>(v.z, v.w));
+}
+template <>
+__device__ __forceinline__ void store4<__half>(__half* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(tc::pack2<true>(v.x, v.y), tc::pack2<true>(v.z, v.w));
+}
+
+constexpr int kJoinThreads = 256;
+
+// o = sum_p exp(lse_p - lse) o_p: one thread per four elements of a query row.
+template <class T>
+__global__ void __launch_bounds__(kJoinThreads)
+    join_parts_kernel(const __grid_constant__ Geo g, const Parts parts, int nparts, int shift, T* o,
+                      float* lse) {
+  const long long x = (long long)blockIdx.x * kJoinThreads + threadIdx.x;
+  const long long row = x >> shift;
+  const int c = (int)(x - (row << shift)) * 4;
+  const long long rows = (long long)g.total * g.H;
+  if (row >= rows || !in_sequence(g, (int)(row / g.H))) return;
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int p = 0; p < nparts; ++p) m = fmaxf(m, __ldg(parts.lse + p * rows + row));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  if (m > -INFINITY) {
+#pragma unroll 4
+    for (int p = 0; p < nparts; ++p) {
+      const float w = expf(__ldg(parts.lse + p * rows + row) - m);
+      if (w > 0.f) {  // a part without weight may not have been written
+        const float4 v = __ldg(reinterpret_cast<const float4*>(parts.o + (p * rows + row) * g.d + c));
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+        sum += w;
+      }
+    }
+    const float inv = 1.f / sum;
+    acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  }
+  store4(o + row * g.d + c, acc);
+  if (c == 0) lse[row] = m > -INFINITY ? m + logf(sum) : -INFINITY;
+}
+
+// delta = dout . o of every row: 16 bytes a lane of o and of dout, 2^shift lanes a
+// row, four rows of a lane in flight.
+template <class T>
+__global__ void __launch_bounds__(kJoinThreads)
+    row_delta_kernel(long long rows, int shift, const T* o, const T* dout, float* delta) {
+  constexpr int E = 16 / sizeof(T), U = 4;
+  const int lane = threadIdx.x & 31, per = 32 >> shift;  // rows of a warp at a time
+  const long long first = ((long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5)) * U * per;
+  const int sub = lane >> shift, c = (lane & ((1 << shift) - 1)) * E;
+  const int d = E << shift;
+  uint4 a[U], b[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long row = first + u * per + sub;
+    if (row < rows) {
+      a[u] = __ldg(reinterpret_cast<const uint4*>(o + row * d + c));
+      b[u] = __ldg(reinterpret_cast<const uint4*>(dout + row * d + c));
+    }
   }
 #pragma unroll
-  for (int x = 16; x; x >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, x);
-  if (lane == 0) delta[row] = acc;
+  for (int u = 0; u < U; ++u) {
+    const long long row = first + u * per + sub;
+    float acc = 0.f;
+    if (row < rows) {
+      const T* x = reinterpret_cast<const T*>(&a[u]);
+      const T* y = reinterpret_cast<const T*>(&b[u]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc = fmaf(value(x[e]), value(y[e]), acc);
+    }
+    for (int y = 1 << (shift - 1); y; y >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, y);
+    if (c == 0 && row < rows) delta[row] = acc;
+  }
 }
 
-// One warp per key row and head: the parts that hold it, added in order.
+// dK, dV: the parts that hold a key row, added in order; one thread per four
+// elements of the pair.
 template <class T>
-__global__ void __launch_bounds__(32 * kJoinRows) join_dkv_kernel(const __grid_constant__ BwdLaunch a) {
+__global__ void __launch_bounds__(kJoinThreads)
+    join_dkv_kernel(const __grid_constant__ BwdLaunch a, int shift) {
   const Geo& g = a.g;
-  const long long row = (long long)blockIdx.x * kJoinRows + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const long long rows = (long long)g.total * g.Hkv;
+  const long long x = (long long)blockIdx.x * kJoinThreads + threadIdx.x;
+  const long long row = x >> shift, rows = (long long)g.total * g.Hkv;
+  const int c = (int)(x - (row << shift)) * 4;
   if (row >= rows) return;
   const int t = (int)(row / g.Hkv), kvh = (int)(row - (long long)t * g.Hkv);
-  if (dkv_direct(a, kvh)) return;
-  int s;
-  if (!seq_of_token(g, t, s)) return;
-  const int pos = t - cu_at(g, s);
-  const bool summary = pos - fdiv(pos, g.fl) * g.l >= g.l - g.c;
-  float acc[8] = {};
+  if (dkv_direct(a, kvh) || !in_sequence(g, t)) return;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j = 0; j < a.njobs; ++j) {
     if (!job_reaches(g, a.job[j], kvh)) continue;
-    if (a.job[j].seg[0].kview == VIEW_SUM && !summary) continue;
+    if (a.job[j].seg[0].kview == VIEW_SUM) {
+      const int pos = token_pos(g, t);
+      if (pos - fdiv(pos, g.fl) * g.l < g.l - g.c) continue;
+    }
+#pragma unroll 4
     for (int p = j * a.nsplit; p < (j + 1) * a.nsplit; ++p) {
-      const float* src = a.parts + (p * rows + row) * 2 * g.d;
-#pragma unroll
-      for (int x = 0; x < 8; ++x)
-        if (lane + 32 * x < 2 * g.d) acc[x] += src[lane + 32 * x];
+      const float4 v = __ldg(reinterpret_cast<const float4*>(a.parts + (p * rows + row) * 2 * g.d + c));
+      acc = make_float4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
     }
   }
-  T* dk = static_cast<T*>(a.dk) + ((size_t)t * a.dk_rows.tok + kvh * a.dk_rows.head) * g.d;
-  T* dv = static_cast<T*>(a.dv) + ((size_t)t * a.dv_rows.tok + kvh * a.dv_rows.head) * g.d;
-#pragma unroll
-  for (int x = 0; x < 8; ++x) {
-    const int c = lane + 32 * x;
-    if (c < g.d) dk[c] = round_to<T>(acc[x]);
-    else if (c < 2 * g.d) dv[c - g.d] = round_to<T>(acc[x]);
-  }
+  T* dst = c < g.d ? static_cast<T*>(a.dk) + ((size_t)t * a.dk_rows.tok + kvh * a.dk_rows.head) * g.d + c
+                   : static_cast<T*>(a.dv) + ((size_t)t * a.dv_rows.tok + kvh * a.dv_rows.head) * g.d + c - g.d;
+  store4(dst, acc);
 }
 
 // One warp per new token: the 16-byte chunks of its key and value rows, head by
@@ -664,48 +684,56 @@ cudaError_t simt_ragged_dkv(const BwdLaunch& a) {
   return pick(a.g.d, RunDkv{a});
 }
 
-cudaError_t join_parts(const Geo& g, int dtype, const Parts& parts, int nparts, void* o,
-                       float* lse, cudaStream_t s) {
-  const unsigned nb = join_blocks((long long)g.total * g.H);
-  const int nt = 32 * kJoinRows;
-  if (dtype == ST_F32)
-    join_parts_kernel<float><<<nb, nt, 0, s>>>(g, parts, nparts, static_cast<float*>(o), lse);
-  else if (dtype == ST_BF16)
-    join_parts_kernel<__nv_bfloat16>
-        <<<nb, nt, 0, s>>>(g, parts, nparts, static_cast<__nv_bfloat16*>(o), lse);
-  else
-    join_parts_kernel<__half><<<nb, nt, 0, s>>>(g, parts, nparts, static_cast<__half*>(o), lse);
+namespace {
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+unsigned join_grid(long long threads) { return (unsigned)((threads + kJoinThreads - 1) / kJoinThreads); }
+
+template <class T>
+cudaError_t join_parts_t(const Geo& g, const Parts& parts, int nparts, void* o, float* lse, cudaStream_t s) {
+  const int shift = log2_of(g.d / 4);
+  join_parts_kernel<T><<<join_grid(((long long)g.total * g.H) << shift), kJoinThreads, 0, s>>>(
+      g, parts, nparts, shift, static_cast<T*>(o), lse);
   return cudaGetLastError();
+}
+template <class T>
+cudaError_t row_delta_t(const Geo& g, const void* o, const void* dout, float* delta, cudaStream_t s) {
+  const long long rows = (long long)g.total * g.H;
+  const int shift = log2_of(g.d * (int)sizeof(T) / 16);
+  const long long per = (32 >> shift) * 4;
+  row_delta_kernel<T><<<join_grid((rows + per - 1) / per * 32), kJoinThreads, 0, s>>>(
+      rows, shift, static_cast<const T*>(o), static_cast<const T*>(dout), delta);
+  return cudaGetLastError();
+}
+template <class T>
+cudaError_t join_dkv_t(const BwdLaunch& a) {
+  const int shift = log2_of(a.g.d / 2);
+  join_dkv_kernel<T><<<join_grid(((long long)a.g.total * a.g.Hkv) << shift), kJoinThreads, 0, a.stream>>>(a, shift);
+  return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t join_parts(const Geo& g, int dtype, const Parts& parts, int nparts, void* o, float* lse,
+                       cudaStream_t s) {
+  return dtype == ST_F32    ? join_parts_t<float>(g, parts, nparts, o, lse, s)
+         : dtype == ST_BF16 ? join_parts_t<__nv_bfloat16>(g, parts, nparts, o, lse, s)
+                            : join_parts_t<__half>(g, parts, nparts, o, lse, s);
 }
 
 cudaError_t row_delta(const Geo& g, int dtype, const void* o, const void* dout, float* delta,
                       cudaStream_t s) {
-  const long long rows = (long long)g.total * g.H;
-  const unsigned nb = join_blocks(rows);
-  const int nt = 32 * kJoinRows;
-  if (dtype == ST_F32)
-    row_delta_kernel<float><<<nb, nt, 0, s>>>(rows, g.d, static_cast<const float*>(o),
-                                              static_cast<const float*>(dout), delta);
-  else if (dtype == ST_BF16)
-    row_delta_kernel<__nv_bfloat16>
-        <<<nb, nt, 0, s>>>(rows, g.d, static_cast<const __nv_bfloat16*>(o),
-                           static_cast<const __nv_bfloat16*>(dout), delta);
-  else
-    row_delta_kernel<__half><<<nb, nt, 0, s>>>(rows, g.d, static_cast<const __half*>(o),
-                                               static_cast<const __half*>(dout), delta);
-  return cudaGetLastError();
+  return dtype == ST_F32    ? row_delta_t<float>(g, o, dout, delta, s)
+         : dtype == ST_BF16 ? row_delta_t<__nv_bfloat16>(g, o, dout, delta, s)
+                            : row_delta_t<__half>(g, o, dout, delta, s);
 }
 
 cudaError_t join_dkv(const BwdLaunch& a, int dtype) {
-  const unsigned nb = join_blocks((long long)a.g.total * a.g.Hkv);
-  const int nt = 32 * kJoinRows;
-  if (dtype == ST_F32)
-    join_dkv_kernel<float><<<nb, nt, 0, a.stream>>>(a);
-  else if (dtype == ST_BF16)
-    join_dkv_kernel<__nv_bfloat16><<<nb, nt, 0, a.stream>>>(a);
-  else
-    join_dkv_kernel<__half><<<nb, nt, 0, a.stream>>>(a);
-  return cudaGetLastError();
+  return dtype == ST_F32    ? join_dkv_t<float>(a)
+         : dtype == ST_BF16 ? join_dkv_t<__nv_bfloat16>(a)
+                            : join_dkv_t<__half>(a);
 }
 
 cudaError_t cache_append(const Geo& g, const Rows& kin, const Rows& vin, int elem_bytes,
