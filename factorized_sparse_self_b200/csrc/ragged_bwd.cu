@@ -14,12 +14,13 @@
 // One CTA per SM (384 threads), units claimed from the grid. Warps 0..7 are two
 // warpgroups that share the 128 rows and take 64 columns each of a 128 x 128
 // tile (thread = row = TMEM lane); P and dS go back to TMEM as 16-bit pairs over
-// the scores they came from and are read from there as the A operand, so they
-// never pass through shared memory. Warp 9 issues the products, warps 8 and 11
+// columns that have been read and are the A operand from there, so they never pass
+// through shared memory. Warp 9 issues the products, warps 8 and 11
 // load rows, warp 10 decodes units.
 // TMEM query-major: S (two buffers, so that S of the next tile is there when a
-// tile's dS is done) 0, 128, dP 256, dQ 384. Key-major: S^T 0, dP^T 128,
-// dV 256, dK 256 + d.
+// tile's dS is done) 0, 128, dP 256, dQ 384. Key-major: S^T 0, dP^T 128 (d = 128
+// fills the rest with dV 256, dK 256 + d): P^T and dS^T both go over dP^T, so that
+// the next tile's S^T is formed under this one's exponentials.
 #include "ragged_tc.cuh"
 
 namespace st {
@@ -58,7 +59,7 @@ struct alignas(1024) Smem {
   float nlse[2][128], ndel[2][128];    // key-major: -LSE log2(e) and -D of a tile's query rows
   uint64_t r_full, r_empty;
   uint64_t full[Cfg<D>::kA + Cfg<D>::kB], empty[Cfg<D>::kA + Cfg<D>::kB];
-  uint64_t s_full[2], dp_full, p_ready, ds_ready, acc_full;
+  uint64_t s_full[2], s_free, dp_full, ds_ready, acc_full;
   uint64_t row_full[2], row_empty[2];
   uint64_t sched_full[kSched], sched_empty[kSched];
   uint64_t fin;
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.claim_bar[i], 1);
     }
     mbar_init(&S.dp_full, 1);
-    mbar_init(&S.p_ready, 256);
+    mbar_init(&S.s_free, 256);
     mbar_init(&S.ds_ready, 256);
     mbar_init(&S.acc_full, 1);
     for (int i = 0; i < kSched; ++i) {
@@ -259,7 +260,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           if (used > 0 && !wait(&S.r_empty, (used - 1) & 1)) break;
           ++used;
-          {
+          const int rview = job.seg[0].kview;
+          const int rbox = DKV ? box_rows(maps, g, u.q, rview, u.r0 / 128)
+                               : (job.qview == VIEW_NAT && u.r0 + 128 <= xrows ? maps.q_tokens : 0);
+          if (rbox) {
+            // each producer loads one of the two tiles
+            if (DKV) load_boxes<D>(smem_u32(S.res[pw]), maps, pw, &S.r_full, g, u.q, rview, u.r0 / 128, u.kvh, rbox);
+            else load_query_boxes<D>(smem_u32(S.res[pw]), pw ? &maps.dout : &maps.q, &S.r_full, maps, u.q, u.hs, u.r0);
+          } else {
             int ra[2], rb[2];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
@@ -343,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) {
         if (lane == 0) fail();
         // copies in flight land before the CTA may exit
+        if (used > 0) mbar_wait_drain(&S.r_full, (used - 1) & 1, limit);
         for (int i = imax(0, tt - NA); i <= tt; ++i) mbar_wait_drain(&S.full[i % NA], (i / NA) & 1, limit);
         for (int i = imax(0, tt - NB); i <= tt; ++i) mbar_wait_drain(&S.full[NA + i % NB], (i / NB) & 1, limit);
       }
@@ -441,15 +450,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             scores(a2, slot_b(ts), kDP, &S.dp_full);
             if (T == 1) commit(&S.r_empty);
             for (int t = 0; t < T; ++t, ++ts) {
-              if (t + 1 < T) wait_a(ts + 1);
-              wait(&S.p_ready, ts & 1);
-              weigh(0, slot_b(ts), kDV, t == 0, nullptr);
               if (t + 1 < T) {
+                // under this tile's exponentials
+                wait_a(ts + 1);
+                wait(&S.s_free, ts & 1);
                 scores(a1, slot_a(ts + 1), 0, &S.s_full[0]);
                 wait_b(ts + 1);
               }
               wait(&S.ds_ready, ts & 1);
-              weigh(kDP, slot_a(ts), kDK, t == 0, t + 1 == T ? &S.acc_full : nullptr);
+              weigh(kDP, slot_b(ts), kDV, t == 0, nullptr);
+              weigh(kDP + 32, slot_a(ts), kDK, t == 0, t + 1 == T ? &S.acc_full : nullptr);
               if (t + 1 < T) {
                 scores(a2, slot_b(ts + 1), kDP, &S.dp_full);
                 if (t + 2 == T) commit(&S.r_empty);
@@ -519,6 +529,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tS, reinterpret_cast<uint32_t*>(p));
         tmem_ld32(tS + 32, reinterpret_cast<uint32_t*>(p) + 32);
         tmem_wait_ld();
+        if constexpr (DKV) {
+          tc_fence_before();
+          mbar_arrive(&S.s_free);
+        }
         const int kl = (t >= tsplit ? lo1 : lo0) - t * 128 - w * 64;
         const int kh = (t >= tsplit ? hi1 : hi0) - t * 128 - w * 64;
         if (!__all_sync(0xffffffffu, kl <= 0 && kh >= 64)) mask_bits<2>(p, kl, kh);
@@ -537,18 +551,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int x = 0; x < 64; ++x) p[x] = fast_exp2(p[x]);
+        uint32_t pk[32], pp[DKV ? 32 : 1];
         if constexpr (DKV) {
-          uint32_t pk[32];
 #pragma unroll
-          for (int x = 0; x < 32; ++x) pk[x] = pack2<F16>(p[2 * x], p[2 * x + 1]);
-          tmem_st32(tS, pk);
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(&S.p_ready);
+          for (int x = 0; x < 32; ++x) pp[x] = pack2<F16>(p[2 * x], p[2 * x + 1]);
         }
         if (!wait(&S.dp_full, ts & 1)) break;
         tc_fence_after();
-        uint32_t pk[32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float dp[32];
@@ -576,11 +585,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 16; ++x) pk[c * 16 + x] = pack2<F16>(p[c * 32 + 2 * x], p[c * 32 + 2 * x + 1]);
         }
-        if (DKV) {
+        if constexpr (DKV) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&S.row_empty[ts & 1]);
+          tmem_st32(tP, pp);
+          tmem_st32(tP + 32, pk);
+        } else {
+          tmem_st32(tS, pk);
         }
-        tmem_st32(DKV ? tP : tS, pk);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&S.ds_ready);
@@ -609,8 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 32; ++x) o[x] = t1 > t0 ? o[x] * a.scale : 0.f;
           float4* part = reinterpret_cast<float4*>(a.dq_part + ((size_t)qr.t * g.H + qr.h) * D + c);
           if (a.mode == OUT_PARTIAL) {
-#pragma unroll
-            for (int x = 0; x < 8; ++x) part[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            store_row32(reinterpret_cast<float*>(part), o);
             continue;
           }
           if (a.mode == OUT_MERGE) {
@@ -623,12 +634,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               o[4 * x + 3] += f.w;
             }
           }
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dq) +
-                                                ((size_t)qr.t * a.dq_rows.tok + qr.h * a.dq_rows.head) * D + c);
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            dst[x] = make_uint4(pack2<F16>(o[8 * x], o[8 * x + 1]), pack2<F16>(o[8 * x + 2], o[8 * x + 3]),
-                                pack2<F16>(o[8 * x + 4], o[8 * x + 5]), pack2<F16>(o[8 * x + 6], o[8 * x + 7]));
+          store_row16<F16>(static_cast<uint16_t*>(a.dq) +
+                               ((size_t)qr.t * a.dq_rows.tok + qr.h * a.dq_rows.head) * D + c,
+                           o, (reinterpret_cast<uintptr_t>(a.dq) & 31) == 0);
         }
         tc_fence_before();
       } else {
@@ -659,16 +667,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 32; ++x) o[x] = t1 > t0 ? o[x] * f : 0.f;
           if (direct) {
-            uint4* dst = reinterpret_cast<uint4*>(out + c);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              dst[x] = make_uint4(pack2<F16>(o[8 * x], o[8 * x + 1]), pack2<F16>(o[8 * x + 2], o[8 * x + 3]),
-                                  pack2<F16>(o[8 * x + 4], o[8 * x + 5]), pack2<F16>(o[8 * x + 6], o[8 * x + 7]));
+            store_row16<F16>(out + c, o, (reinterpret_cast<uintptr_t>(w ? a.dv : a.dk) & 31) == 0);
           } else {
-            float4* dst = reinterpret_cast<float4*>(
-                a.parts + (((size_t)part * g.total + tok) * g.Hkv + kvh) * 2 * D + w * D + c);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            store_row32(a.parts + (((size_t)part * g.total + tok) * g.Hkv + kvh) * 2 * D + w * D + c, o);
           }
         }
         tc_fence_before();
@@ -686,8 +687,8 @@ cudaError_t launch(const BwdLaunch& a) {
   const Geo& g = a.g;
   TileMaps m = {};
   const Rows whole = {g.H, 1, 0};
-  if (DKV ? !make_query_map(&m.q, m, g, g.q, a.q, F16) || !make_query_map(&m.dout, m, g, whole, a.dout, F16)
-          : !make_key_maps(m, g, a.k, a.v, F16))
+  if (!make_query_map(&m.q, m, g, g.q, a.q, F16) || !make_query_map(&m.dout, m, g, whole, a.dout, F16) ||
+      !make_key_maps(m, g, a.k, a.v, F16))
     return cudaErrorInvalidValue;
   const size_t smem = sizeof(Smem<D>);
   static_assert(sizeof(Smem<D>) <= 232448, "shared memory");
