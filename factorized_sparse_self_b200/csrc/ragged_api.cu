@@ -12,6 +12,7 @@ namespace {
 
 constexpr int kPartsLimit = 32;  // most key ranges of one row
 constexpr int kFewRows = 32;     // most query rows per key/value head for the few-row kernel
+constexpr long long kPartsBytes = 256LL << 20;  // most workspace that key ranges may take
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -104,7 +105,7 @@ st_status fill_geo(const st_pattern_desc* p, st_dtype dtype, const st_packed_des
   g.q.head = g.k.head = g.v.head = 1;
   // grids and row numbers are 31-bit
   if ((int64_t)g.total * g.q.tok > 0x7fffffff || (int64_t)g.total * g.k.tok > 0x7fffffff ||
-      (int64_t)g.total * g.v.tok > 0x7fffffff || (int64_t)g.total * g.H > 0x7fffffff ||
+      (int64_t)g.total * g.v.tok > 0x7fffffff || (int64_t)g.total * g.H > 0x7fff0000 ||
       (int64_t)g.total * g.G + g.S > 0x7fffffff || g.Hkv > 65535)
     return ST_ERR_UNSUPPORTED;
   return ST_OK;
@@ -186,27 +187,24 @@ FwdPlan plan_fwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype, long lo
   const int key_tile = f.few ? 16 : dtype == ST_F32 ? 64 : 128;
   const long long longest = std::max(1LL, (max_q * G + rows - 1) / rows * g.Hkv);
   const long long all = std::max(longest, ((long long)g.total * G + rows - 1) / rows * g.Hkv);
+  const size_t qrows = (size_t)g.total * g.H;
+  const long long fit = std::max(1LL, kPartsBytes / (long long)std::max<size_t>(1, qrows * g.d * sizeof(float)));
   if (f.few) {
     // ranges of 128 to 1024 keys, about four for each of the CTAs that run at once
     const long long want = keys * all / (8 * sms);
     f.least = clamp_int(want, 128, 1024) / key_tile;
-    f.nsplit = clamp_int((keys + f.least * key_tile - 1) / (f.least * key_tile), 1, kPartsLimit);
+    f.nsplit = clamp_int((keys + f.least * key_tile - 1) / (f.least * key_tile), 1, std::min<long long>(fit, kPartsLimit));
   } else {
     f.least = 512 / key_tile;
     long long n = 1;
-    if (paged) {
-      if (all < 4 * sms) n = (3 * sms + longest - 1) / longest;
-    } else if (longest < sms) {
-      n = (sms + longest - 1) / longest;
-    }
-    f.nsplit = clamp_int(std::min(n, keys / 512), 1, kPartsLimit);
+    if (all < 4 * sms) n = paged ? (3 * sms + longest - 1) / longest : (sms + longest - 1) / longest;
+    f.nsplit = clamp_int(std::min(n, keys / 512), 1, std::min<long long>(fit, kPartsLimit));
     // ranges of one length: shorter sequences are cut into fewer
     f.least = (int)std::max<long long>(f.least, (keys + key_tile - 1) / key_tile / f.nsplit);
   }
   const bool two = two_orders(p);
   f.merge = two && f.nsplit == 1 && !f.few;
   f.nparts = f.merge ? 1 : two ? 2 * f.nsplit : f.nsplit > 1 ? f.nsplit : 0;
-  const size_t qrows = (size_t)g.total * g.H;
   f.parts_o = round256(qrows * g.d * sizeof(float) * f.nparts);
   f.bytes = f.nparts ? f.parts_o + round256(qrows * sizeof(float) * f.nparts) : 0;
   return f;
@@ -277,14 +275,16 @@ BwdPlan plan_bwd(const Geo& g, const st_pattern_desc& p) {
     for (int s = 0; s < jobs[j].nseg; ++s)
       b.kjob[b.njobs++] = Job{jobs[j].hc, jobs[j].qview, 1, {jobs[j].seg[s], jobs[j].seg[s]}};
   // key tiles of one longest sequence against the query rows that reach them
-  const long long units = ((long long)p.T + 127) / 128 * g.Hkv;
-  b.nsplit = units < sm_count() ? clamp_int(std::min<long long>((sm_count() + units - 1) / units,
-                                                               (long long)p.T * g.G / 512),
-                                            1, kPartsLimit)
-                                : 1;
+  const size_t qrows = (size_t)g.total * g.H, krows = (size_t)g.total * g.Hkv;
+  const long long sms = sm_count(), units = ((long long)p.T + 127) / 128 * g.Hkv;
+  const long long all = std::max(units, ((long long)g.total + 127) / 128 * g.Hkv);
+  const long long fit = std::max(1LL, kPartsBytes / (long long)std::max<size_t>(1, krows * 2 * g.d * sizeof(float) * b.njobs));
+  b.nsplit = 1;
+  if (units < sms && all < 2 * sms)
+    b.nsplit = clamp_int(std::min((sms + units - 1) / units, (long long)p.T * g.G / 512), 1,
+                         std::min<long long>(fit, kPartsLimit));
   // one part is enough only where every key head has one job over all its keys
   b.parts = b.nsplit > 1 || (b.njobs == 2 && !(g.split && g.G == 1 && b.kjob[1].seg[0].kview != VIEW_SUM));
-  const size_t qrows = (size_t)g.total * g.H, krows = (size_t)g.total * g.Hkv;
   b.delta = round256(qrows * sizeof(float));
   b.dq_part = two_orders(p) ? round256(qrows * g.d * sizeof(float)) : 0;
   b.parts_bytes = b.parts ? round256(krows * 2 * g.d * sizeof(float) * b.njobs * b.nsplit) : 0;
