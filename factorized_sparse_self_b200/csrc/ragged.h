@@ -57,11 +57,14 @@ struct BwdLaunch {
   Job qjob[2];       // query jobs of this launch
   int32_t nqjobs, mode;
   const void *q, *k, *v, *dout;
-  const float *lse, *delta;
+  const float* lse;
+  float* delta;  // mended in place
   void *dq, *dk, *dv;
   Rows dq_rows, dk_rows, dv_rows;  // of the gradients
   float* parts;      // dK, dV parts
   float* dq_part;    // fp32 dQ [total][H][d] of the first query order
+  int32_t mend_tiles;  // 16-bit: key tiles up to which a unit's rows have their delta mended
+  float *kb_part, *r_part;  // of the first query order: sums P K, lost part of delta
   int32_t nsplit;
   float scale;
   uint64_t wait_ns;

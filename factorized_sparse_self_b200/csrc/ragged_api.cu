@@ -264,11 +264,19 @@ struct BwdPlan {
   Job kjob[2];
   int njobs, nsplit;
   bool parts;
+  int mend_tiles;
   size_t delta, dq_part, parts_bytes, bytes;
 };
 
-BwdPlan plan_bwd(const Geo& g, const st_pattern_desc& p) {
+BwdPlan plan_bwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype) {
   BwdPlan b{};
+  // Units of at most two key tiles are where rows have few keys. With two orders
+  // the sums of both are needed: all units, if the band is short. d = 128 pays for it
+  // (dense step 965 -> 1003 us) and mends patterns of few keys only.
+  if (dtype != ST_F32) {
+    if (two_orders(p)) b.mend_tiles = p.l < 128 ? 0x7fffffff : 0;
+    else b.mend_tiles = g.d == 64 || most_keys(p) <= 2048 ? 2 : 0;
+  }
   Job jobs[2];
   const int n = make_jobs(p, jobs);
   for (int j = 0; j < n; ++j)
@@ -289,6 +297,7 @@ BwdPlan plan_bwd(const Geo& g, const st_pattern_desc& p) {
   b.dq_part = two_orders(p) ? round256(qrows * g.d * sizeof(float)) : 0;
   b.parts_bytes = b.parts ? round256(krows * 2 * g.d * sizeof(float) * b.njobs * b.nsplit) : 0;
   b.bytes = b.delta + b.dq_part + b.parts_bytes;
+  if (b.dq_part && b.mend_tiles) b.bytes += b.delta + b.dq_part;
   return b;
 }
 
@@ -332,7 +341,7 @@ st_status st_packed_attn_bwd_workspace(const st_pattern_desc* p, st_dtype dtype,
   if (!bytes) return ST_ERR_INVALID;
   st_status s = fill_geo(p, dtype, x, true, g);
   if (s != ST_OK) return s;
-  *bytes = plan_bwd(g, *p).bytes;
+  *bytes = plan_bwd(g, *p, dtype).bytes;
   return ST_OK;
 }
 
@@ -354,7 +363,7 @@ st_status st_packed_attn_bwd(const st_pattern_desc* p, st_dtype dtype, const st_
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) ||
       !aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned4(cu))
     return ST_ERR_INVALID;
-  const BwdPlan b = plan_bwd(g, *p);
+  const BwdPlan b = plan_bwd(g, *p, dtype);
   if (!workspace_ok(ws, ws_bytes, b.bytes)) return ST_ERR_WORKSPACE;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   s = get_status(g, cs);
@@ -375,14 +384,18 @@ st_status st_packed_attn_bwd(const st_pattern_desc* p, st_dtype dtype, const st_
   char* w = static_cast<char*>(ws);
   float* delta = reinterpret_cast<float*>(w);
   a.delta = delta;
-  a.dq_part = reinterpret_cast<float*>(w + b.delta);
-  a.parts = reinterpret_cast<float*>(w + b.delta + b.dq_part);
+  w += b.delta;
+  a.dq_part = reinterpret_cast<float*>(w);
+  w += b.dq_part;
+  a.parts = reinterpret_cast<float*>(w);
+  w += b.parts_bytes;
+  a.mend_tiles = b.mend_tiles;
+  a.r_part = reinterpret_cast<float*>(w);
+  a.kb_part = reinterpret_cast<float*>(w + b.delta);
   a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)g.d);
   a.wait_ns = wait_limit_ns();
   a.stream = cs;
   cudaError_t e = row_delta(g, dtype, o, dout, delta, cs);
-  if (e == cudaSuccess) e = dtype == ST_F32 ? simt_ragged_dkv(a) : tc_ragged_dkv(a, dtype);
-  if (e == cudaSuccess && b.parts) e = join_dkv(a, dtype);
   Job jobs[2];
   const int n = make_jobs(*p, jobs);
   auto go_dq = [&]() { return dtype == ST_F32 ? simt_ragged_dq(a) : tc_ragged_dq(a, dtype); };
@@ -400,6 +413,8 @@ st_status st_packed_attn_bwd(const st_pattern_desc* p, st_dtype dtype, const st_
     a.mode = OUT_FINAL;
     e = go_dq();
   }
+  if (e == cudaSuccess) e = dtype == ST_F32 ? simt_ragged_dkv(a) : tc_ragged_dkv(a, dtype);
+  if (e == cudaSuccess && b.parts) e = join_dkv(a, dtype);
   return e == cudaSuccess ? ST_OK : ST_ERR_CUDA;
 }
 

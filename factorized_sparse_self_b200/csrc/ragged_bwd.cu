@@ -11,16 +11,27 @@
 // and the results are the same in every run. Rows of a unit are (query, head of
 // the group) pairs, so dK and dV of grouped heads are sums over more rows.
 //
+// D = dO . O comes from the rounded O. Where a row has many keys O is small beside
+// dP and so is that error; where it has few, it is as large as the rounding of dS.
+// Rows of dS sum to zero, so r = sum_j P (dP - D) is what D lost. In units of few
+// key tiles the query-major kernel also sums P K, takes r times it from dQ, and
+// hands D + r to the key-major kernel, which therefore runs after it. (Errors of dQ
+// and dK over that of rounding the result: strided, l = 100, split, fp16 1.72 -> 1.42;
+// fixed, l = 20, bf16 1.68 -> 1.42; dense, 2000 tokens 1.51 -> 1.41.) At d = 128 the sum
+// takes the second S's place in TMEM: long dense sequences go without.
+//
 // One CTA per SM (384 threads), units claimed from the grid. Warps 0..7 are two
 // warpgroups that share the 128 rows and take 64 columns each of a 128 x 128
 // tile (thread = row = TMEM lane); P and dS go back to TMEM as 16-bit pairs over
 // columns that have been read and are the A operand from there, so they never pass
 // through shared memory. Warp 9 issues the products, warps 8 and 11
 // load rows, warp 10 decodes units.
-// TMEM query-major: S (two buffers, so that S of the next tile is there when a
-// tile's dS is done) 0, 128, dP 256, dQ 384. Key-major: S^T 0, dP^T 128 (d = 128
-// fills the rest with dV 256, dK 256 + d): P^T and dS^T both go over dP^T, so that
-// the next tile's S^T is formed under this one's exponentials.
+// TMEM: S, dP (key-major: transposed), 128 columns each, then the accumulators, d
+// columns each: dQ and P K, or dV and dK. P and dS both go over dP, so S is free as
+// soon as it is in registers and the next tile's is formed under this one's
+// exponentials. Query-major, d = 64 or without P K, there is room for two S: P and dS go over S, and
+// the next dP is formed before the tile's products, not behind them (backward of 12288
+// rasters, l = 192, split: 223 against 241 us).
 #include "ragged_tc.cuh"
 
 namespace st {
@@ -50,6 +61,7 @@ struct BUnit {
   int32_t t0, t1;  // tiles of the other side
   int32_t cnt0;    // query-major: tiles of segment 0
   int32_t u0[2];   // query-major: first tile of each segment
+  int32_t mend;    // query-major: whether its rows' D is mended
 };
 
 template <int D>
@@ -57,9 +69,10 @@ struct alignas(1024) Smem {
   uint8_t res[2][Cfg<D>::kTileBytes];  // Q, dO or K, V
   uint8_t ring[Cfg<D>::kA + Cfg<D>::kB][Cfg<D>::kTileBytes];
   float nlse[2][128], ndel[2][128];    // key-major: -LSE log2(e) and -D of a tile's query rows
+                                       // (mend: ndel holds the two halves of r)
   uint64_t r_full, r_empty;
   uint64_t full[Cfg<D>::kA + Cfg<D>::kB], empty[Cfg<D>::kA + Cfg<D>::kB];
-  uint64_t s_full[2], s_free, dp_full, ds_ready, acc_full;
+  uint64_t s_full[2], s_free, dp_full, ds_ready, acc_full, r_sum;
   uint64_t row_full[2], row_empty[2];
   uint64_t sched_full[kSched], sched_empty[kSched];
   uint64_t fin;
@@ -133,18 +146,22 @@ __device__ __forceinline__ bool decode(const BwdLaunch& a, int slots, int n, BUn
     out->cnt0 = cnt0;
     out->u0[0] = u0[0];
     out->u0[1] = u0[1];
+    out->mend = a.mend_tiles > 0 && t1 - t0 <= a.mend_tiles;
   }
   __syncwarp();
   return true;
 }
 
-template <int D, bool F16, bool DKV>
+// MEND (query-major): units of few key tiles mend D.
+template <int D, bool F16, bool DKV, bool MEND>
 __global__ void __launch_bounds__(kThreads, 1)
     ragged_bwd_tc(const __grid_constant__ BwdLaunch a, const __grid_constant__ TileMaps maps, int slots) {
   extern __shared__ __align__(1024) uint8_t raw[];
   Smem<D>& S = *reinterpret_cast<Smem<D>*>(raw);
   constexpr int NA = Cfg<D>::kA, NB = Cfg<D>::kB, NS = NA + NB, TB = Cfg<D>::kTileBytes;
-  constexpr uint32_t kDP = DKV ? 128 : 256, kDQ = 384, kDV = 256, kDK = 256 + D;
+  constexpr bool TWO_S = !DKV && (D == 64 || !MEND);
+  constexpr uint32_t kDP = TWO_S ? 256 : 128, kAcc = kDP + 128;
+  constexpr uint32_t kDQ = kAcc, kKB = kAcc + D, kDV = kAcc, kDK = kAcc + D;
   const Geo& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t limit = a.wait_ns;
@@ -162,15 +179,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.s_full[i], 1);
       mbar_init(&S.row_full[i], 2);
       mbar_init(&S.row_empty[i], 8);
       mbar_init(&S.claim_bar[i], 1);
     }
+    mbar_init(&S.s_full[0], 1);
+    mbar_init(&S.s_full[1], 1);
     mbar_init(&S.dp_full, 1);
     mbar_init(&S.s_free, 256);
     mbar_init(&S.ds_ready, 256);
     mbar_init(&S.acc_full, 1);
+    mbar_init(&S.r_sum, 256);
     for (int i = 0; i < kSched; ++i) {
       mbar_init(&S.sched_full[i], 1);
       mbar_init(&S.sched_empty[i], 11);  // two producers, MMA, eight compute warps
@@ -389,8 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       };
       // accumulator (col) += weights (16-bit, 64 keys or rows at columns w and w + 64) times
-      // ring slot i, which is let go
-      auto weigh = [&](uint32_t w, int i, uint32_t col, bool fresh, uint64_t* more) {
+      // ring slot i, which is let go when done
+      auto weigh = [&](uint32_t w, int i, uint32_t col, bool fresh, bool done, uint64_t* more) {
         const uint64_t bd = sdesc_at(bm, i * TB);
         tc_fence_after();
         if (elect_one()) {
@@ -398,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 8; ++x)
             mma_ts(tmem + col, tmem + w + (x & 3) * 8 + (x >> 2) * 64, sdesc_at(bd, x * 2048), idA,
                    !fresh || x > 0);
-          mma_commit(&S.empty[i]);
+          if (done) mma_commit(&S.empty[i]);
           if (more) mma_commit(more);
         }
         __syncwarp();
@@ -417,54 +436,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (T > 0) {
           wait(&S.r_full, used & 1);
           ++used;
-          if constexpr (!DKV) {
-            wait_a(ts);
-            scores(a1, slot_a(ts), (ts & 1) * 128, &S.s_full[ts & 1]);
-            wait_b(ts);
-            scores(a2, slot_b(ts), kDP, &S.dp_full);
-            commit(&S.empty[slot_b(ts)]);
-            if (T > 1) {
-              wait_a(ts + 1);
-              scores(a1, slot_a(ts + 1), ((ts + 1) & 1) * 128, &S.s_full[(ts + 1) & 1]);
+          const bool mend = MEND && u.mend;
+          // S of tile ts + i of the unit's T; its buffer, P and dS columns
+          auto buf = [&](uint32_t t) { return TWO_S ? (t & 1) : 0u; };
+          auto next_s = [&](uint32_t t) {
+            wait_a(t);
+            if (!TWO_S && t != ts) wait(&S.s_free, (t - 1) & 1);
+            scores(a1, slot_a(t), buf(t) * 128, &S.s_full[buf(t)]);
+          };
+          auto next_dp = [&](uint32_t t) {
+            scores(a2, slot_b(t), kDP, &S.dp_full);
+            if (!DKV) commit(&S.empty[slot_b(t)]);
+          };
+          next_s(ts);
+          wait_b(ts);
+          next_dp(ts);
+          if (TWO_S && T > 1) next_s(ts + 1);
+          if (T == 1) commit(&S.r_empty);
+          for (int t = 0; t < T; ++t, ++ts) {
+            const bool more = t + 1 < T;
+            if (!TWO_S && more) next_s(ts + 1);  // under this tile's exponentials
+            if (more) wait_b(ts + 1);
+            wait(&S.ds_ready, ts & 1);
+            uint64_t* full = more ? nullptr : &S.acc_full;
+            const uint32_t cp = TWO_S ? buf(ts) * 128 : kDP;
+            if (TWO_S && more) next_dp(ts + 1);
+            if constexpr (DKV) {
+              weigh(cp, slot_b(ts), kDV, t == 0, true, nullptr);
+              weigh(cp + 32, slot_a(ts), kDK, t == 0, true, full);
             } else {
-              commit(&S.r_empty);
+              if (mend) weigh(cp, slot_a(ts), kKB, t == 0, false, nullptr);
+              weigh(cp + 32, slot_a(ts), kDQ, t == 0, true, full);
             }
-            for (int t = 0; t < T; ++t, ++ts) {
-              if (t + 1 < T) wait_b(ts + 1);
-              wait(&S.ds_ready, ts & 1);
-              if (t + 1 < T) {
-                scores(a2, slot_b(ts + 1), kDP, &S.dp_full);
-                commit(&S.empty[slot_b(ts + 1)]);
-                if (t + 2 == T) commit(&S.r_empty);
-              }
-              weigh((ts & 1) * 128, slot_a(ts), kDQ, t == 0, t + 1 == T ? &S.acc_full : nullptr);
-              if (t + 2 < T) {
-                wait_a(ts + 2);
-                scores(a1, slot_a(ts + 2), (ts & 1) * 128, &S.s_full[ts & 1]);
-              }
-            }
-          } else {
-            wait_a(ts);
-            scores(a1, slot_a(ts), 0, &S.s_full[0]);
-            wait_b(ts);
-            scores(a2, slot_b(ts), kDP, &S.dp_full);
-            if (T == 1) commit(&S.r_empty);
-            for (int t = 0; t < T; ++t, ++ts) {
-              if (t + 1 < T) {
-                // under this tile's exponentials
-                wait_a(ts + 1);
-                wait(&S.s_free, ts & 1);
-                scores(a1, slot_a(ts + 1), 0, &S.s_full[0]);
-                wait_b(ts + 1);
-              }
-              wait(&S.ds_ready, ts & 1);
-              weigh(kDP, slot_b(ts), kDV, t == 0, nullptr);
-              weigh(kDP + 32, slot_a(ts), kDK, t == 0, t + 1 == T ? &S.acc_full : nullptr);
-              if (t + 1 < T) {
-                scores(a2, slot_b(ts + 1), kDP, &S.dp_full);
-                if (t + 2 == T) commit(&S.r_empty);
-              }
-            }
+            if (!TWO_S && more) next_dp(ts + 1);
+            if (t + 2 == T) commit(&S.r_empty);
+            if (TWO_S && t + 2 < T) next_s(ts + 2);
           }
         }
         if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
@@ -483,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const float sc2 = a.scale * kLog2e;
     bool ok = true;
-    uint32_t ts = 0, us = 0;  // tiles, units with tiles so far
+    uint32_t ts = 0, us = 0, rs = 0;  // tiles, units with tiles, mended units so far
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       ok = __all_sync(0xffffffffu, bar_wait(bar, parity, limit, abort));
       return ok;
@@ -494,9 +500,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!u.live) break;
       const Job& job = DKV ? a.job[u.job] : a.qjob[u.job];
       const int t0 = u.t0, t1 = u.t1;
+      const bool mend = MEND && u.mend;
       // live columns of this thread's row, in the unit's tile numbering
       int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0;
       float nl = 0.f, nd = 0.f;  // query-major: -LSE log2(e), -D
+      float r0 = 0.f, r1 = 0.f;  // mend: sums of dS
       if constexpr (DKV) {
         if (u.r0 + row < n_keys(u.q, job.seg[0].kview)) {
           live_queries(g, u.q, job.seg[0].rule, u.r0 + row, lo0, hi0);
@@ -520,16 +528,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int tsplit = DKV ? t1 : u.cnt0;
       for (int t = t0; t < t1; ++t, ++ts) {
-        const int buf = DKV ? 0 : (int)(ts & 1);
-        const uint32_t tS = tmem + tl + (DKV ? 0 : buf * 128) + w * 64;
-        const uint32_t tP = tmem + tl + kDP + w * 64;
-        if (!wait(&S.s_full[buf], DKV ? (ts & 1) : ((ts >> 1) & 1))) break;
+        const int buf = TWO_S ? (int)(ts & 1) : 0;
+        const uint32_t tS = tmem + tl + buf * 128 + w * 64, tDP = tmem + tl + kDP + w * 64;
+        const uint32_t tP = TWO_S ? tS : tDP;  // where P and dS go
+        if (!wait(&S.s_full[buf], (TWO_S ? ts >> 1 : ts) & 1)) break;
         tc_fence_after();
         float p[64];
         tmem_ld32(tS, reinterpret_cast<uint32_t*>(p));
         tmem_ld32(tS + 32, reinterpret_cast<uint32_t*>(p) + 32);
         tmem_wait_ld();
-        if constexpr (DKV) {
+        if (!TWO_S) {
           tc_fence_before();
           mbar_arrive(&S.s_free);
         }
@@ -551,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int x = 0; x < 64; ++x) p[x] = fast_exp2(p[x]);
-        uint32_t pk[32], pp[DKV ? 32 : 1];
-        if constexpr (DKV) {
+        uint32_t pk[32], pp[32];
+        if (DKV || mend) {
 #pragma unroll
           for (int x = 0; x < 32; ++x) pp[x] = pack2<F16>(p[2 * x], p[2 * x + 1]);
         }
@@ -561,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float dp[32];
-          tmem_ld32(tP + c * 32, reinterpret_cast<uint32_t*>(dp));
+          tmem_ld32(tDP + c * 32, reinterpret_cast<uint32_t*>(dp));
           tmem_wait_ld();
           if constexpr (DKV) {
             const float4* Dl = reinterpret_cast<const float4*>(S.ndel[ts & 1] + w * 64 + c * 32);
@@ -580,6 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float* y = p + c * 32 + x;
               fadd2(dp[x], dp[x + 1], dp[x], dp[x + 1], nd, nd);
               fmul2(y[0], y[1], y[0], y[1], dp[x], dp[x + 1]);
+              if constexpr (MEND) fadd2(r0, r1, r0, r1, y[0], y[1]);
             }
           }
 #pragma unroll
@@ -588,11 +597,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (DKV) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&S.row_empty[ts & 1]);
-          tmem_st32(tP, pp);
-          tmem_st32(tP + 32, pk);
-        } else {
-          tmem_st32(tS, pk);
         }
+        if (DKV || mend) tmem_st32(tP, pp);
+        tmem_st32(tP + 32, pk);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&S.ds_ready);
@@ -602,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (!DKV) {
         QRow qr;
         const bool have = query_at(g, u.q, job.qview, u.hs, u.r0 + row, qr);
+        if (!have) qr = QRow{0, 0, 0};
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
         if (t1 > t0) {
@@ -609,34 +617,74 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++us;
           tc_fence_after();
         }
-#pragma unroll 1
-        for (int c = w * (D / 2); c < (w + 1) * (D / 2); c += 32) {
-          float o[32];
+        const size_t rr = have ? (size_t)qr.t * g.H + qr.h : 0;
+        uint16_t* out = static_cast<uint16_t*>(a.dq) + ((size_t)qr.t * a.dq_rows.tok + qr.h * a.dq_rows.head) * D;
+        const bool wide = (reinterpret_cast<uintptr_t>(a.dq) & 31) == 0;
+        auto load = [&](float* o, uint32_t col) {
           if (t1 > t0) {
-            tmem_ld32(tmem + tl + kDQ + c, reinterpret_cast<uint32_t*>(o));
+            tmem_ld32(tmem + tl + col, reinterpret_cast<uint32_t*>(o));
             tmem_wait_ld();
           }
-          if (!have) continue;
 #pragma unroll
           for (int x = 0; x < 32; ++x) o[x] = t1 > t0 ? o[x] * a.scale : 0.f;
-          float4* part = reinterpret_cast<float4*>(a.dq_part + ((size_t)qr.t * g.H + qr.h) * D + c);
-          if (a.mode == OUT_PARTIAL) {
-            store_row32(reinterpret_cast<float*>(part), o);
-            continue;
-          }
-          if (a.mode == OUT_MERGE) {
+        };
+        auto add = [&](float* o, const float* part) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              const float4 f = part[x];
-              o[4 * x] += f.x;
-              o[4 * x + 1] += f.y;
-              o[4 * x + 2] += f.z;
-              o[4 * x + 3] += f.w;
-            }
+          for (int x = 0; x < 32; x += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(part + x);
+            o[x] += f.x;
+            o[x + 1] += f.y;
+            o[x + 2] += f.z;
+            o[x + 3] += f.w;
           }
-          store_row16<F16>(static_cast<uint16_t*>(a.dq) +
-                               ((size_t)qr.t * a.dq_rows.tok + qr.h * a.dq_rows.head) * D + c,
-                           o, (reinterpret_cast<uintptr_t>(a.dq) & 31) == 0);
+        };
+        if (mend) {
+          float r = 0.f;  // what D lost: both warpgroups' columns, both orders
+          if (t1 > t0) {
+            S.ndel[w][row] = r0 + r1;
+            mbar_arrive(&S.r_sum);
+            if (!wait(&S.r_sum, rs & 1)) break;
+            ++rs;
+            r = S.ndel[0][row] + S.ndel[1][row];
+          }
+          if (have && a.mode == OUT_MERGE) r += a.r_part[rr];
+          if (have && w == 0) {
+            if (a.mode == OUT_PARTIAL) a.r_part[rr] = r;
+            else a.delta[rr] = r - nd;  // for the key-major kernel; this unit has read its rows
+          }
+#pragma unroll 1
+          for (int c = w * (D / 2); c < (w + 1) * (D / 2); c += 32) {
+            float o[32], kb[32];
+            load(o, kDQ + c);
+            load(kb, kKB + c);
+            if (!have) continue;
+            const size_t at = rr * D + c;
+            if (a.mode == OUT_PARTIAL) {
+              store_row32(a.dq_part + at, o);
+              store_row32(a.kb_part + at, kb);
+              continue;
+            }
+            if (a.mode == OUT_MERGE) {
+              add(o, a.dq_part + at);
+              add(kb, a.kb_part + at);
+            }
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = fmaf(-r, kb[x], o[x]);
+            store_row16<F16>(out + c, o, wide);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = w * (D / 2); c < (w + 1) * (D / 2); c += 32) {
+            float o[32];
+            load(o, kDQ + c);
+            if (!have) continue;
+            if (a.mode == OUT_PARTIAL) {
+              store_row32(a.dq_part + rr * D + c, o);
+              continue;
+            }
+            if (a.mode == OUT_MERGE) add(o, a.dq_part + rr * D + c);
+            store_row16<F16>(out + c, o, wide);
+          }
         }
         tc_fence_before();
       } else {
@@ -682,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool F16, bool DKV>
+template <int D, bool F16, bool DKV, bool MEND>
 cudaError_t launch(const BwdLaunch& a) {
   const Geo& g = a.g;
   TileMaps m = {};
@@ -692,26 +740,28 @@ cudaError_t launch(const BwdLaunch& a) {
     return cudaErrorInvalidValue;
   const size_t smem = sizeof(Smem<D>);
   static_assert(sizeof(Smem<D>) <= 232448, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(ragged_bwd_tc<D, F16, DKV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(ragged_bwd_tc<D, F16, DKV, MEND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
   const long long slots = slot_count(g, DKV ? 1 : most_heads(g, a.qjob[0].hc), 128);
   const long long units = slots * g.Hkv * (DKV ? a.njobs * a.nsplit : a.nqjobs);
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
-  ragged_bwd_tc<D, F16, DKV><<<(unsigned)units, kThreads, smem, a.stream>>>(a, m, (int)slots);
+  ragged_bwd_tc<D, F16, DKV, MEND><<<(unsigned)units, kThreads, smem, a.stream>>>(a, m, (int)slots);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t tc_ragged_dq(const BwdLaunch& a, int dtype) {
-  if (a.g.d == 64) return dtype == ST_F16 ? launch<64, true, false>(a) : launch<64, false, false>(a);
-  return dtype == ST_F16 ? launch<128, true, false>(a) : launch<128, false, false>(a);
+  const bool h = dtype == ST_F16;
+  if (a.g.d == 64) return h ? launch<64, true, false, true>(a) : launch<64, false, false, true>(a);
+  if (a.mend_tiles) return h ? launch<128, true, false, true>(a) : launch<128, false, false, true>(a);
+  return h ? launch<128, true, false, false>(a) : launch<128, false, false, false>(a);
 }
-
 cudaError_t tc_ragged_dkv(const BwdLaunch& a, int dtype) {
-  if (a.g.d == 64) return dtype == ST_F16 ? launch<64, true, true>(a) : launch<64, false, true>(a);
-  return dtype == ST_F16 ? launch<128, true, true>(a) : launch<128, false, true>(a);
+  const bool h = dtype == ST_F16;
+  if (a.g.d == 64) return h ? launch<64, true, true, false>(a) : launch<64, false, true, false>(a);
+  return h ? launch<128, true, true, false>(a) : launch<128, false, true, false>(a);
 }
 
 }  // namespace rag

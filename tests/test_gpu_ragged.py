@@ -100,6 +100,42 @@ def test_packed_longer_sequences(dtype, d):
     packed(("fixed", "split", 64, 8), 4, 2, d, dtype, [2300], backward=True)
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f16", 128)])
+@pytest.mark.parametrize("pat", [("dense", "merged", 1, 1), ("fixed", "split", 20, 9), ("strided", "merged", 10, 1), ("strided", "split", 200, 1)], ids=str)
+def test_many_units_of_different_lengths(pat, dtype, d):
+    """Several units for every CTA, of no, few and many key tiles, one behind the other."""
+    packed(pat, 24, 6, d, dtype, [1500, 3, 0, 700, 129, 1, 260], backward=True)
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each, started together and repeated: each keeps its results."""
+    P = st.st_pattern("strided", "merged", 24)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    data, want = [], []
+    for n in (1500, 1100):
+        q, k, v, dout = (randn(g, n, h, 64, dtype=torch.bfloat16) for h in (8, 4, 4, 8))
+        data.append((q, k, v, dout, starts([n - 300, 300]), n))
+
+    def run(x, stream=None):
+        q, k, v, dout, cu, n = x
+        o, lse = st.st_packed_attn_fwd(P, q, k, v, cu, n, stream=stream)
+        return (o, lse, *st.st_packed_attn_bwd(P, q, k, v, o, lse, dout, cu, n, stream=stream))
+
+    want = [run(x) for x in data]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in data]
+    got = [[] for _ in data]
+    for _ in range(5):
+        for i, x in enumerate(data):
+            got[i].append(run(x, streams[i]))
+    torch.cuda.synchronize()
+    assert st.st_last_device_status() == st.ST_OK
+    for w, all_of in zip(want, got):
+        for out in all_of:
+            for a, b in zip(w, out):
+                assert torch.equal(a, b)
+
+
 def test_large_scores_and_given_scale():
     # scores up to about +-60: the running maximum moves by far more than a rounding
     packed(("dense", "merged", 1, 1), 2, 1, 64, "bf16", [700, 300], std=3.0, backward=True)
