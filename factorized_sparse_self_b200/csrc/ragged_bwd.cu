@@ -39,7 +39,8 @@ namespace rag {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kSched = 2;
+constexpr int kSched = 2;  // ring of decoded units
+constexpr int kAhead = 2;  // tiles before a unit's end at which the next is claimed
 constexpr uint32_t kRegsCompute = 200, kRegsIssue = 104;  // 168 at launch: 2 * 200 + 104 = 3 * 168
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -76,8 +77,8 @@ struct alignas(1024) Smem {
   uint64_t row_full[2], row_empty[2];
   uint64_t sched_full[kSched], sched_empty[kSched];
   uint64_t fin;
-  alignas(16) uint4 claim[2];
-  uint64_t claim_bar[2];
+  alignas(16) uint4 claim;
+  uint64_t claim_bar, want;
   BUnit unit[kSched];
   uint32_t tmem;
   int abort;
@@ -181,7 +182,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.row_full[i], 2);
       mbar_init(&S.row_empty[i], 8);
-      mbar_init(&S.claim_bar[i], 1);
     }
     mbar_init(&S.s_full[0], 1);
     mbar_init(&S.s_full[1], 1);
@@ -195,6 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.sched_empty[i], 11);  // two producers, MMA, eight compute warps
     }
     mbar_init(&S.fin, 1);
+    mbar_init(&S.claim_bar, 1);
+    mbar_init(&S.want, 1);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -220,17 +222,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         return k < kSched || __all_sync(0xffffffffu, bar_wait(&S.sched_empty[k % kSched],
                                                               (k / kSched + 1) & 1, limit, abort));
       };
-      Claims claims = {S.claim, S.claim_bar, 0};
-      if (lane == 0) claims_issue(claims, 0);
+      Claims claims = {&S.claim, &S.claim_bar, &S.want, 0, 0};
       for (int n = blockIdx.x; n >= 0;) {
         ok = slot_free();
         if (!ok) break;
-        if (decode<DKV>(a, slots, n, &S.unit[k % kSched])) {
+        const bool some = decode<DKV>(a, slots, n, &S.unit[k % kSched]);
+        if (some) {
           __threadfence_block();
           if (lane == 0) mbar_arrive(&S.sched_full[k % kSched]);
           ++k;
         }
-        n = claims_take(claims, limit, abort);
+        n = claims_take(claims, some, limit, abort);
         ok = n != -2;
       }
       if (ok) ok = slot_free();
@@ -241,11 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) {
         if (lane == 0) fail();
-        // a claim in flight lands before the CTA may exit
-        const int last = claims.n > 0 ? claims.n - 1 : 0;
-        mbar_wait_drain(&S.claim_bar[last & 1], (last >> 1) & 1, limit);
-        if (claimed(&S.claim[last & 1]) >= 0)
-          mbar_wait_drain(&S.claim_bar[(last + 1) & 1], ((last + 1) >> 1) & 1, limit);
+        claims_drain(claims, limit);
       }
     } else if (warp != 9) {
       // ---------------- producers ----------------
@@ -299,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             gath.add(&S.r_full);
           }
           for (int t = u.t0; t < u.t1; ++t, ++tt) {
+            if (pw == 0 && lane == 0 && t == imax(u.t0, u.t1 - kAhead)) mbar_arrive(&S.want);
             int view = 0, j = t, R;
             if constexpr (DKV) {
               R = job.qview == VIEW_NAT && j * 128 + 128 <= xrows ? maps.q_tokens : 0;
@@ -362,6 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
           }
           if (!ok) break;
+        } else if (pw == 0 && lane == 0) {
+          mbar_arrive(&S.want);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);

@@ -26,7 +26,8 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kRows = 256;  // query rows of a unit
-constexpr int kSched = 3;   // units decoded ahead
+constexpr int kSched = 2;   // ring of decoded units
+constexpr int kAhead = 2;   // tiles before a unit's end at which the next is claimed
 constexpr uint32_t kRegsSoftmax = 208, kRegsIssue = 88;  // 168 at launch: 2 * 208 + 88 = 3 * 168
 constexpr float kRescale = 8.f;  // log2
 constexpr float kLn2 = 0.69314718055994531f;
@@ -47,8 +48,8 @@ struct alignas(1024) Smem {
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t sched_full[kSched], sched_empty[kSched];
   uint64_t fin;
-  alignas(16) uint4 claim[2];
-  uint64_t claim_bar[2];
+  alignas(16) uint4 claim;
+  uint64_t claim_bar, want;
   Unit unit[kSched];
   uint32_t tmem;
   int abort;
@@ -83,8 +84,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.sched_empty[i], 11);  // two producers, MMA, eight softmax warps
     }
     mbar_init(&S.fin, 1);
-    mbar_init(&S.claim_bar[0], 1);
-    mbar_init(&S.claim_bar[1], 1);
+    mbar_init(&S.claim_bar, 1);
+    mbar_init(&S.want, 1);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -110,17 +111,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         return k < kSched || __all_sync(0xffffffffu, bar_wait(&S.sched_empty[k % kSched],
                                                                (k / kSched + 1) & 1, limit, abort));
       };
-      Claims claims = {S.claim, S.claim_bar, 0};
-      if (lane == 0) claims_issue(claims, 0);
+      Claims claims = {&S.claim, &S.claim_bar, &S.want, 0, 0};
       for (int n = blockIdx.x; n >= 0;) {
         ok = slot_free();
         if (!ok) break;
-        if (decode_unit(a, slots, n, kRows, &S.unit[k % kSched])) {
+        const bool some = decode_unit(a, slots, n, kRows, &S.unit[k % kSched]);
+        if (some) {
           __threadfence_block();
           if (lane == 0) mbar_arrive(&S.sched_full[k % kSched]);
           ++k;
         }
-        n = claims_take(claims, limit, abort);
+        n = claims_take(claims, some, limit, abort);
         ok = n != -2;
       }
       if (ok) ok = slot_free();
@@ -131,10 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) {
         if (lane == 0) fail();
-        // a claim in flight lands before the CTA may exit
-        const int last = claims.n > 0 ? claims.n - 1 : 0;
-        mbar_wait_drain(&S.claim_bar[last & 1], (last >> 1) & 1, limit);
-        if (claimed(&S.claim[last & 1]) >= 0) mbar_wait_drain(&S.claim_bar[(last + 1) & 1], ((last + 1) >> 1) & 1, limit);
+        claims_drain(claims, limit);
       }
     } else if (warp != 9) {
       // ---------------- producers ----------------
@@ -179,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             gath.add(&S.q_full[qb]);
           }
           for (int t = u.t0; t < u.t1 && ok; ++t) {
+            if (pw == 0 && lane == 0 && t == imax(u.t0, u.t1 - kAhead)) mbar_arrive(&S.want);
             int seg, j;
             unit_tile(u, t, seg, j);
             const int view = job.seg[seg].kview, R = box_rows(maps, g, u.q, view, j);
@@ -205,6 +204,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (!ok) break;
+        } else if (pw == 0 && lane == 0) {
+          mbar_arrive(&S.want);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);

@@ -255,29 +255,38 @@ __device__ __forceinline__ int claimed(const void* src) {
   return ok ? (int)x : -1;
 }
 
-// One scheduler warp's claims, one ahead.
+// One scheduler warp's claims. The next unit is claimed when the producers come to
+// the last tiles of the current one (`want`, one arrival a unit), not before: a CTA
+// that claims while its long unit runs keeps short ones from idle SMs (dense, 4096
+// tokens, 256 key-major units on 148 SMs: SMs busy 69 % of the time with two units
+// claimed ahead).
 struct Claims {
-  uint4* slot;     // [2], shared memory
-  uint64_t* bar;   // [2]
-  int n;           // claims taken
+  uint4* slot;    // shared memory
+  uint64_t* bar;
+  uint64_t* want;
+  int n, units;   // claims made, units handed on
 };
-__device__ __forceinline__ void claims_issue(const Claims& c, int k) {
-  mbar_arrive_expect_tx(&c.bar[k & 1], 16);
-  claim_next(&c.slot[k & 1], &c.bar[k & 1]);
-}
-// Next unit index (by a whole warp): -1 when the grid is used up, -2 when the
-// wait ran out. The claim after it is asked for before this one is used.
-__device__ __forceinline__ int claims_take(Claims& c, uint64_t limit, volatile int* abort) {
-  const int k = c.n++;
-  if (!__all_sync(0xffffffffu, bar_wait(&c.bar[k & 1], (k >> 1) & 1, limit, abort))) return -2;
-  const int got = claimed(&c.slot[k & 1]);
-  __syncwarp();
-  if (got >= 0 && (threadIdx.x & 31) == 0) {
-    fence_async_smem();  // the answer in the other slot was read before it is written anew
-    claims_issue(c, k + 1);
+// Next unit index (by a whole warp): -1 when the grid is used up, -2 when a wait
+// ran out.
+__device__ __forceinline__ int claims_take(Claims& c, bool handed_on, uint64_t limit, volatile int* abort) {
+  if (handed_on) {
+    const int u = c.units++;
+    if (!__all_sync(0xffffffffu, bar_wait(c.want, u & 1, limit, abort))) return -2;
   }
+  if ((threadIdx.x & 31) == 0) {
+    fence_async_smem();  // the answer before this one was read
+    mbar_arrive_expect_tx(c.bar, 16);
+    claim_next(c.slot, c.bar);
+  }
+  const int k = c.n++;
+  if (!__all_sync(0xffffffffu, bar_wait(c.bar, k & 1, limit, abort))) return -2;
+  const int got = claimed(c.slot);
   __syncwarp();
   return got;
+}
+// After a wait that ran out: a claim in flight lands before the CTA may exit.
+__device__ __forceinline__ void claims_drain(const Claims& c, uint64_t limit) {
+  if (c.n > 0) mbar_wait_drain(c.bar, (c.n - 1) & 1, limit);
 }
 
 // Host: the boxes of a launch. False when the driver refuses one.
