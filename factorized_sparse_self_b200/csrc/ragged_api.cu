@@ -176,8 +176,8 @@ int clamp_int(long long x, long long lo, long long hi) {
 // by one, so only few units leave SMs idle: those of one longest sequence (the
 // others may be short) have to be worth the GPU. A prompt's units see 1 .. T
 // keys, the longest ones first; a chunk's see all of the context, so they should
-// come in threes per SM. Dense, H = 32, Hkv = 8, d = 128, chunks of 512 tokens behind
-// 32 K, 8 K, 4 K keys: 508, 451, 471, 498 us with 2, 3, 4, 6 per SM.
+// come in twos per SM. Dense, H = 32, Hkv = 8, d = 128, chunks of 512 tokens behind
+// 32 K, 8 K, 4 K keys: 440, 444, 465 us with 2, 3, 4 per SM.
 FwdPlan plan_fwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype, long long max_q, bool paged) {
   FwdPlan f{};
   const long long sms = sm_count(), keys = most_keys(p);
@@ -197,7 +197,7 @@ FwdPlan plan_fwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype, long lo
   } else {
     f.least = 512 / key_tile;
     long long n = 1;
-    if (all < 4 * sms) n = paged ? (3 * sms + longest - 1) / longest : (sms + longest - 1) / longest;
+    if (all < 4 * sms) n = paged ? (2 * sms + longest - 1) / longest : (sms + longest - 1) / longest;
     f.nsplit = clamp_int(std::min(n, keys / 512), 1, std::min<long long>(fit, kPartsLimit));
     // ranges of one length: shorter sequences are cut into fewer
     f.least = (int)std::max<long long>(f.least, (keys + key_tile - 1) / key_tile / f.nsplit);

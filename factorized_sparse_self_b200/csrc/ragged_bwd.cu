@@ -40,7 +40,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kSched = 2;  // ring of decoded units
-constexpr int kAhead = 2;  // tiles before a unit's end at which the next is claimed
+constexpr int kAhead = 3;  // tiles before a unit's end at which the next is claimed
 constexpr uint32_t kRegsCompute = 200, kRegsIssue = 104;  // 168 at launch: 2 * 200 + 104 = 3 * 168
 constexpr float kLog2e = 1.4426950408889634f;
 

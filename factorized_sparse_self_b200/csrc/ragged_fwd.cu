@@ -27,7 +27,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kRows = 256;  // query rows of a unit
 constexpr int kSched = 2;   // ring of decoded units
-constexpr int kAhead = 2;   // tiles before a unit's end at which the next is claimed
+constexpr int kAhead = 3;   // tiles before a unit's end at which the next is claimed
 constexpr uint32_t kRegsSoftmax = 208, kRegsIssue = 88;  // 168 at launch: 2 * 208 + 88 = 3 * 168
 constexpr float kRescale = 8.f;  // log2
 constexpr float kLn2 = 0.69314718055994531f;
