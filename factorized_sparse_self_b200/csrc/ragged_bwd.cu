@@ -50,6 +50,9 @@ struct Cfg {
   // ring slots of the first streamed operand (K or Q, held until the tile's last
   // product) and of the second (V or dO, let go earlier)
   static constexpr int kA = D == 64 ? 4 : 3, kB = D == 64 ? 4 : 2;
+  // resident buffers: with two the next unit's rows load under this one (d = 128
+  // has no room)
+  static constexpr int kRes = D == 64 ? 2 : 1;
 };
 
 // 128 rows of one (sequence, key/value head): query rows or keys.
@@ -67,11 +70,11 @@ struct BUnit {
 
 template <int D>
 struct alignas(1024) Smem {
-  uint8_t res[2][Cfg<D>::kTileBytes];  // Q, dO or K, V
+  uint8_t res[Cfg<D>::kRes][2][Cfg<D>::kTileBytes];  // Q, dO or K, V
   uint8_t ring[Cfg<D>::kA + Cfg<D>::kB][Cfg<D>::kTileBytes];
   float nlse[2][128], ndel[2][128];    // key-major: -LSE log2(e) and -D of a tile's query rows
                                        // (mend: ndel holds the two halves of r)
-  uint64_t r_full, r_empty;
+  uint64_t r_full[Cfg<D>::kRes], r_empty[Cfg<D>::kRes];
   uint64_t full[Cfg<D>::kA + Cfg<D>::kB], empty[Cfg<D>::kA + Cfg<D>::kB];
   uint64_t s_full[2], s_free, dp_full, ds_ready, acc_full, r_sum;
   uint64_t row_full[2], row_empty[2];
@@ -159,7 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ragged_bwd_tc(const __grid_constant__ BwdLaunch a, const __grid_constant__ TileMaps maps, int slots) {
   extern __shared__ __align__(1024) uint8_t raw[];
   Smem<D>& S = *reinterpret_cast<Smem<D>*>(raw);
-  constexpr int NA = Cfg<D>::kA, NB = Cfg<D>::kB, NS = NA + NB, TB = Cfg<D>::kTileBytes;
+  constexpr int NA = Cfg<D>::kA, NB = Cfg<D>::kB, NS = NA + NB, TB = Cfg<D>::kTileBytes,
+                NR = Cfg<D>::kRes;
   constexpr bool TWO_S = !DKV && (D == 64 || !MEND);
   constexpr uint32_t kDP = TWO_S ? 256 : 128, kAcc = kDP + 128;
   constexpr uint32_t kDQ = kAcc, kKB = kAcc + D, kDV = kAcc, kDK = kAcc + D;
@@ -173,8 +177,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     S.abort = 0;
-    mbar_init(&S.r_full, 2);  // both producers
-    mbar_init(&S.r_empty, 1);
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(&S.r_full[i], 2);  // both producers
+      mbar_init(&S.r_empty[i], 1);
+    }
     for (int i = 0; i < NS; ++i) {
       mbar_init(&S.full[i], 2);
       mbar_init(&S.empty[i], 1);
@@ -275,15 +281,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pos = key_pos(g, u.q, view, imin(e, n_keys(u.q, view) - 1));
             kv_rows(g, u.q, pos, u.kvh, rk, rv);
           };
-          if (used > 0 && !wait(&S.r_empty, (used - 1) & 1)) break;
+          const int rs = used % NR;
+          if (used >= NR && !wait(&S.r_empty[rs], (used / NR + 1) & 1)) break;
           ++used;
           const int rview = job.seg[0].kview;
           const int rbox = DKV ? box_rows(maps, g, u.q, rview, u.r0 / 128)
                                : (job.qview == VIEW_NAT && u.r0 + 128 <= xrows ? maps.q_tokens : 0);
           if (rbox) {
             // each producer loads one of the two tiles
-            if (DKV) load_boxes<D>(smem_u32(S.res[pw]), maps, pw, &S.r_full, g, u.q, rview, u.r0 / 128, u.kvh, rbox);
-            else load_query_boxes<D>(smem_u32(S.res[pw]), pw ? &maps.dout : &maps.q, &S.r_full, maps, u.q, u.hs, u.r0);
+            if (DKV) load_boxes<D>(smem_u32(S.res[rs][pw]), maps, pw, &S.r_full[rs], g, u.q, rview, u.r0 / 128, u.kvh, rbox);
+            else load_query_boxes<D>(smem_u32(S.res[rs][pw]), pw ? &maps.dout : &maps.q, &S.r_full[rs], maps, u.q, u.hs, u.r0);
           } else {
             int ra[2], rb[2];
 #pragma unroll
@@ -292,9 +299,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (DKV) key_rows(job.seg[0].kview, e, ra[y], rb[y]);
               else query_rows(e, ra[y], rb[y]);
             }
-            gather64<D>(smem_u32(S.res[0]), pw * 64, DKV ? a.k : a.q, ra[0], ra[1]);
-            gather64<D>(smem_u32(S.res[1]), pw * 64, DKV ? a.v : a.dout, rb[0], rb[1]);
-            gath.add(&S.r_full);
+            gather64<D>(smem_u32(S.res[rs][0]), pw * 64, DKV ? a.k : a.q, ra[0], ra[1]);
+            gather64<D>(smem_u32(S.res[rs][1]), pw * 64, DKV ? a.v : a.dout, rb[0], rb[1]);
+            gath.add(&S.r_full[rs]);
           }
           for (int t = u.t0; t < u.t1; ++t, ++tt) {
             if (pw == 0 && lane == 0 && t == imax(u.t0, u.t1 - kAhead)) mbar_arrive(&S.want);
@@ -329,8 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const int NR = i ? NB : NA, s = (i ? NA : 0) + tt % NR;
-              if (tt >= NR && !wait(&S.empty[s], (tt / NR + 1) & 1)) break;
+              const int n = i ? NB : NA, s = (i ? NA : 0) + tt % n;
+              if (tt >= n && !wait(&S.empty[s], (tt / n + 1) & 1)) break;
               if (!R) {
                 gather64<D>(smem_u32(S.ring[s]), pw * 64, DKV ? (i ? a.dout : a.q) : (i ? a.v : a.k),
                             i ? rb[0] : ra[0], i ? rb[1] : ra[1]);
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) {
         if (lane == 0) fail();
         // copies in flight land before the CTA may exit
-        if (used > 0) mbar_wait_drain(&S.r_full, (used - 1) & 1, limit);
+        for (int i = imax(0, used - NR); i < used; ++i) mbar_wait_drain(&S.r_full[i % NR], (i / NR) & 1, limit);
         for (int i = imax(0, tt - NA); i <= tt; ++i) mbar_wait_drain(&S.full[i % NA], (i / NA) & 1, limit);
         for (int i = imax(0, tt - NB); i <= tt; ++i) mbar_wait_drain(&S.full[NA + i % NB], (i / NB) & 1, limit);
       }
@@ -386,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ok = bar_wait(bar, parity, limit, abort);
         __syncwarp();
       };
-      const uint64_t a1 = sdesc(smem_u32(S.res[0]), 16, 1024), a2 = sdesc(smem_u32(S.res[1]), 16, 1024);
+      const uint64_t res0 = sdesc(smem_u32(S.res[0][0]), 16, 1024);
       const uint64_t bk = sdesc(smem_u32(S.ring[0]), 16, 1024), bm = sdesc(smem_u32(S.ring[0]), 16384, 1024);
       int used = 0;     // units with tiles
       uint32_t ts = 0;  // tiles so far
@@ -435,7 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!u.live) break;
         const int T = u.t1 - u.t0;
         if (T > 0) {
-          wait(&S.r_full, used & 1);
+          const int rb = used % NR;
+          const uint64_t a1 = sdesc_at(res0, rb * 2 * TB), a2 = sdesc_at(a1, TB);
+          wait(&S.r_full[rb], (used / NR) & 1);
           ++used;
           const bool mend = MEND && u.mend;
           // S of tile ts + i of the unit's T; its buffer, P and dS columns
@@ -453,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_b(ts);
           next_dp(ts);
           if (TWO_S && T > 1) next_s(ts + 1);
-          if (T == 1) commit(&S.r_empty);
+          if (T == 1) commit(&S.r_empty[rb]);
           for (int t = 0; t < T; ++t, ++ts) {
             const bool more = t + 1 < T;
             if (!TWO_S && more) next_s(ts + 1);  // under this tile's exponentials
@@ -470,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               weigh(cp + 32, slot_a(ts), kDQ, t == 0, true, full);
             }
             if (!TWO_S && more) next_dp(ts + 1);
-            if (t + 2 == T) commit(&S.r_empty);
+            if (t + 2 == T) commit(&S.r_empty[rb]);
             if (TWO_S && t + 2 < T) next_s(ts + 2);
           }
         }
