@@ -56,6 +56,7 @@ struct BwdLaunch {
   int32_t njobs;
   Job qjob[2];       // query jobs of this launch
   int32_t nqjobs, mode;
+  int32_t part_view;  // dK, dV by OUT_MERGE: keys that the first order's part holds
   const void *q, *k, *v, *dout;
   const float* lse;
   float* delta;  // mended in place
@@ -80,7 +81,8 @@ __device__ __forceinline__ bool job_reaches(const Geo& g, const Job& job, int kv
 // Whether kvh's dK, dV come from one unit alone and are written by it: one key
 // range, one job, and an order that lists every key.
 __device__ __forceinline__ bool dkv_direct(const BwdLaunch& a, int kvh) {
-  if (a.nsplit > 1) return false;
+  if (a.mode == OUT_MERGE) return true;
+  if (a.mode == OUT_PARTIAL || a.nsplit > 1) return false;
   int n = 0, view = VIEW_NAT;
   for (int j = 0; j < a.njobs; ++j)
     if (job_reaches(a.g, a.job[j], kvh)) {
@@ -88,6 +90,10 @@ __device__ __forceinline__ bool dkv_direct(const BwdLaunch& a, int kvh) {
       view = a.job[j].seg[0].kview;
     }
   return n == 1 && view != VIEW_SUM;
+}
+// Whether a view lists the key at a position of its sequence.
+__device__ __forceinline__ bool view_lists(const Geo& g, int view, int pos) {
+  return view != VIEW_SUM || pos - fdiv(pos, g.fl) * g.l >= g.l - g.c;
 }
 #endif
 

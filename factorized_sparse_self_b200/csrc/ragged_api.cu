@@ -263,7 +263,8 @@ st_status run_fwd(const st_pattern_desc& p, st_dtype dtype, Geo& g, float scale,
 struct BwdPlan {
   Job kjob[2];
   int njobs, nsplit;
-  bool parts;
+  bool parts;  // dK, dV are joined from parts
+  bool merge;  // the second launch adds the first one's part itself
   int mend_tiles;
   size_t delta, dq_part, parts_bytes, bytes;
 };
@@ -291,11 +292,19 @@ BwdPlan plan_bwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype) {
   if (units < sms && all < 2 * sms)
     b.nsplit = clamp_int(std::min((sms + units - 1) / units, (long long)p.T * g.G / 512), 1,
                          std::min<long long>(fit, kPartsLimit));
+  // Two jobs of every key head and units enough for each job to fill the GPU: the
+  // second order goes first and leaves a part, the first order lists every key and
+  // adds it. Backward, d = 64, H = 16, Hkv = 8, l = 32, strided, both patterns per head,
+  // 64, 256, 512, 1024 key tiles: 68, 154, 215, 373 us against one launch and a join's
+  // 57, 155, 236, 428.
+  const bool both = b.njobs == 2 && (!g.split || g.G > 1);
+  b.merge = both && b.nsplit == 1 && all >= 2 * sms;
   // one part is enough only where every key head has one job over all its keys
-  b.parts = b.nsplit > 1 || (b.njobs == 2 && !(g.split && g.G == 1 && b.kjob[1].seg[0].kview != VIEW_SUM));
+  b.parts = !b.merge && (b.nsplit > 1 || (b.njobs == 2 && (both || b.kjob[1].seg[0].kview == VIEW_SUM)));
   b.delta = round256(qrows * sizeof(float));
   b.dq_part = two_orders(p) ? round256(qrows * g.d * sizeof(float)) : 0;
-  b.parts_bytes = b.parts ? round256(krows * 2 * g.d * sizeof(float) * b.njobs * b.nsplit) : 0;
+  const int nparts = b.merge ? 1 : b.parts ? b.njobs * b.nsplit : 0;
+  b.parts_bytes = round256(krows * 2 * g.d * sizeof(float) * nparts);
   b.bytes = b.delta + b.dq_part + b.parts_bytes;
   if (b.dq_part && b.mend_tiles) b.bytes += b.delta + b.dq_part;
   return b;
@@ -413,7 +422,19 @@ st_status st_packed_attn_bwd(const st_pattern_desc* p, st_dtype dtype, const st_
     a.mode = OUT_FINAL;
     e = go_dq();
   }
-  if (e == cudaSuccess) e = dtype == ST_F32 ? simt_ragged_dkv(a) : tc_ragged_dkv(a, dtype);
+  auto go_dkv = [&]() { return dtype == ST_F32 ? simt_ragged_dkv(a) : tc_ragged_dkv(a, dtype); };
+  if (b.merge) {
+    a.njobs = 1;
+    a.part_view = b.kjob[1].seg[0].kview;
+    for (int j = 1; j >= 0 && e == cudaSuccess; --j) {
+      a.job[0] = b.kjob[j];
+      a.mode = j == 1 ? OUT_PARTIAL : OUT_MERGE;
+      e = go_dkv();
+    }
+  } else if (e == cudaSuccess) {
+    a.mode = OUT_FINAL;
+    e = go_dkv();
+  }
   if (e == cudaSuccess && b.parts) e = join_dkv(a, dtype);
   return e == cudaSuccess ? ST_OK : ST_ERR_CUDA;
 }

@@ -638,16 +638,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 32; ++x) o[x] = t1 > t0 ? o[x] * a.scale : 0.f;
         };
-        auto add = [&](float* o, const float* part) {
-#pragma unroll
-          for (int x = 0; x < 32; x += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(part + x);
-            o[x] += f.x;
-            o[x + 1] += f.y;
-            o[x + 2] += f.z;
-            o[x + 3] += f.w;
-          }
-        };
         if (mend) {
           float r = 0.f;  // what D lost: both warpgroups' columns, both orders
           if (t1 > t0) {
@@ -675,8 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               continue;
             }
             if (a.mode == OUT_MERGE) {
-              add(o, a.dq_part + at);
-              add(kb, a.kb_part + at);
+              add_row32(o, a.dq_part + at);
+              add_row32(kb, a.kb_part + at);
             }
 #pragma unroll
             for (int x = 0; x < 32; ++x) o[x] = fmaf(-r, kb[x], o[x]);
@@ -692,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               store_row32(a.dq_part + rr * D + c, o);
               continue;
             }
-            if (a.mode == OUT_MERGE) add(o, a.dq_part + rr * D + c);
+            if (a.mode == OUT_MERGE) add_row32(o, a.dq_part + rr * D + c);
             store_row16<F16>(out + c, o, wide);
           }
         }
@@ -700,9 +690,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         const int view = job.seg[0].kview, kvh = u.kvh;
         const bool have = u.r0 + row < n_keys(u.q, view);
-        const int tok = have ? u.q.qb + key_pos(g, u.q, view, u.r0 + row) : 0;
+        const int pos = have ? key_pos(g, u.q, view, u.r0 + row) : 0, tok = u.q.qb + pos;
         const bool direct = dkv_direct(a, kvh);
-        const int part = u.job * a.nsplit + u.split;
+        const bool add = a.mode == OUT_MERGE && view_lists(g, a.part_view, pos);
+        float* part = a.parts + (((size_t)(u.job * a.nsplit + u.split) * g.total + tok) * g.Hkv + kvh) * 2 * D + w * D;
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
         if (t1 > t0) {
@@ -724,11 +715,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!have) continue;
 #pragma unroll
           for (int x = 0; x < 32; ++x) o[x] = t1 > t0 ? o[x] * f : 0.f;
-          if (direct) {
-            store_row16<F16>(out + c, o, (reinterpret_cast<uintptr_t>(w ? a.dv : a.dk) & 31) == 0);
-          } else {
-            store_row32(a.parts + (((size_t)part * g.total + tok) * g.Hkv + kvh) * 2 * D + w * D + c, o);
-          }
+          if (add) add_row32(o, part + c);
+          if (direct) store_row16<F16>(out + c, o, (reinterpret_cast<uintptr_t>(w ? a.dv : a.dk) & 31) == 0);
+          else store_row32(part + c, o);
         }
         tc_fence_before();
       }

@@ -405,17 +405,23 @@ __global__ void __launch_bounds__(NT) ragged_dkv_simt(const __grid_constant__ Bw
   for (int i = 0; i < 4; ++i) {
     const int k = k0 + 4 * ty + i;
     if (k >= nk) continue;
-    const int t = q.qb + key_pos(g, q, view, k);
+    const int pos = key_pos(g, q, view, k), t = q.qb + pos;
+    float* p = a.parts + (((size_t)blockIdx.z * g.total + t) * g.Hkv + kvh) * 2 * D;
+    const bool add = a.mode == OUT_MERGE && view_lists(g, a.part_view, pos);
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
       const int c = tx + 16 * j;
+      dk[i][j] *= a.scale;
+      if (add) {
+        dk[i][j] += p[c];
+        dv[i][j] += p[D + c];
+      }
       if (direct) {
         static_cast<float*>(a.dk)[((size_t)t * a.dk_rows.tok + kvh * a.dk_rows.head) * D + c] =
-            dk[i][j] * a.scale;
+            dk[i][j];
         static_cast<float*>(a.dv)[((size_t)t * a.dv_rows.tok + kvh * a.dv_rows.head) * D + c] = dv[i][j];
       } else {
-        float* p = a.parts + (((size_t)blockIdx.z * g.total + t) * g.Hkv + kvh) * 2 * D;
-        p[c] = dk[i][j] * a.scale;
+        p[c] = dk[i][j];
         p[D + c] = dv[i][j];
       }
     }
@@ -548,10 +554,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j = 0; j < a.njobs; ++j) {
     if (!job_reaches(g, a.job[j], kvh)) continue;
-    if (a.job[j].seg[0].kview == VIEW_SUM) {
-      const int pos = token_pos(g, t);
-      if (pos - fdiv(pos, g.fl) * g.l < g.l - g.c) continue;
-    }
+    const int view = a.job[j].seg[0].kview;
+    if (view == VIEW_SUM && !view_lists(g, view, token_pos(g, t))) continue;
 #pragma unroll 4
     for (int p = j * a.nsplit; p < (j + 1) * a.nsplit; ++p) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(a.parts + (p * rows + row) * 2 * g.d + c));

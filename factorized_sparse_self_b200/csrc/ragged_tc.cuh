@@ -93,6 +93,17 @@ __device__ __forceinline__ void store_row32(float* dst, const float* o) {
 #pragma unroll
   for (int x = 0; x < 4; ++x) st_global_v8(dst + 8 * x, reinterpret_cast<const uint32_t*>(o) + 8 * x);
 }
+// o += 32 fp32 values of such a part.
+__device__ __forceinline__ void add_row32(float* o, const float* part) {
+#pragma unroll
+  for (int x = 0; x < 32; x += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(part + x);
+    o[x] += f.x;
+    o[x + 1] += f.y;
+    o[x + 2] += f.z;
+    o[x + 3] += f.w;
+  }
+}
 
 // ---- rows gathered into an operand tile -----------------------------------------
 // A tile is 128 rows of D 16-bit elements as D / 64 blocks of [128][64] with the

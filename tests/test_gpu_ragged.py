@@ -107,6 +107,15 @@ def test_many_units_of_different_lengths(pat, dtype, d):
     packed(pat, 24, 6, d, dtype, [1500, 3, 0, 700, 129, 1, 260], backward=True)
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f16", 128), ("f32", 64)])
+@pytest.mark.parametrize("pat", [("strided", "merged", 16, 1), ("strided", "split", 7, 1), ("fixed", "merged", 16, 4), ("fixed", "split", 40, 40),
+                                 ("fixed", "split", 20, 3)], ids=str)
+def test_many_key_units(pat, dtype, d):
+    """Key tiles enough for each key order to go by itself, the last one adding what the first one left."""
+    packed(pat, 72, 24, d, dtype, [900, 0, 1, 250, 129, 19, 385], backward=True)
+    packed(pat, 64, 32, d, dtype, [200] * 7, backward=True, fused=True, lead=3)
+
+
 def test_two_calls_at_once():
     """Two streams, a workspace each, started together and repeated: each keeps its results."""
     P = st.st_pattern("strided", "merged", 24)
