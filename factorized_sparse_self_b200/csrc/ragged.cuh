@@ -126,8 +126,7 @@ ST_HD int key_pos(const Geo& g, const Seq& q, int view, int e) {
     const int b = qdiv(e, g.fc, g.c);
     return b * g.l + (g.l - g.c) + (e - b * g.c);
   }
-  e += q.rotk;
-  if (e >= q.nk) e -= q.nk;
+  e += e >= q.nk - q.rotk ? q.rotk - q.nk : q.rotk;
   const int big = q.rem * (q.P + 1);  // <= nk
   if (e < big) {
     const int r = e / (q.P + 1);
@@ -145,8 +144,7 @@ ST_HD int n_keys(const Seq& q, int view) { return view == VIEW_SUM ? q.nsum : q.
 ST_HD int query_row(const Geo& g, const Seq& q, int view, int e) {
   if (view == VIEW_NAT) return e;
   if (e >= q.nqv) return e - q.nqv;
-  e += q.rotq;
-  if (e >= q.nqv) e -= q.nqv;
+  e += e >= q.nqv - q.rotq ? q.rotq - q.nqv : q.rotq;
   // Classes start at slope D = P - Po, one more between remo and rem (or one
   // less between rem and remo): three pieces of equal classes.
   const int D = q.P - q.Po;
@@ -219,7 +217,7 @@ ST_HD void live_queries(const Geo& g, const Seq& q, int rule, int k, int& a, int
     case RULE_CAUSAL:
       return;
     case RULE_BAND:
-      b = imin(b - k, g.l + 1) + k;
+      if (b - k > g.l) b = k + g.l + 1;
       return;
     case RULE_BLOCK:
       b = k + imin(b - k, g.l - (k - qdiv(k, g.fl, g.l) * g.l));

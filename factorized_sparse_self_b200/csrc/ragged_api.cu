@@ -13,6 +13,7 @@ namespace {
 constexpr int kPartsLimit = 32;  // most key ranges of one row
 constexpr int kFewRows = 32;     // most query rows per key/value head for the few-row kernel
 constexpr long long kPartsBytes = 256LL << 20;  // most workspace that key ranges may take
+constexpr int64_t kMaxRows = 0x7fff0000;  // most query rows or keys: 32-bit numbers, rounded up to tiles
 
 size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -105,8 +106,8 @@ st_status fill_geo(const st_pattern_desc* p, st_dtype dtype, const st_packed_des
   g.q.head = g.k.head = g.v.head = 1;
   // grids and row numbers are 31-bit
   if ((int64_t)g.total * g.q.tok > 0x7fffffff || (int64_t)g.total * g.k.tok > 0x7fffffff ||
-      (int64_t)g.total * g.v.tok > 0x7fffffff || (int64_t)g.total * g.H > 0x7fff0000 ||
-      (int64_t)g.total * g.G + g.S > 0x7fffffff || g.Hkv > 65535)
+      (int64_t)g.total * g.v.tok > 0x7fffffff || (int64_t)g.total * g.H > kMaxRows ||
+      (int64_t)g.total * g.G + g.S > kMaxRows || g.Hkv > 65535)
     return ST_ERR_UNSUPPORTED;
   return ST_OK;
 }
@@ -121,7 +122,7 @@ st_status fill_cache(const st_cache_desc* c, Geo& g) {
                        (c->page_size - 1) * (c->slot_stride / d) +
                        (g.Hkv - 1) * (c->head_stride / d);
   if (last >= 0x7fffffff || c->page_stride / d > 0x7fffffff ||
-      (int64_t)c->max_pages * c->page_size > 0x7fffffff ||
+      (int64_t)c->max_pages * c->page_size > kMaxRows ||
       (int64_t)g.S * c->max_pages > 0x7fffffff)
     return ST_ERR_UNSUPPORTED;
   g.num_pages = c->num_pages;

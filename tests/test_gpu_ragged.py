@@ -108,6 +108,14 @@ def test_many_units_of_different_lengths(pat, dtype, d):
 
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f16", 128), ("f32", 64)])
+@pytest.mark.parametrize("pat", [(kind, mode, l, c) for kind in ("strided", "fixed") for mode in ("split", "merged")
+                                 for l, c in ((2 ** 31 - 1, 5), (2 ** 31 - 1, 2 ** 31 - 1))], ids=str)
+def test_largest_strides(pat, dtype, d):
+    """One class, window or block holds the whole sequence."""
+    packed(pat, 4, 2, d, dtype, [300, 1, 129], backward=True)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f16", 128), ("f32", 64)])
 @pytest.mark.parametrize("pat", [("strided", "merged", 16, 1), ("strided", "split", 7, 1), ("fixed", "merged", 16, 4), ("fixed", "split", 40, 40),
                                  ("fixed", "split", 20, 3)], ids=str)
 def test_many_key_units(pat, dtype, d):

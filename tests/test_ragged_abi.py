@@ -83,6 +83,16 @@ def test_row_numbers_past_31_bits():
     assert got["paged"] == got["paged_ws"] == st.ST_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("keys", [0x7fff0001, 0x7fffffff])
+def test_key_and_row_numbers_leave_room_for_a_tile(keys):
+    """Tile ends are rounded up in 32 bits."""
+    c = cache(num_pages=1, page_size=keys, max_pages=1, page_stride=0, slot_stride=0)
+    codes = every_call(pattern(), st.ST_BF16, desc(n_seqs=1), c)
+    assert codes["paged"] == codes["paged_ws"] == st.ST_ERR_UNSUPPORTED
+    codes = every_call(pattern(), st.ST_BF16, desc(n_seqs=1, total=keys, H=1, Hkv=1), cache())
+    assert set(codes.values()) == {st.ST_ERR_UNSUPPORTED}
+
+
 def test_null_and_unknown():
     for name, code in every_call(None, st.ST_BF16, desc(), cache()).items():
         assert code == st.ST_ERR_INVALID, name
