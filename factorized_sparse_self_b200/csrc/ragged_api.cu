@@ -118,20 +118,20 @@ st_status fill_cache(const st_cache_desc* c, Geo& g) {
   if (c->page_stride < 0 || c->slot_stride < 0 || c->head_stride < 0 || c->page_stride % d ||
       c->slot_stride % d || c->head_stride % d)
     return ST_ERR_INVALID;
-  const int64_t last = (c->num_pages - 1) * (c->page_stride / d) +
-                       (c->page_size - 1) * (c->slot_stride / d) +
-                       (g.Hkv - 1) * (c->head_stride / d);
-  if (last >= 0x7fffffff || c->page_stride / d > 0x7fffffff ||
-      (int64_t)c->max_pages * c->page_size > kMaxRows ||
-      (int64_t)g.S * c->max_pages > 0x7fffffff)
+  const int64_t page = c->page_stride / d, slot = c->slot_stride / d, head = c->head_stride / d;
+  if (std::max({page, slot, head}) > 0x7fffffff) return ST_ERR_UNSUPPORTED;
+  const int64_t pages = (c->num_pages - 1) * page, slots = (c->page_size - 1) * slot,
+                heads = (g.Hkv - 1) * head;  // below 2^62 each
+  if (std::max({pages, slots, heads}) >= 0x7fffffff || pages + slots + heads >= 0x7fffffff ||
+      (int64_t)c->max_pages * c->page_size > kMaxRows || (int64_t)g.S * c->max_pages > 0x7fffffff)
     return ST_ERR_UNSUPPORTED;
   g.num_pages = c->num_pages;
   g.page_size = c->page_size;
   g.max_pages = c->max_pages;
   g.fpage = make_fastdiv(c->page_size);
-  g.k.tok = (int32_t)(c->slot_stride / d);
-  g.k.head = (int32_t)(c->head_stride / d);
-  g.k.page = (int32_t)(c->page_stride / d);
+  g.k.tok = (int32_t)slot;
+  g.k.head = (int32_t)head;
+  g.k.page = (int32_t)page;
   g.v = g.k;
   return ST_OK;
 }

@@ -93,6 +93,21 @@ def test_key_and_row_numbers_leave_room_for_a_tile(keys):
     assert set(codes.values()) == {st.ST_ERR_UNSUPPORTED}
 
 
+@pytest.mark.parametrize("big", [1 << 62, 1 << 61, (1 << 63) - 64], ids=hex)
+@pytest.mark.parametrize("which", ["page_stride", "slot_stride", "head_stride"])
+def test_cache_strides_past_64_bits(which, big):
+    """Sums of such strides would wrap around to small numbers."""
+    codes = every_call(pattern(), st.ST_BF16, desc(Hkv=4), cache(page_size=129, num_pages=129, **{which: big}))
+    assert codes["paged"] == codes["paged_ws"] == st.ST_ERR_UNSUPPORTED
+
+
+def test_cache_extent_past_64_bits():
+    n = 0x7fff0000
+    codes = every_call(pattern(), st.ST_BF16, desc(Hkv=4, n_seqs=1),
+                       cache(num_pages=n, page_size=n, max_pages=1, page_stride=64 * n, slot_stride=64 * n, head_stride=64 * n))
+    assert codes["paged"] == codes["paged_ws"] == st.ST_ERR_UNSUPPORTED
+
+
 def test_null_and_unknown():
     for name, code in every_call(None, st.ST_BF16, desc(), cache()).items():
         assert code == st.ST_ERR_INVALID, name
