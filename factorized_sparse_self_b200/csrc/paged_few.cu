@@ -1,6 +1,6 @@
 // Attention of a few query rows per key/value head over a paged cache: decoding
-// steps (one new token, the heads of a group as rows) and very short chunks, in
-// bf16 or fp16.
+// steps (one new token, the heads of a group as rows), very short chunks and the
+// chunks of few strided sequences, in bf16 or fp16.
 //
 // Such a call reads every live key and value once and does 4 d flops a row with
 // each, far below the tensor cores' rate at 16 rows, so memory bounds it; what

@@ -11,7 +11,10 @@ using namespace st::rag;
 namespace {
 
 constexpr int kPartsLimit = 32;  // most key ranges of one row
-constexpr int kFewRows = 32;     // most query rows per key/value head for the few-row kernel
+// Most query rows per key/value head for the few-row kernel. Dense, Hkv = 8, d = 128,
+// 64 sequences of 4096 keys, 16, 32, 64 rows: 213, 311, 584 us against the tile
+// kernel's 389, 391, 412.
+constexpr int kFewRows = 32;
 constexpr long long kPartsBytes = 256LL << 20;  // most workspace that key ranges may take
 constexpr int64_t kMaxRows = 0x7fff0000;  // most query rows or keys: 32-bit numbers, rounded up to tiles
 
@@ -183,11 +186,20 @@ FwdPlan plan_fwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype, long lo
   FwdPlan f{};
   const long long sms = sm_count(), keys = most_keys(p);
   const int G = g.split ? (g.G + 1) / 2 : g.G;
-  f.few = paged && dtype != ST_F32 && max_q * G <= kFewRows;
+  // Rows of a short strided chunk lie in many classes, so 256 of them meet most of
+  // the context, one tile after the other: 16 rows a unit are better until such
+  // units fill a quarter of the GPU. Merged, l = 128, Hkv = 8, d = 128, one sequence of
+  // 16 K keys, 128, 256, 512 rows: 27, 39, 55 us against the tile kernel's 117, 207,
+  // 207; four of 8 K keys, 256 rows: 70 against 127; 32 of 4 K keys, 32, 64 rows: 57,
+  // 102 against 64, 78.
+  auto units = [&](int rows, long long tokens) { return (tokens * G + rows - 1) / rows * g.Hkv; };
+  f.few = paged && dtype != ST_F32 &&
+          (max_q * G <= kFewRows ||
+           (p.kind == ST_STRIDED && 4 * std::max(units(256, max_q), units(256, g.total)) < sms));
   const int rows = f.few ? 16 : dtype == ST_F32 ? 64 : 256;
   const int key_tile = f.few ? 16 : dtype == ST_F32 ? 64 : 128;
-  const long long longest = std::max(1LL, (max_q * G + rows - 1) / rows * g.Hkv);
-  const long long all = std::max(longest, ((long long)g.total * G + rows - 1) / rows * g.Hkv);
+  const long long longest = std::max(1LL, units(rows, max_q));
+  const long long all = std::max(longest, units(rows, g.total));
   const size_t qrows = (size_t)g.total * g.H;
   const long long fit = std::max(1LL, kPartsBytes / (long long)std::max<size_t>(1, qrows * g.d * sizeof(float)));
   if (f.few) {

@@ -352,6 +352,15 @@ def test_paged_lengths_are_hints():
         paged(("strided", "merged", 16, 1), 8, 2, 64, "f16", [900, 300], [1, 1], 16, max_q=mq, max_kv=mk)
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f16", 128), ("f32", 64)])
+@pytest.mark.parametrize("pat", [p for p in PATTERNS if p[0] == "strided"], ids=lambda p: "-".join(map(str, p)))
+def test_paged_strided_chunks_of_few_and_many_rows(pat, dtype, d):
+    """The expected chunk chooses the kernel: rows of a few queries, or tiles of 256 rows."""
+    for mq in (1, 100000):
+        paged(pat, 6, 3, d, dtype, [1300, 90, 0, 700], [300, 100, 2, 129], 24, seed=mq, max_q=mq)
+        paged(pat, 5, 1, d, dtype, [650], [600], 64, layout="hnd", seed=mq + 1, max_q=mq)
+
+
 @pytest.mark.parametrize("pat", [("dense", "merged", 1, 1), ("strided", "merged", 12, 1), ("fixed", "split", 16, 3)], ids=str)
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_prompt_then_decode_agrees_with_the_whole_prompt(pat, dtype):
