@@ -631,6 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint16_t* out = static_cast<uint16_t*>(a.dq) + ((size_t)qr.t * a.dq_rows.tok + qr.h * a.dq_rows.head) * D;
         const bool wide = (reinterpret_cast<uintptr_t>(a.dq) & 31) == 0;
         auto load = [&](float* o, uint32_t col) {
+          __syncwarp();  // rows past the unit's end left the last turn early
           if (t1 > t0) {
             tmem_ld32(tmem + tl + col, reinterpret_cast<uint32_t*>(o));
             tmem_wait_ld();
@@ -708,6 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
+          __syncwarp();  // keys past the unit's end left the last turn early
           if (t1 > t0) {
             tmem_ld32(tmem + tl + (w ? kDV : kDK) + c, reinterpret_cast<uint32_t*>(o));
             tmem_wait_ld();

@@ -468,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
+        __syncwarp();  // rows past the unit's end left the last turn early
         if (any) {
           tmem_ld32(tO + c, reinterpret_cast<uint32_t*>(o));
           tmem_wait_ld();
