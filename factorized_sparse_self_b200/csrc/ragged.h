@@ -42,6 +42,7 @@ struct FwdLaunch {
   int32_t part0, part1;  // first part of each job
   int32_t nsplit;  // OUT_PARTIAL: most key ranges of a unit
   int32_t least;   // fewest key tiles of a range
+  int32_t taper;   // ranges get shorter, and short ones go last
   int32_t mode;    // OutMode
   float scale_log2;
   uint64_t wait_ns;

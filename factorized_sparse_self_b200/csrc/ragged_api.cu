@@ -159,6 +159,7 @@ struct FwdPlan {
   int nsplit;   // most key ranges per unit and job
   int least;    // fewest key tiles (of the kernel) of a range
   int nparts;   // parts of a row (0: rows are written directly)
+  bool taper;   // ranges get shorter, and short ones go last
   bool merge;   // the second order joins the first's part itself
   size_t parts_o, bytes;
 };
@@ -179,9 +180,15 @@ int clamp_int(long long x, long long lo, long long hi) {
 // Key ranges (the kernels cut short units into fewer). Units go to free SMs one
 // by one, so only few units leave SMs idle: those of one longest sequence (the
 // others may be short) have to be worth the GPU. A prompt's units see 1 .. T
-// keys, the longest ones first; a chunk's see all of the context, so they should
-// come in twos per SM. Dense, H = 32, Hkv = 8, d = 128, chunks of 512 tokens behind
-// 32 K, 8 K, 4 K keys: 440, 444, 465 us with 2, 3, 4 per SM.
+// keys, the longest ones first; a chunk's see all of the context, so they come in
+// twos per SM, fewer where other sequences bring units too, and taper: the first
+// range of every unit, the longest, goes first, the short ones fill the end. Dense, H =
+// 32, Hkv = 8, d = 128, us:
+//                                              tapered  ranges of one length
+//   2, 3, 4 per SM: chunks of 512 behind 32 K, 8 K, 4 K keys   395, 400, 426   444, 451, 476
+//   128 tokens behind 64 K keys                158, 176, 180   211, 211, 206
+//   256 behind 16 K, four times                389, 419, 436   406, 440, 451
+//   (that one by this rule, 6 ranges: 350)
 FwdPlan plan_fwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype, long long max_q, bool paged) {
   FwdPlan f{};
   const long long sms = sm_count(), keys = most_keys(p);
@@ -210,11 +217,15 @@ FwdPlan plan_fwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype, long lo
   } else {
     f.least = 512 / key_tile;
     long long n = 1;
-    if (all < 4 * sms) n = paged ? (2 * sms + longest - 1) / longest : (sms + longest - 1) / longest;
+    if (all < 4 * sms) {
+      n = ((paged ? 2 : 1) * sms + longest - 1) / longest;
+      if (paged) n = std::min(n, std::max(4LL, 6 * sms / all));
+    }
     f.nsplit = clamp_int(std::min(n, keys / 512), 1, std::min<long long>(fit, kPartsLimit));
     // ranges of one length: shorter sequences are cut into fewer
     f.least = (int)std::max<long long>(f.least, (keys + key_tile - 1) / key_tile / f.nsplit);
   }
+  f.taper = paged && !f.few && longest * f.nsplit > sms;
   const bool two = two_orders(p);
   f.merge = two && f.nsplit == 1 && !f.few;
   f.nparts = f.merge ? 1 : two ? 2 * f.nsplit : f.nsplit > 1 ? f.nsplit : 0;
@@ -241,6 +252,7 @@ st_status run_fwd(const st_pattern_desc& p, st_dtype dtype, Geo& g, float scale,
   a.parts.lse = reinterpret_cast<float*>(static_cast<char*>(ws) + f.parts_o);
   a.nsplit = f.nsplit;
   a.least = f.least;
+  a.taper = f.taper;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)g.d)) * 1.4426950408889634f;
   a.wait_ns = wait_limit_ns();
   a.stream = stream;

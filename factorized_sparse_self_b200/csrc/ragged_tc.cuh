@@ -333,8 +333,9 @@ __device__ __forceinline__ bool decode_unit(const FwdLaunch& a, int slots, int n
   const Geo& g = a.g;
   const int nsplit = a.nsplit, least = a.least;
   const int lane = threadIdx.x & 31;
-  const int part = n % nsplit;
-  int m = n / nsplit;
+  const int per = slots * g.Hkv * a.njobs;
+  const int part = a.taper ? n / per : n % nsplit;
+  int m = a.taper ? n - part * per : n / nsplit;
   const int jb = m % a.njobs;
   m /= a.njobs;
   const Job& job = jb ? a.job1 : a.job;
@@ -361,6 +362,11 @@ __device__ __forceinline__ bool decode_unit(const FwdLaunch& a, int slots, int n
   const int total = __shfl_sync(0xffffffffu, cnt, 0) + __shfl_sync(0xffffffffu, cnt, 1);
   const int parts = parts_of(total, nsplit, least);
   if (part >= parts) return false;
+  // tapered: the rest shrinks with the square of the parts that are left
+  auto cut = [&](int p) {
+    const long long P = parts, left = parts - p;
+    return a.taper ? (int)(total - total * (left * left) / (P * P)) : (int)(total * (long long)p / P);
+  };
   if (lane < 4) {
     out->ja[w][sg] = j0;
     out->jb[w][sg] = j1;
@@ -375,8 +381,8 @@ __device__ __forceinline__ bool decode_unit(const FwdLaunch& a, int slots, int n
       out->part = part;
       out->cnt0 = cnt;
       out->parts = parts;
-      out->t0 = (int)((long long)total * part / parts);
-      out->t1 = (int)((long long)total * (part + 1) / parts);
+      out->t0 = cut(part);
+      out->t1 = cut(part + 1);
     }
   }
   __syncwarp();

@@ -345,6 +345,13 @@ def test_paged_long_contexts(dtype, d):
     paged(("fixed", "split", 64, 8), 2, 1, d, dtype, [4097, 4096], [1, 300], 20)
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f16", 128)])
+@pytest.mark.parametrize("pat", [("dense", "merged", 1, 1), ("fixed", "merged", 700, 600), ("strided", "split", 4000, 1)], ids=str)
+def test_paged_chunks_in_ranges_of_different_lengths(pat, dtype, d):
+    """More key ranges than SMs: long ones first, a short sequence in fewer of them, one with a single row."""
+    paged(pat, 32, 8, d, dtype, [5100, 1300, 4000, 40], [300, 70, 1, 33], 16, layout="hnd")
+
+
 def test_paged_lengths_are_hints():
     """max_q and max_kv steer the split only."""
     for mq, mk in ((1, 1), (5000, 100000), (1, 100000)):
