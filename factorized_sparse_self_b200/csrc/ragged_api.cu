@@ -297,11 +297,10 @@ struct BwdPlan {
 BwdPlan plan_bwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype) {
   BwdPlan b{};
   // Units of at most two key tiles are where rows have few keys. With two orders
-  // the sums of both are needed: all units, if the band is short. d = 128 pays for it
-  // (dense step 965 -> 1003 us) and mends patterns of few keys only.
+  // the sums of both are needed: all units, if the band is short.
   if (dtype != ST_F32) {
     if (two_orders(p)) b.mend_tiles = p.l < 128 ? 0x7fffffff : 0;
-    else b.mend_tiles = g.d == 64 || most_keys(p) <= 2048 ? 2 : 0;
+    else b.mend_tiles = 2;
   }
   Job jobs[2];
   const int n = make_jobs(p, jobs);

@@ -18,7 +18,7 @@
 // hands D + r to the key-major kernel, which therefore runs after it. (Errors of dQ
 // and dK over that of rounding the result: strided, l = 100, split, fp16 1.72 -> 1.42;
 // fixed, l = 20, bf16 1.68 -> 1.42; dense, 2000 tokens 1.51 -> 1.41.) At d = 128 the sum
-// takes the second S's place in TMEM: long dense sequences go without.
+// takes the second S's place in TMEM for those units (dQ of a dense step 264 -> 272 us).
 //
 // One CTA per SM (384 threads), units claimed from the grid. Warps 0..7 are two
 // warpgroups that share the 128 rows and take 64 columns each of a 128 x 128
@@ -29,8 +29,8 @@
 // TMEM: S, dP (key-major: transposed), 128 columns each, then the accumulators, d
 // columns each: dQ and P K, or dV and dK. P and dS both go over dP, so S is free as
 // soon as it is in registers and the next tile's is formed under this one's
-// exponentials. Query-major, d = 64 or without P K, there is room for two S: P and dS go over S, and
-// the next dP is formed before the tile's products, not behind them (backward of 12288
+// exponentials. Query-major there is room for two S (not at d = 128 where units of any
+// length mend): P and dS go over S, and the next dP is formed before the tile's products, not behind them (backward of 12288
 // rasters, l = 192, split: 223 against 241 us).
 #include "ragged_tc.cuh"
 
@@ -76,7 +76,7 @@ struct alignas(1024) Smem {
                                        // (mend: ndel holds the two halves of r)
   uint64_t r_full[Cfg<D>::kRes], r_empty[Cfg<D>::kRes];
   uint64_t full[Cfg<D>::kA + Cfg<D>::kB], empty[Cfg<D>::kA + Cfg<D>::kB];
-  uint64_t s_full[2], s_free, dp_full, ds_ready, acc_full, r_sum;
+  uint64_t s_full[2], s_free, dp_full, ds_ready, acc_full, r_sum, kb_read;
   uint64_t row_full[2], row_empty[2];
   uint64_t sched_full[kSched], sched_empty[kSched];
   uint64_t fin;
@@ -156,17 +156,20 @@ __device__ __forceinline__ bool decode(const BwdLaunch& a, int slots, int n, BUn
   return true;
 }
 
-// MEND (query-major): units of few key tiles mend D.
-template <int D, bool F16, bool DKV, bool MEND>
+// MEND (query-major): some units (those of few key tiles) mend D; ALL: any unit may
+// (d = 128: tensor memory then has no room for a second S).
+template <int D, bool F16, bool DKV, bool MEND, bool ALL>
 __global__ void __launch_bounds__(kThreads, 1)
     ragged_bwd_tc(const __grid_constant__ BwdLaunch a, const __grid_constant__ TileMaps maps, int slots) {
   extern __shared__ __align__(1024) uint8_t raw[];
   Smem<D>& S = *reinterpret_cast<Smem<D>*>(raw);
   constexpr int NA = Cfg<D>::kA, NB = Cfg<D>::kB, NS = NA + NB, TB = Cfg<D>::kTileBytes,
                 NR = Cfg<D>::kRes;
-  constexpr bool TWO_S = !DKV && (D == 64 || !MEND);
+  constexpr bool TWO_S = !DKV && (D == 64 || !ALL);
+  // d = 128: a unit that mends has one S, its sums P K take the place of the other
+  constexpr bool SHARE = MEND && TWO_S && D == 128;
   constexpr uint32_t kDP = TWO_S ? 256 : 128, kAcc = kDP + 128;
-  constexpr uint32_t kDQ = kAcc, kKB = kAcc + D, kDV = kAcc, kDK = kAcc + D;
+  constexpr uint32_t kDQ = kAcc, kKB = SHARE ? 128 : kAcc + D, kDV = kAcc, kDK = kAcc + D;
   const Geo& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t limit = a.wait_ns;
@@ -196,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&S.ds_ready, 256);
     mbar_init(&S.acc_full, 1);
     mbar_init(&S.r_sum, 256);
+    mbar_init(&S.kb_read, 256);
     for (int i = 0; i < kSched; ++i) {
       mbar_init(&S.sched_full[i], 1);
       mbar_init(&S.sched_empty[i], 11);  // two producers, MMA, eight compute warps
@@ -397,6 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t bk = sdesc(smem_u32(S.ring[0]), 16, 1024), bm = sdesc(smem_u32(S.ring[0]), 16384, 1024);
       int used = 0;     // units with tiles
       uint32_t ts = 0;  // tiles so far
+      uint32_t shared = 0;  // SHARE: units that mended so far
+      bool kept = false;    // and whether the last unit is one
       // ring slots of tile t (counted from the first): its first operand, its second
       auto slot_a = [&](uint32_t t) { return (int)(t % NA); };
       auto slot_b = [&](uint32_t t) { return NA + (int)(t % NB); };
@@ -448,39 +454,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++used;
           const bool mend = MEND && u.mend;
           // S of tile ts + i of the unit's T; its buffer, P and dS columns
-          auto buf = [&](uint32_t t) { return TWO_S ? (t & 1) : 0u; };
-          auto next_s = [&](uint32_t t) {
+          const uint32_t tb = ts;
+          auto buf = [&](uint32_t t) { return TWO_S ? (t - tb) & 1 : 0u; };
+          auto next_s = [&](uint32_t t, uint32_t b) {
             wait_a(t);
             if (!TWO_S && t != ts) wait(&S.s_free, (t - 1) & 1);
-            scores(a1, slot_a(t), buf(t) * 128, &S.s_full[buf(t)]);
+            scores(a1, slot_a(t), b * 128, &S.s_full[b]);
           };
           auto next_dp = [&](uint32_t t) {
             scores(a2, slot_b(t), kDP, &S.dp_full);
             if (!DKV) commit(&S.empty[slot_b(t)]);
           };
-          next_s(ts);
+          next_s(ts, 0);
           wait_b(ts);
           next_dp(ts);
-          if (TWO_S && T > 1) next_s(ts + 1);
           if (T == 1) commit(&S.r_empty[rb]);
-          for (int t = 0; t < T; ++t, ++ts) {
-            const bool more = t + 1 < T;
-            if (!TWO_S && more) next_s(ts + 1);  // under this tile's exponentials
-            if (more) wait_b(ts + 1);
-            wait(&S.ds_ready, ts & 1);
-            uint64_t* full = more ? nullptr : &S.acc_full;
-            const uint32_t cp = TWO_S ? buf(ts) * 128 : kDP;
-            if (TWO_S && more) next_dp(ts + 1);
-            if constexpr (DKV) {
-              weigh(cp, slot_b(ts), kDV, t == 0, true, nullptr);
-              weigh(cp + 32, slot_a(ts), kDK, t == 0, true, full);
-            } else {
-              if (mend) weigh(cp, slot_a(ts), kKB, t == 0, false, nullptr);
-              weigh(cp + 32, slot_a(ts), kDQ, t == 0, true, full);
+          if (SHARE && kept) wait(&S.kb_read, (shared - 1) & 1);  // the second S's place is free again
+          if (SHARE && mend) {
+            ++shared;
+            kept = true;
+            for (int t = 0; t < T; ++t, ++ts) {
+              const bool more = t + 1 < T;
+              if (more) wait_b(ts + 1);
+              wait(&S.ds_ready, ts & 1);
+              if (more) next_dp(ts + 1);
+              weigh(0, slot_a(ts), kKB, t == 0, false, nullptr);
+              weigh(32, slot_a(ts), kDQ, t == 0, true, more ? nullptr : &S.acc_full);
+              if (more) next_s(ts + 1, 0);
+              if (t + 2 == T) commit(&S.r_empty[rb]);
             }
-            if (!TWO_S && more) next_dp(ts + 1);
-            if (t + 2 == T) commit(&S.r_empty[rb]);
-            if (TWO_S && t + 2 < T) next_s(ts + 2);
+          } else {
+            kept = false;
+            if (TWO_S && T > 1) next_s(ts + 1, 1);
+            for (int t = 0; t < T; ++t, ++ts) {
+              const bool more = t + 1 < T;
+              if (!TWO_S && more) next_s(ts + 1, 0);  // under this tile's exponentials
+              if (more) wait_b(ts + 1);
+              wait(&S.ds_ready, ts & 1);
+              uint64_t* full = more ? nullptr : &S.acc_full;
+              const uint32_t cp = TWO_S ? buf(ts) * 128 : kDP;
+              if (TWO_S && more) next_dp(ts + 1);
+              if constexpr (DKV) {
+                weigh(cp, slot_b(ts), kDV, t == 0, true, nullptr);
+                weigh(cp + 32, slot_a(ts), kDK, t == 0, true, full);
+              } else {
+                if (!SHARE && mend) weigh(cp, slot_a(ts), kKB, t == 0, false, nullptr);
+                weigh(cp + 32, slot_a(ts), kDQ, t == 0, true, full);
+              }
+              if (!TWO_S && more) next_dp(ts + 1);
+              if (t + 2 == T) commit(&S.r_empty[rb]);
+              if (TWO_S && t + 2 < T) next_s(ts + 2, buf(ts));
+            }
           }
         }
         if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
@@ -500,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sc2 = a.scale * kLog2e;
     bool ok = true;
     uint32_t ts = 0, us = 0, rs = 0;  // tiles, units with tiles, mended units so far
+    uint32_t sp = 0;                  // bit b: parity of S buffer b
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       ok = __all_sync(0xffffffffu, bar_wait(bar, parity, limit, abort));
       return ok;
@@ -538,10 +563,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int tsplit = DKV ? t1 : u.cnt0;
       for (int t = t0; t < t1; ++t, ++ts) {
-        const int buf = TWO_S ? (int)(ts & 1) : 0;
+        const int buf = TWO_S && !(SHARE && mend) ? (t - t0) & 1 : 0;
         const uint32_t tS = tmem + tl + buf * 128 + w * 64, tDP = tmem + tl + kDP + w * 64;
         const uint32_t tP = TWO_S ? tS : tDP;  // where P and dS go
-        if (!wait(&S.s_full[buf], (TWO_S ? ts >> 1 : ts) & 1)) break;
+        if (!wait(&S.s_full[buf], (sp >> buf) & 1)) break;
+        sp ^= 1u << buf;
         tc_fence_after();
         float p[64];
         tmem_ld32(tS, reinterpret_cast<uint32_t*>(p));
@@ -598,7 +624,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               float* y = p + c * 32 + x;
               fadd2(dp[x], dp[x + 1], dp[x], dp[x + 1], nd, nd);
               fmul2(y[0], y[1], y[0], y[1], dp[x], dp[x + 1]);
-              if constexpr (MEND) fadd2(r0, r1, r0, r1, y[0], y[1]);
+            }
+            if (mend) {
+#pragma unroll
+              for (int x = 0; x < 32; x += 2) fadd2(r0, r1, r0, r1, p[c * 32 + x], p[c * 32 + x + 1]);
             }
           }
 #pragma unroll
@@ -673,6 +702,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 32; ++x) o[x] = fmaf(-r, kb[x], o[x]);
             store_row16<F16>(out + c, o, wide);
           }
+          if (SHARE && t1 > t0) {
+            tc_fence_before();
+            mbar_arrive(&S.kb_read);
+          }
         } else {
 #pragma unroll 1
           for (int c = w * (D / 2); c < (w + 1) * (D / 2); c += 32) {
@@ -731,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool F16, bool DKV, bool MEND>
+template <int D, bool F16, bool DKV, bool MEND, bool ALL>
 cudaError_t launch(const BwdLaunch& a) {
   const Geo& g = a.g;
   TileMaps m = {};
@@ -741,13 +774,13 @@ cudaError_t launch(const BwdLaunch& a) {
     return cudaErrorInvalidValue;
   const size_t smem = sizeof(Smem<D>);
   static_assert(sizeof(Smem<D>) <= 232448, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(ragged_bwd_tc<D, F16, DKV, MEND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(ragged_bwd_tc<D, F16, DKV, MEND, ALL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
   const long long slots = slot_count(g, DKV ? 1 : most_heads(g, a.qjob[0].hc), 128);
   const long long units = slots * g.Hkv * (DKV ? a.njobs * a.nsplit : a.nqjobs);
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
-  ragged_bwd_tc<D, F16, DKV, MEND><<<(unsigned)units, kThreads, smem, a.stream>>>(a, m, (int)slots);
+  ragged_bwd_tc<D, F16, DKV, MEND, ALL><<<(unsigned)units, kThreads, smem, a.stream>>>(a, m, (int)slots);
   return cudaGetLastError();
 }
 
@@ -755,14 +788,14 @@ cudaError_t launch(const BwdLaunch& a) {
 
 cudaError_t tc_ragged_dq(const BwdLaunch& a, int dtype) {
   const bool h = dtype == ST_F16;
-  if (a.g.d == 64) return h ? launch<64, true, false, true>(a) : launch<64, false, false, true>(a);
-  if (a.mend_tiles) return h ? launch<128, true, false, true>(a) : launch<128, false, false, true>(a);
-  return h ? launch<128, true, false, false>(a) : launch<128, false, false, false>(a);
+  if (a.g.d == 64) return h ? launch<64, true, false, true, false>(a) : launch<64, false, false, true, false>(a);
+  if (a.mend_tiles > 2) return h ? launch<128, true, false, true, true>(a) : launch<128, false, false, true, true>(a);
+  return h ? launch<128, true, false, true, false>(a) : launch<128, false, false, true, false>(a);
 }
 cudaError_t tc_ragged_dkv(const BwdLaunch& a, int dtype) {
   const bool h = dtype == ST_F16;
-  if (a.g.d == 64) return h ? launch<64, true, true, false>(a) : launch<64, false, true, false>(a);
-  return h ? launch<128, true, true, false>(a) : launch<128, false, true, false>(a);
+  if (a.g.d == 64) return h ? launch<64, true, true, false, false>(a) : launch<64, false, true, false, false>(a);
+  return h ? launch<128, true, true, false, false>(a) : launch<128, false, true, false, false>(a);
 }
 
 }  // namespace rag

@@ -124,6 +124,32 @@ def test_many_key_units(pat, dtype, d):
     packed(pat, 64, 32, d, dtype, [200] * 7, backward=True, fused=True, lead=3)
 
 
+@pytest.mark.parametrize("pat,H,Hkv,d,dtype,lens", [
+    (("dense", "merged", 1, 1), 20, 4, 128, "bf16", [2518, 78, 177]), (("dense", "merged", 1, 1), 4, 2, 64, "bf16", [2000]),
+    (("strided", "split", 100, 1), 16, 8, 128, "f16", [79, 1159, 19, 52, 10]), (("fixed", "split", 20, 9), 10, 2, 128, "bf16", [3, 2276, 57]),
+    (("strided", "merged", 10, 1), 10, 2, 128, "bf16", [7, 48, 16, 3, 1668, 459])], ids=str)
+def test_gradients_lose_no_more_than_their_roundings(pat, H, Hkv, d, dtype, lens):
+    """dQ and dK are sums of products with dS rounded to 16 bits, then rounded themselves: two independent errors of one
+    size, the square root of 2 together. What D loses to the rounding of o would come on top; 6 % is left for it."""
+    dt = DT[dtype]
+    g = torch.Generator(device="cuda").manual_seed(12)
+    n, at = sum(lens), [0]
+    q, k, v, dout = (randn(g, n, h, d, dtype=dt) for h in (H, Hkv, Hkv, H))
+    P, cu = st.st_pattern(*pat), starts(lens)
+    o, lse = st.st_packed_attn_fwd(P, q, k, v, cu, max(lens))
+    got = st.st_packed_attn_bwd(P, q, k, v, o, lse, dout, cu, max(lens))
+    want = [[], [], []]
+    for m in lens:
+        a, b = at[-1], at[-1] + m
+        at.append(b)
+        for x, (ref, _) in zip(want, One(pat, q[a:b], k[a:b], v[a:b], dt).backward(dout[a:b])):
+            x.append(ref)
+    for name, x, ref in zip(("dq", "dk", "dv"), got, want):
+        ref = torch.cat(ref)
+        lost, rounding = (float((y.double() - ref).norm()) for y in (x, ref.to(dt)))
+        assert lost <= 1.5 * rounding, (name, lost / rounding)
+
+
 def test_two_calls_at_once():
     """Two streams, a workspace each, started together and repeated: each keeps its results."""
     P = st.st_pattern("strided", "merged", 24)
