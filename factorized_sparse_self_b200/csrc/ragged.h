@@ -65,7 +65,8 @@ struct BwdLaunch {
   Rows dq_rows, dk_rows, dv_rows;  // of the gradients
   float* parts;      // dK, dV parts
   float* dq_part;    // fp32 dQ [total][H][d] of the first query order
-  int32_t mend_tiles;  // 16-bit: key tiles up to which a unit's rows have their delta mended
+  int32_t mend_tiles;  // 16-bit: key tiles up to which a unit's rows have their delta mended,
+  int32_t mend_below;  // if all are at positions below this
   float *kb_part, *r_part;  // of the first query order: sums P K, lost part of delta
   int32_t nsplit;
   float scale;

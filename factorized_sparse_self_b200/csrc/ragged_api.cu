@@ -290,17 +290,18 @@ struct BwdPlan {
   int njobs, nsplit;
   bool parts;  // dK, dV are joined from parts
   bool merge;  // the second launch adds the first one's part itself
-  int mend_tiles;
+  int mend_tiles, mend_below;
   size_t delta, dq_part, parts_bytes, bytes;
 };
 
 BwdPlan plan_bwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype) {
   BwdPlan b{};
   // Units of at most two key tiles are where rows have few keys. With two orders
-  // the sums of both are needed: all units, if the band is short.
+  // the sums of both are needed: all units, if the band is short; else rows have few
+  // keys only where the second order has none for them, below position 2 l.
   if (dtype != ST_F32) {
-    if (two_orders(p)) b.mend_tiles = p.l < 128 ? 0x7fffffff : 0;
-    else b.mend_tiles = 2;
+    b.mend_tiles = two_orders(p) && p.l < 128 ? 0x7fffffff : 2;
+    b.mend_below = two_orders(p) && p.l >= 128 && p.l < 0x40000000 ? 2 * p.l : 0x7fffffff;
   }
   Job jobs[2];
   const int n = make_jobs(p, jobs);
@@ -330,7 +331,7 @@ BwdPlan plan_bwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype) {
   const int nparts = b.merge ? 1 : b.parts ? b.njobs * b.nsplit : 0;
   b.parts_bytes = round256(krows * 2 * g.d * sizeof(float) * nparts);
   b.bytes = b.delta + b.dq_part + b.parts_bytes;
-  if (b.dq_part && b.mend_tiles) b.bytes += b.delta + b.dq_part;
+  if (b.dq_part && b.mend_tiles > 2) b.bytes += b.delta + b.dq_part;
   return b;
 }
 
@@ -423,6 +424,7 @@ st_status st_packed_attn_bwd(const st_pattern_desc* p, st_dtype dtype, const st_
   a.parts = reinterpret_cast<float*>(w);
   w += b.parts_bytes;
   a.mend_tiles = b.mend_tiles;
+  a.mend_below = b.mend_below;
   a.r_part = reinterpret_cast<float*>(w);
   a.kb_part = reinterpret_cast<float*>(w + b.delta);
   a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)g.d);
@@ -437,6 +439,7 @@ st_status st_packed_attn_bwd(const st_pattern_desc* p, st_dtype dtype, const st_
     for (int j = 0; j < n && e == cudaSuccess; ++j) {
       a.qjob[0] = jobs[j];
       a.mode = j == 0 ? OUT_PARTIAL : OUT_MERGE;
+      if (j == 1 && a.mend_tiles == 2) a.mend_tiles = 0;  // the first order has mended
       e = go_dq();
     }
   } else if (e == cudaSuccess) {

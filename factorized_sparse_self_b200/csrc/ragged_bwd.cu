@@ -150,7 +150,9 @@ __device__ __forceinline__ bool decode(const BwdLaunch& a, int slots, int n, BUn
     out->cnt0 = cnt0;
     out->u0[0] = u0[0];
     out->u0[1] = u0[1];
-    out->mend = a.mend_tiles > 0 && t1 - t0 <= a.mend_tiles;
+    // (positions by the natural order; a limit is set for no other)
+    out->mend = !DKV && a.mend_tiles > 0 && t1 - t0 <= a.mend_tiles &&
+                fdiv(imin(r0 + 128, q.nq * hs.n) - 1, hs.f) < a.mend_below;
   }
   __syncwarp();
   return true;
@@ -678,8 +680,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             r = S.ndel[0][row] + S.ndel[1][row];
           }
           if (have && a.mode == OUT_MERGE) r += a.r_part[rr];
+          // the first of two orders: either every unit leaves its sums to the second, or
+          // units of rows that only this order reaches mend by themselves
+          const bool leave = a.mode == OUT_PARTIAL && a.mend_tiles > 2;
           if (have && w == 0) {
-            if (a.mode == OUT_PARTIAL) a.r_part[rr] = r;
+            if (leave) a.r_part[rr] = r;
             else a.delta[rr] = r - nd;  // for the key-major kernel; this unit has read its rows
           }
 #pragma unroll 1
@@ -689,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             load(kb, kKB + c);
             if (!have) continue;
             const size_t at = rr * D + c;
-            if (a.mode == OUT_PARTIAL) {
+            if (leave) {
               store_row32(a.dq_part + at, o);
               store_row32(a.kb_part + at, kb);
               continue;
@@ -700,7 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int x = 0; x < 32; ++x) o[x] = fmaf(-r, kb[x], o[x]);
-            store_row16<F16>(out + c, o, wide);
+            if (a.mode == OUT_PARTIAL) store_row32(a.dq_part + at, o);
+            else store_row16<F16>(out + c, o, wide);
           }
           if (SHARE && t1 > t0) {
             tc_fence_before();

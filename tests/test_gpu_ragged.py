@@ -127,7 +127,8 @@ def test_many_key_units(pat, dtype, d):
 @pytest.mark.parametrize("pat,H,Hkv,d,dtype,lens", [
     (("dense", "merged", 1, 1), 20, 4, 128, "bf16", [2518, 78, 177]), (("dense", "merged", 1, 1), 4, 2, 64, "bf16", [2000]),
     (("strided", "split", 100, 1), 16, 8, 128, "f16", [79, 1159, 19, 52, 10]), (("fixed", "split", 20, 9), 10, 2, 128, "bf16", [3, 2276, 57]),
-    (("strided", "merged", 10, 1), 10, 2, 128, "bf16", [7, 48, 16, 3, 1668, 459])], ids=str)
+    (("strided", "merged", 10, 1), 10, 2, 128, "bf16", [7, 48, 16, 3, 1668, 459]), (("strided", "merged", 174, 1), 32, 8, 128, "bf16", [80, 86]),
+    (("strided", "merged", 130, 1), 8, 2, 64, "f16", [1000, 300, 20])], ids=str)
 def test_gradients_lose_no_more_than_their_roundings(pat, H, Hkv, d, dtype, lens):
     """dQ and dK are sums of products with dS rounded to 16 bits, then rounded themselves: two independent errors of one
     size, the square root of 2 together. What D loses to the rounding of o would come on top; 6 % is left for it."""
