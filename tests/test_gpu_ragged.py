@@ -151,6 +151,36 @@ def test_gradients_lose_no_more_than_their_roundings(pat, H, Hkv, d, dtype, lens
         assert lost <= 1.5 * rounding, (name, lost / rounding)
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f16", 128), ("f32", 32)])
+@pytest.mark.parametrize("pat", [("dense", "merged", 1, 1), ("strided", "merged", 3, 1), ("fixed", "merged", 4, 2)], ids=str)
+def test_thousands_of_sequences_of_one_token(pat, dtype, d):
+    """One key each: O is its value row, dV the sum of dO over the group, dQ and dK are zero but for roundings."""
+    dt, H, Hkv, n = DT[dtype], 6, 2, 3001
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q, k, v, dout = (randn(g, n, h, d, dtype=dt) for h in (H, Hkv, Hkv, H))
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda").repeat_interleave(2)  # an empty one behind each
+    P = st.st_pattern(*pat)
+    o, lse = st.st_packed_attn_fwd(P, q, k, v, cu, 1)
+    dq, dk, dv = st.st_packed_attn_bwd(P, q, k, v, o, lse, dout, cu, 1)
+    assert st.st_last_device_status() == st.ST_OK
+    rep = lambda x: x.double().repeat_interleave(H // Hkv, 1)
+    e, eps = torch.finfo(dt).eps / 2, 2.0 ** -24
+    s = (q.double() * rep(k)).sum(2) * d ** -0.5
+    size = (q.double() * rep(k)).abs().sum(2) * d ** -0.5
+    # P = exp(s - LSE): the sums of d products and the logarithm's fp32 roundings, and the approximate exp2's
+    off = (d + 16) * eps * (size + 1) + 2.0 ** -20
+    assert bool(((lse.double() - s).abs() <= off).all())
+    assert bool(((o.double() - rep(v)).abs() <= (2 * e + off[..., None]) * rep(v).abs()).all())
+    gd = dout.double().view(n, Hkv, H // Hkv, d)
+    tol = (2 * e + off.view(n, Hkv, -1).amax(2)[..., None]) * gd.abs().sum(2) + e * gd.abs().sum(2)
+    assert bool(((dv.double() - gd.sum(2)).abs() <= tol).all())
+    # dS = P (dP - D): what o lost to its rounding, at most, where D is not mended
+    ds = (2 * e + 2 * off) * (dout.double() * rep(v)).abs().sum(2) + (d + 16) * eps * (dout.double() * rep(v)).abs().sum(2)
+    assert bool((dq.double().abs() <= (ds * d ** -0.5)[..., None] * rep(k).abs() * (1 + 4 * e) + 2.0 ** -24).all())
+    lim = ((ds * d ** -0.5)[..., None] * q.double().abs()).view(n, Hkv, -1, d).sum(2) * (1 + 4 * e) + 2.0 ** -24
+    assert bool((dk.double().abs() <= lim).all())
+
+
 def test_two_calls_at_once():
     """Two streams, a workspace each, started together and repeated: each keeps its results."""
     P = st.st_pattern("strided", "merged", 24)
