@@ -264,9 +264,17 @@ ST_HD int most_heads(const Geo& g, int hc) { return hc >= 0 ? (g.G + 1) / 2 : g.
 
 // Unit slots: sequence s owns the slots from floor(cu[s] * mult / BM) + s up to
 // the next sequence's first, at least ceil(n_s * mult / BM) of them, so a slot's
-// sequence is found by bisection of cu and no table of units is built.
+// sequence is found by bisection of cu and no table of units is built. Slots below
+// the first sequence's (its rows need not start at 0) belong to no sequence: their
+// tile lies past every sequence's rows.
 ST_HD long long slot_count(const Geo& g, int mult, int BM) {
   return (long long)g.total * mult / BM + g.S;
+}
+ST_HD int slot_first(int cu_s, int s, int mult, int BM) {
+  return (int)((long long)cu_s * mult / BM) + s;
+}
+ST_HD int slot_tile(int slot, int first, int BM) {
+  return slot >= first ? slot - first : 0x7fffffff / BM;
 }
 
 #ifdef __CUDACC__
@@ -306,9 +314,9 @@ __device__ __forceinline__ int last_true(int n, P pred) {
 // Sequence and tile of a slot (the tile may be past the sequence's rows), by a
 // whole warp.
 __device__ __forceinline__ int find_slot(const Geo& g, int mult, int BM, int slot, int& tile) {
-  auto first = [&](int s) { return (int)((long long)cu_at(g, s) * mult / BM) + s; };
+  auto first = [&](int s) { return slot_first(cu_at(g, s), s, mult, BM); };
   const int s = last_true(g.S, [&](int x) { return first(x) <= slot; });
-  tile = slot - first(s);
+  tile = slot_tile(slot, first(s), BM);
   return s;
 }
 
