@@ -270,8 +270,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 64 ? 3 : 2)
       w[x] = mx > -INFINITY ? fast_exp2(sm[x * kRowsU + row] - mx) : 0.f;
       sum += w[x] * sm[(kWarps + x) * kRowsU + row];
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const float L = sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays NaN
+    const float L = sum != 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
     const size_t stride = (size_t)g.total * g.H;
     for (int c = lane * 2; c < D; c += 64) {
       float v0 = 0.f, v1 = 0.f;

@@ -443,12 +443,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++no;
         tc_fence_after();
       }
-      float L = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
-      float wc = l > 0.f ? 1.f / l : 0.f, wp = 0.f;
+      // (a sum that is not a number is kept, here and where parts are joined: the row
+      // must not pass for an empty one)
+      float L = l != 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+      float wc = l != 0.f ? 1.f / l : 0.f, wp = 0.f;
       const size_t rr = have ? (size_t)qr.t * g.H + qr.h : 0;
       if (a.mode == OUT_MERGE && have) {
         const float lp = a.parts.lse[rr], mx = fmaxf(lp, L);
-        if (mx > -INFINITY) {
+        if (lp != -INFINITY || L != -INFINITY) {
           const float out = mx + __logf(__expf(lp - mx) + __expf(L - mx));
           wp = __expf(lp - out);
           wc *= __expf(L - out);
@@ -477,12 +479,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 32; ++x) o[x] = any ? o[x] * wc : 0.f;
         if (a.mode == OUT_PARTIAL) {
-          if (wc > 0.f) {  // a part without weight is not read
+          if (wc != 0.f) {  // a part without weight is not read
             store_row32(a.parts.o + ((size_t)(part0 + part) * g.total * g.H + rr) * D + c, o);
           }
           continue;
         }
-        if (a.mode == OUT_MERGE && wp > 0.f) {
+        if (a.mode == OUT_MERGE && wp != 0.f) {
           const float4* src = reinterpret_cast<const float4*>(a.parts.o + rr * D + c);
 #pragma unroll
           for (int x = 0; x < 8; ++x) {

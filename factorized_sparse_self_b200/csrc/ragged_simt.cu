@@ -208,13 +208,13 @@ __global__ void __launch_bounds__(NT, 2) ragged_fwd_simt(const __grid_constant__
     weigh_tile<D>(W, B, ty, tx, acc);
   }
   // log-sum-exp of the row; joined with the other order's where asked
-  const float lse = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
-  float wc = sum > 0.f ? 1.f / sum : 0.f, wp = 0.f, out = lse;
+  const float lse = sum != 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+  float wc = sum != 0.f ? 1.f / sum : 0.f, wp = 0.f, out = lse;
   const size_t rr = have ? (size_t)qr.t * g.H + qr.h : 0;
   if (a.mode == OUT_MERGE && have) {
     const float lp = a.parts.lse[rr];
     const float mx = fmaxf(lp, lse);
-    if (mx > -INFINITY) {
+    if (lp != -INFINITY || lse != -INFINITY) {  // NaN stays NaN
       out = mx + logf(expf(lp - mx) + expf(lse - mx));
       wp = expf(lp - out);
       wc *= expf(lse - out);
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(NT, 2) ragged_fwd_simt(const __grid_constant__
       if (a.mode == OUT_PARTIAL) {
         a.parts.o[(size_t)(part0 + part) * g.total * g.H * D + o + c] = v;
       } else {
-        if (a.mode == OUT_MERGE && fp > 0.f) v = fmaf(fp, a.parts.o[o + c], v);
+        if (a.mode == OUT_MERGE && fp != 0.f) v = fmaf(fp, a.parts.o[o + c], v);
         static_cast<float*>(a.o)[o + c] = v;
       }
     }
@@ -517,7 +517,8 @@ __device__ __forceinline__ void store4<__half>(__half* p, float4 v) {
 
 constexpr int kJoinThreads = 256;
 
-// o = sum_p exp(lse_p - lse) o_p: one thread per four elements of a query row.
+// o = sum_p exp(lse_p - lse) o_p: one thread per four elements of a query row. A part
+// whose LSE is NaN makes the row NaN.
 template <class T>
 __global__ void __launch_bounds__(kJoinThreads)
     join_parts_kernel(const __grid_constant__ Geo g, const Parts parts, int nparts, int shift, T* o,
@@ -528,15 +529,20 @@ __global__ void __launch_bounds__(kJoinThreads)
   const long long rows = (long long)g.total * g.H;
   if (row >= rows || !in_sequence(g, (int)(row / g.H))) return;
   float m = -INFINITY;
+  bool any = false;  // whether a part is not empty (fmaxf passes over NaN)
 #pragma unroll 4
-  for (int p = 0; p < nparts; ++p) m = fmaxf(m, __ldg(parts.lse + p * rows + row));
+  for (int p = 0; p < nparts; ++p) {
+    const float f = __ldg(parts.lse + p * rows + row);
+    m = fmaxf(m, f);
+    any |= f != -INFINITY;
+  }
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-  if (m > -INFINITY) {
+  if (any) {
 #pragma unroll 4
     for (int p = 0; p < nparts; ++p) {
       const float w = expf(__ldg(parts.lse + p * rows + row) - m);
-      if (w > 0.f) {  // a part without weight may not have been written
+      if (w != 0.f) {  // a part without weight may not have been written
         const float4 v = __ldg(reinterpret_cast<const float4*>(parts.o + (p * rows + row) * g.d + c));
         acc.x = fmaf(w, v.x, acc.x);
         acc.y = fmaf(w, v.y, acc.y);
@@ -549,7 +555,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
   }
   store4(o + row * g.d + c, acc);
-  if (c == 0) lse[row] = m > -INFINITY ? m + logf(sum) : -INFINITY;
+  if (c == 0) lse[row] = any ? m + logf(sum) : -INFINITY;
 }
 
 // delta = dout . o of every row: 16 bytes a lane of o and of dout, 2^shift lanes a

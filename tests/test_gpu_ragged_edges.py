@@ -58,3 +58,79 @@ def test_paged_rows_before_the_first_sequence(pat, ty, lead):
                 check("o", o[a:a + n], ro, to)
                 check("lse", lse[a:a + n], rl, tl)
                 a += n
+
+
+# ---- query rows that are not finite ---------------------------------------------------------------
+
+
+def spoil(q, rows):
+    """q with NaN in one entry of the first of `rows`, infinities in the second, overflowing scores in the third (float16
+    cannot reach them: infinities of both signs)."""
+    bad = q.clone()
+    bad[rows[0], :, 5] = float("nan")
+    bad[rows[1]] = float("inf")
+    if q.dtype == torch.float16:
+        bad[rows[2]] = float("-inf")
+    else:
+        bad[rows[2]] = 3e38
+    return bad
+
+
+def only_those(rows, good, bad):
+    """Rows of NaN among `rows`, the others bit by bit as without them."""
+    keep = torch.ones(good.shape[0], dtype=torch.bool, device=good.device)
+    keep[rows] = False
+    assert torch.equal(good[keep], bad[keep])
+    assert bool(torch.isnan(bad[rows]).all())
+    assert not bool(torch.isnan(good).any())
+
+
+# one part a row; key ranges; two orders, the second joining the first, and with key ranges
+SPLITS = [(("dense", "merged", 1, 1), [300, 140], 24, 6), (("dense", "merged", 1, 1), [2100, 90], 2, 1),
+          (("strided", "merged", 16, 1), [300, 900], 72, 24), (("strided", "merged", 3, 1), [2100, 90], 2, 1),
+          (("fixed", "merged", 40, 30), [2100, 90], 2, 1)]
+
+
+@pytest.mark.parametrize("ty", THREE, ids=lambda t: f"{t[0]}-d{t[1]}")
+@pytest.mark.parametrize("pat,lens,H,Hkv", SPLITS, ids=str)
+def test_packed_query_rows_that_are_not_finite(pat, lens, H, Hkv, ty):
+    dtype, d = ty
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n = sum(lens)
+    q, k, v, dout = (randn(g, n, h, d, dtype=DT[dtype]) for h in (H, Hkv, Hkv, H))
+    P, cu = st.st_pattern(*pat), starts(lens)
+    rows = [lens[0] - 1, lens[0] - 40, 200]
+    bad = spoil(q, rows)
+    good_out = st.st_packed_attn_fwd(P, q, k, v, cu, max(lens))
+    bad_out = st.st_packed_attn_fwd(P, bad, k, v, cu, max(lens))
+    for a, b in zip(good_out, bad_out):
+        only_those(rows, a, b)
+    # the gradients of the other sequence, and dQ of the other rows
+    a = st.st_packed_attn_bwd(P, q, k, v, *good_out, dout, cu, max(lens))
+    b = st.st_packed_attn_bwd(P, bad, k, v, *bad_out, dout, cu, max(lens))
+    only_those(rows, a[0], b[0])
+    for x, y in zip(a[1:], b[1:]):
+        assert torch.equal(x[lens[0]:], y[lens[0]:])
+    assert st.st_last_device_status() == st.ST_OK
+
+
+@pytest.mark.parametrize("ty", THREE, ids=lambda t: f"{t[0]}-d{t[1]}")
+@pytest.mark.parametrize("pat", [("dense", "merged", 1, 1), ("strided", "merged", 16, 1), ("fixed", "merged", 40, 30)], ids=str)
+def test_paged_query_rows_that_are_not_finite(pat, ty):
+    """Decoding and chunks, with one key range and several (max_kv steers the split only)."""
+    dtype, d = ty
+    H, Hkv = 4, 2
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for lens, new, rows in (([3000, 2500, 2000, 40], [1, 1, 1, 1], [0, 1, 2]), ([3000, 40], [300, 9], [299, 0, 100])):
+        kc, vc, table = make_cache(g, lens, 16, Hkv, d, DT[dtype])
+        kc.normal_(generator=g)
+        vc.normal_(generator=g)
+        q = randn(g, sum(new), H, d, dtype=DT[dtype])
+        bad = spoil(q, rows)
+        kv, cu = torch.tensor(lens, dtype=torch.int32, device="cuda"), starts(new)
+        for max_kv in (1, 3000):
+            for max_q in (1, max(new), 100000):
+                out = [st.st_paged_attn(st.st_pattern(*pat), x, kc, vc, table, cu, kv, max_q, max_kv) for x in (q, bad)]
+                for a, b in zip(*out):
+                    only_those(rows, a, b)
+    assert st.st_last_device_status() == st.ST_OK
