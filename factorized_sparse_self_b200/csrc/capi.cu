@@ -28,19 +28,27 @@ std::mutex g_mu;
 
 // Device status word of the current device (allocated on first use, which is
 // inside st_pattern_layout or the first call of the ragged and paged entry
-// points, never inside the layouts' fwd/bwd).
+// points, never inside the layouts' fwd/bwd). That call may be under capture: the
+// thread allocates in the relaxed mode, and the word is cleared on a stream of its
+// own, which neither joins a capture nor waits for one.
+int* new_status_word() {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
+  int* p = nullptr;
+  cudaStream_t s = nullptr;
+  bool ok = cudaMalloc(&p, sizeof(int)) == cudaSuccess &&
+            cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) == cudaSuccess &&
+            cudaMemsetAsync(p, 0, sizeof(int), s) == cudaSuccess &&
+            cudaStreamSynchronize(s) == cudaSuccess;
+  if (s) ok = cudaStreamDestroy(s) == cudaSuccess && ok;
+  if (!ok && p) cudaFree(p);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  return ok ? p : nullptr;
+}
 int* status_word(int dev, bool create) {
   if (dev < 0 || dev >= kMaxDevices) return nullptr;
   std::lock_guard<std::mutex> lk(g_mu);
-  if (!g_status[dev] && create) {
-    int* p = nullptr;
-    if (cudaMalloc(&p, sizeof(int)) != cudaSuccess) return nullptr;
-    if (cudaMemset(p, 0, sizeof(int)) != cudaSuccess) {
-      cudaFree(p);
-      return nullptr;
-    }
-    g_status[dev] = p;
-  }
+  if (!g_status[dev] && create) g_status[dev] = new_status_word();
   return g_status[dev];
 }
 

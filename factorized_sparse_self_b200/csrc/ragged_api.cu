@@ -139,16 +139,10 @@ st_status fill_cache(const st_cache_desc* c, Geo& g) {
   return ST_OK;
 }
 
-// The status word of the current device; it is created by the first call
-// (which therefore may not be captured).
-st_status get_status(Geo& g, cudaStream_t stream) {
+// The status word of the current device; the first call creates it.
+st_status get_status(Geo& g) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
-  g.status = device_status(dev, false);
-  if (g.status) return ST_OK;
-  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess || cap != cudaStreamCaptureStatusNone)
-    return ST_ERR_CUDA;
   g.status = device_status(dev, true);
   return g.status ? ST_OK : ST_ERR_CUDA;
 }
@@ -363,7 +357,7 @@ st_status st_packed_attn_fwd(const st_pattern_desc* p, st_dtype dtype, const st_
   const FwdPlan f = plan_fwd(g, *p, dtype, p->T, false);
   if (!workspace_ok(ws, ws_bytes, f.bytes)) return ST_ERR_WORKSPACE;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  s = get_status(g, cs);
+  s = get_status(g);
   if (s != ST_OK) return s;
   g.cu = cu;
   return run_fwd(*p, dtype, g, scale, f, q, k, v, o, lse, ws, cs);
@@ -400,7 +394,7 @@ st_status st_packed_attn_bwd(const st_pattern_desc* p, st_dtype dtype, const st_
   const BwdPlan b = plan_bwd(g, *p, dtype);
   if (!workspace_ok(ws, ws_bytes, b.bytes)) return ST_ERR_WORKSPACE;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  s = get_status(g, cs);
+  s = get_status(g);
   if (s != ST_OK) return s;
   g.cu = cu;
   a.g = g;
@@ -495,7 +489,7 @@ st_status st_paged_attn(const st_pattern_desc* p, st_dtype dtype, const st_packe
   const FwdPlan f = plan_fwd(g, *p, dtype, max_q, true);
   if (!workspace_ok(ws, ws_bytes, f.bytes)) return ST_ERR_WORKSPACE;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  s = get_status(g, cs);
+  s = get_status(g);
   if (s != ST_OK) return s;
   g.cu = cu;
   g.kv_lens = kv_lens;
@@ -523,7 +517,7 @@ st_status st_cache_append(st_dtype dtype, const st_packed_desc* x, const st_cach
       !aligned4(cu) || !aligned4(kv_lens))
     return ST_ERR_INVALID;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  s = get_status(gc, cs);
+  s = get_status(gc);
   if (s != ST_OK) return s;
   gc.cu = cu;
   gc.kv_lens = kv_lens;

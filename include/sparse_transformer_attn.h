@@ -271,10 +271,9 @@ st_status st_sparse_attn_bwd_noalloc(const st_layout* layout, st_dtype dtype, in
  *  - workspace: device memory of at least the queried size, 256-byte aligned,
  *    overwritten; may be NULL when the size is 0. Calls (or replays of captured
  *    graphs) that may run at the same time need a workspace each.
- *  - The first of these calls on a device creates the word that kernels report
- *    to (the device status; a few bytes): make it, a workspace query for
- *    instance, before any stream capture. Afterwards no call allocates, and none
- *    synchronises.
+ *  - The first of these calls that launches on a device creates the word that
+ *    kernels report to (the device status; a few bytes), under stream capture as
+ *    well. No other call allocates, and none synchronises the caller's streams.
  *  - The results are bitwise reproducible from run to run.
  *  - Everything runs on the current device, on which the tensors must lie.
  */

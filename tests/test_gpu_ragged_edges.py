@@ -1,9 +1,13 @@
 """Packed and paged attention on the GPU where callers' data lie at the edges: rows before the first sequence, rows that
 are not finite, lengths past the cache, first calls inside a capture. Reference and bounds: tests/ragged_ref.py."""
+import subprocess
+import sys
+
 import pytest
 import torch
 
 import factorized_sparse_self_b200 as st
+from conftest import ROOT
 from ragged_ref import One, check
 from test_gpu_ragged import DT, make_cache, packed, randn, starts
 
@@ -134,3 +138,61 @@ def test_paged_query_rows_that_are_not_finite(pat, ty):
                 for a, b in zip(*out):
                     only_those(rows, a, b)
     assert st.st_last_device_status() == st.ST_OK
+
+
+# ---- a process whose first call is captured ---------------------------------------------------------
+
+FIRST = r"""
+import torch
+import factorized_sparse_self_b200 as st
+
+calls = {calls!r}
+g = torch.Generator(device="cuda").manual_seed(0)
+n, H, Hkv, d = 200, 4, 2, 64
+q, k, v, dout = (torch.randn(n, h, d, generator=g, device="cuda").to(torch.{dtype}) for h in (H, Hkv, Hkv, H))
+P = st.st_pattern("strided", "merged", 16)
+cu = torch.tensor([0, 150, n], dtype=torch.int32, device="cuda")
+kc, vc = (torch.zeros(14, 16, Hkv, d, dtype=q.dtype, device="cuda") for _ in range(2))
+table = torch.arange(20, dtype=torch.int32, device="cuda").remainder(14).view(2, 10).contiguous()
+table[1] = torch.tensor([10, 11, 12, 13, 0, 0, 0, 0, 0, 0], dtype=torch.int32)
+kv = torch.tensor([150, 50], dtype=torch.int32, device="cuda")
+
+def run():
+    out = []
+    if "packed" in calls:
+        o, lse = st.st_packed_attn_fwd(P, q, k, v, cu, 150)
+        out += [o, lse, *st.st_packed_attn_bwd(P, q, k, v, o, lse, dout, cu, 150)]
+    if "append" in calls:
+        st.st_cache_append(k, v, kc, vc, table, cu, kv)
+        out += [kc, vc]
+    if "paged" in calls:
+        out += st.st_paged_attn(P, q, kc, vc, table, cu, kv, 150, 150)
+    return out
+
+torch.cuda.synchronize()
+if {query}:
+    st.st_packed_attn_fwd_workspace(P, q, k, v, cu, 150)
+    st.st_paged_attn_workspace(P, q, kc, vc, table, cu, kv, 150, 150)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+for x in got:
+    x.zero_()
+graph.replay()
+torch.cuda.synchronize()
+assert st.st_last_device_status() == st.ST_OK
+got = [x.clone() for x in got]
+assert any(bool((x != 0).any()) for x in got)
+for a, b in zip(got, run()):
+    assert torch.equal(a, b)
+print("FIRST CALL OK")
+"""
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("query,calls", [(True, ("packed",)), (False, ("packed",)), (False, ("append", "paged"))], ids=str)
+def test_first_call_of_a_process_under_capture(query, calls, dtype):
+    """Nothing ran before, at most a workspace query: the status word is made while the stream is captured."""
+    got = subprocess.run([sys.executable, "-c", FIRST.format(query=query, calls=calls, dtype=dtype)], cwd=ROOT,
+                         capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0 and "FIRST CALL OK" in got.stdout, got.stderr[-2000:]
