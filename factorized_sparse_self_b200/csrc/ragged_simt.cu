@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 // One warp per new token: the 16-byte chunks of its key and value rows, head by
 // head, go to the slot of its position, eight in flight a lane. Tokens at negative
 // positions are dropped; so are positions past the page table and pages outside
-// the cache, which are reported. Bound by the copy itself: 36.8 k tokens of 4 KB
+// the cache, which are reported, as is a length outside the page table. Bound by the copy itself: 36.8 k tokens of 4 KB
 // (302 MB moved) take 53 us, 5.7 TB/s (a warp per token and head: 111 us, each
 // looking its sequence and page up for 512 bytes).
 __global__ void __launch_bounds__(32 * kJoinRows)
@@ -634,7 +634,10 @@ __global__ void __launch_bounds__(32 * kJoinRows)
   if (t >= g.total) return;
   int s;
   if (!seq_of_token(g, t, s)) return;
-  const int pos = __ldg(g.kv_lens + s) - (cu_at(g, s + 1) - t);
+  const int len = __ldg(g.kv_lens + s);
+  if (len < 0 || len > g.max_pages * g.page_size) set_status(g.status, ST_ERR_INVALID);
+  if (len < 0) return;
+  const int pos = len - (cu_at(g, s + 1) - t);
   if (pos < 0) return;
   const int pg = fdiv(pos, g.fpage);
   const int page = pg < g.max_pages ? __ldg(g.table + (size_t)s * g.max_pages + pg) : -1;

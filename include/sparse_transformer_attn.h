@@ -298,7 +298,9 @@ typedef struct {
  * each sequence, the new tokens included: new token t of n is at position
  * kv_len - n + t. Rows at negative positions attend nothing (O = 0, LSE = -inf),
  * so a padding sequence may have kv_len 0. A kv_len outside 0 .. max_pages *
- * page_size is clamped and sets the device status to ST_ERR_INVALID. */
+ * page_size sets the device status to ST_ERR_INVALID; attention clamps it, an
+ * append drops the tokens at positions outside that range and writes the others
+ * where kv_len puts them. */
 typedef struct {
   int32_t num_pages, page_size, max_pages;
   int64_t page_stride, slot_stride, head_stride;

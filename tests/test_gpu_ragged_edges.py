@@ -196,3 +196,38 @@ def test_first_call_of_a_process_under_capture(query, calls, dtype):
     got = subprocess.run([sys.executable, "-c", FIRST.format(query=query, calls=calls, dtype=dtype)], cwd=ROOT,
                          capture_output=True, text=True, timeout=300)
     assert got.returncode == 0 and "FIRST CALL OK" in got.stdout, got.stderr[-2000:]
+
+
+# ---- lengths outside the page table -----------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f32", 32)])
+def test_append_reports_lengths_outside_the_page_table(dtype, d):
+    """Two pages of 16 slots a sequence. Tokens that the length puts past the last slot, or before the first, are
+    dropped; the others are written; the length is reported either way."""
+    Hkv, page = 2, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    table = torch.tensor([[2, 0], [3, 1]], dtype=torch.int32, device="cuda")
+    k, v = (randn(g, 7, Hkv, d, dtype=DT[dtype]) for _ in range(2))
+    new = [3, 4]
+    for bad in (33, 34, 60, 2 ** 31 - 1, -1, -30, -2 ** 31):
+        for which in (0, 1):
+            lens = [20, 20]
+            lens[which] = bad
+            kc, vc = (torch.full((4, page, Hkv, d), x, dtype=DT[dtype], device="cuda") for x in (3.0, 4.0))
+            want_k, want_v = kc.clone(), vc.clone()
+            a = 0
+            for s, (n, m) in enumerate(zip(lens, new)):
+                for t in range(m):
+                    p = n - m + t
+                    if 0 <= p < 2 * page:
+                        want_k[int(table[s, p // page]), p % page] = k[a + t]
+                        want_v[int(table[s, p // page]), p % page] = v[a + t]
+                a += m
+            st.st_cache_append(k, v, kc, vc, table, starts(new), torch.tensor(lens, dtype=torch.int32, device="cuda"))
+            assert st.st_last_device_status() == st.ST_ERR_INVALID, bad
+            assert st.st_last_device_status() == st.ST_OK
+            assert torch.equal(kc, want_k) and torch.equal(vc, want_v), bad
+    # the largest length, and rows at negative positions, are no error
+    st.st_cache_append(k, v, kc, vc, table, starts(new), torch.tensor([32, 2], dtype=torch.int32, device="cuda"))
+    assert st.st_last_device_status() == st.ST_OK
