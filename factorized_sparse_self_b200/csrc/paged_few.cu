@@ -8,12 +8,13 @@
 // head, job, key range), one CTA of four warps. Each warp takes every fourth tile
 // of 16 keys on its own: its ring of K / V tiles in shared memory is filled by
 // 16-byte asynchronous copies through the page table, no barrier stands between
-// warps until the end, and two to three CTAs of an SM keep about 100 KB in
-// flight. Scores and products are 16 x 8 x 16 matrix instructions (the rows fill
-// their 16-row operand; tcgen05 would want 128), the softmax is online with fp32
-// statistics: the accumulator is rescaled only when a row's maximum grows by more
-// than 2^8. The four warps' results are joined in shared memory; key ranges are
-// joined by the parts kernel.
+// warps until the end, and the two CTAs of an SM (rings of 96 KB each at d = 128, of
+// 80 at d = 64; a third would not fit) keep about 128 KB in flight. Scores and
+// products are 16 x 8 x 16 matrix instructions (the rows fill their 16-row operand;
+// tcgen05 would want 128), the softmax is online with fp32 statistics: the
+// accumulator is rescaled only when a row's maximum grows by more than 2^8. The four
+// warps' results are joined in shared memory; key ranges are joined by the parts
+// kernel.
 #include "ragged.h"
 #include "tc_common.cuh"
 
@@ -72,7 +73,7 @@ __device__ __forceinline__ void mma16(float* c, const uint32_t* a, uint32_t b0, 
 }
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kWarps * 32, D == 64 ? 3 : 2)
+__global__ void __launch_bounds__(kWarps * 32, 2)
     few_rows_kernel(const __grid_constant__ FwdLaunch a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int NS = Cfg<D>::kStages, TB = Cfg<D>::kTile;
