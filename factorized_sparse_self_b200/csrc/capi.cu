@@ -145,6 +145,7 @@ void arm(Call& c, int kernel) {
 namespace st {
 int* device_status(int dev, bool create) { return status_word(dev, create); }
 uint64_t wait_limit_ns() { return g_wait_ns.load(); }
+bool take_force_timeout() { return g_force_timeout.exchange(0) != 0; }
 }  // namespace st
 
 extern "C" {
@@ -342,7 +343,7 @@ st_status st_sparse_attn_fwd_heads(const st_layout* L, st_dtype dtype, int32_t B
   if (dtype == ST_F32) {
     e = simt_fwd(c, q, k, v, o, lse);
   } else {
-    e = tc_fwd(c, q, k, v, o, lse, g_force_timeout.exchange(0));
+    e = tc_fwd(c, q, k, v, o, lse, take_force_timeout());
   }
   return e == cudaSuccess ? ST_OK : ST_ERR_CUDA;
 }

@@ -35,6 +35,9 @@ inline void record_end(const Call& c) {
 // created, or cannot be), and the bound of on-device waits.
 int* device_status(int dev, bool create);
 uint64_t wait_limit_ns();
+// Whether this launch is to run into its waits on purpose (st_set_wait_limit); clears
+// the request.
+bool take_force_timeout();
 
 // Multiprocessor count of the current device (queried once per device).
 int sm_count();

@@ -45,6 +45,7 @@ struct FwdLaunch {
   int32_t taper;   // ranges get shorter, and short ones go last
   int32_t mode;    // OutMode
   float scale_log2;
+  int32_t force_timeout;  // test hook: each CTA's first key tile is never loaded
   uint64_t wait_ns;
   cudaStream_t stream;
 };

@@ -249,6 +249,7 @@ st_status run_fwd(const st_pattern_desc& p, st_dtype dtype, Geo& g, float scale,
   a.taper = f.taper;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)g.d)) * 1.4426950408889634f;
   a.wait_ns = wait_limit_ns();
+  a.force_timeout = !f.few && dtype != ST_F32 && take_force_timeout();
   a.stream = stream;
   Job jobs[2];
   const int n = make_jobs(p, jobs);

@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return k < kSched || __all_sync(0xffffffffu, bar_wait(&S.sched_empty[k % kSched],
                                                               (k / kSched + 1) & 1, limit, abort));
       };
-      Claims claims = {&S.claim, &S.claim_bar, &S.want, 0, 0};
+      Claims claims = {&S.claim, &S.claim_bar, &S.want, 0, 0, 0, true};
       for (int n = blockIdx.x; n >= 0;) {
         ok = slot_free();
         if (!ok) break;
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) {
         if (lane == 0) fail();
-        claims_drain(claims, limit);
+        claims_drop(claims, limit);
       }
     } else if (warp != 9) {
       // ---------------- producers ----------------
@@ -381,13 +381,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
       }
       gath.flush();
-      if (!ok) {
-        if (lane == 0) fail();
-        // copies in flight land before the CTA may exit
-        for (int i = imax(0, used - NR); i < used; ++i) mbar_wait_drain(&S.r_full[i % NR], (i / NR) & 1, limit);
-        for (int i = imax(0, tt - NA); i <= tt; ++i) mbar_wait_drain(&S.full[i % NA], (i / NA) & 1, limit);
-        for (int i = imax(0, tt - NB); i <= tt; ++i) mbar_wait_drain(&S.full[NA + i % NB], (i / NB) & 1, limit);
-      }
+      if (!ok && lane == 0) fail();
+      // copies in flight land before the CTA may exit (another role may have given up
+      // without waiting for them); a tile that was begun may have filled its slots
+      const int end = ok ? tt : tt + 1;
+      for (int i = imax(0, used - NR); i < used; ++i) mbar_wait_drain(&S.r_full[i % NR], (i / NR) & 1, limit);
+      for (int i = imax(0, end - NA); i < end; ++i) mbar_wait_drain(&S.full[i % NA], (i / NA) & 1, limit);
+      for (int i = imax(0, end - NB); i < end; ++i) mbar_wait_drain(&S.full[NA + i % NB], (i / NB) & 1, limit);
     } else {
       // ---------------- MMA issuer ----------------
       const uint32_t idS = idesc_16(128, 128, false, false, F16);

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return k < kSched || __all_sync(0xffffffffu, bar_wait(&S.sched_empty[k % kSched],
                                                                (k / kSched + 1) & 1, limit, abort));
       };
-      Claims claims = {&S.claim, &S.claim_bar, &S.want, 0, 0};
+      Claims claims = {&S.claim, &S.claim_bar, &S.want, 0, 0, 0, true};
       for (int n = blockIdx.x; n >= 0;) {
         ok = slot_free();
         if (!ok) break;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) {
         if (lane == 0) fail();
-        claims_drain(claims, limit);
+        claims_drop(claims, limit);
       }
     } else if (warp != 9) {
       // ---------------- producers ----------------
@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv, ++kt) {
               const int s = kt % NS;
+              if (a.force_timeout && kt == 0) continue;  // test hook: this stage never fills
               if (kt >= NS && !wait(&S.kv_empty[s], (kt / NS + 1) & 1)) break;
               if (!R) {
                 gather64<D>(smem_u32(S.kv[s]), pw * 64, kv ? a.v : a.k, kv ? rv[0] : rk[0], kv ? rv[1] : rk[1]);
@@ -211,13 +212,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&S.sched_empty[n % kSched]);
       }
       gath.flush();
-      if (!ok) {
-        if (lane == 0) fail();
-        // copies in flight land before the CTA may exit
-        for (int i = imax(0, used - QB); i < used; ++i) mbar_wait_drain(&S.q_full[i % QB], (i / QB) & 1, limit);
-        for (int i = imax(0, kt - NS); i < kt; ++i)
-          mbar_wait_drain(&S.kv_full[i % NS], (i / NS) & 1, limit);
-      }
+      if (!ok && lane == 0) fail();
+      // copies in flight land before the CTA may exit (another role may have given up
+      // without waiting for them)
+      for (int i = imax(0, used - QB); i < used; ++i) mbar_wait_drain(&S.q_full[i % QB], (i / QB) & 1, limit);
+      for (int i = imax(0, kt - NS); i < kt; ++i) mbar_wait_drain(&S.kv_full[i % NS], (i / NS) & 1, limit);
     } else if (warp == 9) {
       // ---------------- MMA issuer ----------------
       const uint32_t idS = idesc_16(128, 128, false, false, F16);

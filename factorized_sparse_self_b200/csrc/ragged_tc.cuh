@@ -276,7 +276,24 @@ struct Claims {
   uint64_t* bar;
   uint64_t* want;
   int n, units;   // claims made, units handed on
+  int read;       // answers read
+  bool left;      // false once the grid was used up (it may not be asked again)
 };
+__device__ __forceinline__ void claims_ask(Claims& c) {
+  if ((threadIdx.x & 31) == 0) {
+    fence_async_smem();  // the answer before this one was read
+    mbar_arrive_expect_tx(c.bar, 16);
+    claim_next(c.slot, c.bar);
+  }
+  ++c.n;
+}
+__device__ __forceinline__ int claims_answer(Claims& c) {
+  const int got = claimed(c.slot);
+  __syncwarp();
+  ++c.read;
+  c.left = got >= 0;
+  return got;
+}
 // Next unit index (by a whole warp): -1 when the grid is used up, -2 when a wait
 // ran out.
 __device__ __forceinline__ int claims_take(Claims& c, bool handed_on, uint64_t limit, volatile int* abort) {
@@ -284,20 +301,19 @@ __device__ __forceinline__ int claims_take(Claims& c, bool handed_on, uint64_t l
     const int u = c.units++;
     if (!__all_sync(0xffffffffu, bar_wait(c.want, u & 1, limit, abort))) return -2;
   }
-  if ((threadIdx.x & 31) == 0) {
-    fence_async_smem();  // the answer before this one was read
-    mbar_arrive_expect_tx(c.bar, 16);
-    claim_next(c.slot, c.bar);
-  }
-  const int k = c.n++;
-  if (!__all_sync(0xffffffffu, bar_wait(c.bar, k & 1, limit, abort))) return -2;
-  const int got = claimed(c.slot);
-  __syncwarp();
-  return got;
+  claims_ask(c);
+  if (!__all_sync(0xffffffffu, bar_wait(c.bar, (c.n - 1) & 1, limit, abort))) return -2;
+  return claims_answer(c);
 }
-// After a wait that ran out: a claim in flight lands before the CTA may exit.
-__device__ __forceinline__ void claims_drain(const Claims& c, uint64_t limit) {
-  if (c.n > 0) mbar_wait_drain(c.bar, (c.n - 1) & 1, limit);
+// After a wait that ran out: a claim in flight lands before the CTA may exit, and
+// the units that have not started are claimed and dropped, for in a launch that has
+// failed each of their CTAs would wait as long again.
+__device__ __forceinline__ void claims_drop(Claims& c, uint64_t limit) {
+  while (c.left) {
+    if (c.read == c.n) claims_ask(c);
+    if (!__all_sync(0xffffffffu, mbar_wait_drain(c.bar, (c.n - 1) & 1, limit))) return;
+    claims_answer(c);
+  }
 }
 
 // Host: the boxes of a launch. False when the driver refuses one.

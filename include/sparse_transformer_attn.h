@@ -355,18 +355,21 @@ st_status st_cache_append(st_dtype dtype, const st_packed_desc* desc, const st_c
 
 /* Synchronises `stream`, then returns and clears the device-side status word
  * of the current device: ST_ERR_DEVICE_TIMEOUT after a kernel's bounded wait
- * ran out, ST_ERR_UNSUPPORTED if the backward kernel found its shared memory
- * misaligned (it then computes nothing); ST_OK otherwise. ST_ERR_CUDA if the
+ * ran out, ST_ERR_UNSUPPORTED if a backward kernel found its shared memory
+ * misaligned (it then computes nothing), ST_ERR_INVALID after a paged call met a
+ * page number or a length outside the cache; ST_OK otherwise. ST_ERR_CUDA if the
  * sync fails. */
 st_status st_last_device_status(void* stream);
 
 /* Upper bound, in nanoseconds, of every on-device wait of later launches
  * (default 2e9), process-wide: it applies to launches from every host thread
  * (the setting is atomic). 0 restores the default. A wait that runs out sets
- * the status word and makes the kernel return early. For tests of the timeout
- * path only, force_timeout != 0 makes the next bf16 / fp16 forward launch, from
- * whichever thread comes first, skip the loads of its first key tile so its
- * waits run out on purpose (the GPU stays usable). */
+ * the status word and makes the kernel return early; units of the launch that have
+ * not started are dropped. For tests of the timeout path only, force_timeout != 0
+ * makes the next bf16 / fp16 forward call whose kernel has such waits (of a layout, or
+ * packed or paged in tiles of 256 rows), from whichever thread comes first, skip the
+ * loads of a CTA's first key tile so its waits run out on purpose (the GPU stays
+ * usable). */
 st_status st_set_wait_limit(uint64_t ns, int32_t force_timeout);
 
 /* Kernel launches one fwd / bwd call makes with this layout and dtype (the
@@ -376,8 +379,8 @@ st_status st_layout_launches(const st_layout* layout, st_dtype dtype, int32_t* f
                              int32_t* bwd_launches);
 
 /* Benchmark instrumentation. enable != 0 creates (once) four pairs of CUDA
- * events on the current device; from then on every fwd call records pair 0
- * around its attention launches, and every bwd call records pair 1 around its
+ * events on the current device; from then on every fwd call of a layout records pair 0
+ * around its attention launches, and every bwd call of one records pair 1 around its
  * main attention kernel, pair 2 around its prologue and pair 3 around its
  * epilogue (16-bit path; the epilogue pair brackets nothing when no row
  * accumulates), on the call's stream. enable = 0 stops recording. Events are

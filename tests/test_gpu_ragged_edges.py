@@ -231,3 +231,62 @@ def test_append_reports_lengths_outside_the_page_table(dtype, d):
     # the largest length, and rows at negative positions, are no error
     st.st_cache_append(k, v, kc, vc, table, starts(new), torch.tensor([32, 2], dtype=torch.int32, device="cuda"))
     assert st.st_last_device_status() == st.ST_OK
+
+
+# ---- waits that run out -----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f16", 128)])
+def test_a_launch_that_times_out_ends_at_once(dtype, d):
+    """32 k units, more than 200 for every SM. Each CTA that runs meets a tile that never comes and gives up after the
+    limit of 20 ms (and as long again for the copies that it waits for); units that have not started are dropped. One
+    CTA after the other would take more than 4 s. The next call is right."""
+    n, H, Hkv = 4000, 16, 8
+    g = torch.Generator(device="cuda").manual_seed(6)
+    q, k, v = (randn(g, n, h, d, dtype=DT[dtype]) for h in (H, Hkv, Hkv))
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    P = st.st_pattern("dense")
+    want = st.st_packed_attn_fwd(P, q, k, v, cu, 1)
+    assert st.st_last_device_status() == st.ST_OK
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    st.st_set_wait_limit(20_000_000, force_timeout=True)
+    try:
+        begin.record()
+        st.st_packed_attn_fwd(P, q, k, v, cu, 1)
+        end.record()
+        assert st.st_last_device_status() == st.ST_ERR_DEVICE_TIMEOUT
+        assert begin.elapsed_time(end) < 1000
+    finally:
+        st.st_set_wait_limit(0, force_timeout=False)
+    assert st.st_last_device_status() == st.ST_OK
+    for a, b in zip(want, st.st_packed_attn_fwd(P, q, k, v, cu, 1)):
+        assert torch.equal(a, b)
+    assert st.st_last_device_status() == st.ST_OK
+
+
+def test_a_forced_time_out_waits_for_a_kernel_with_waits():
+    """Calls whose kernels have none (a decoding step, float32) pass it by; a chunk takes it, once."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    kc, vc, table = make_cache(g, [400, 300], 16, 2, 64, torch.bfloat16)
+    kc.normal_(generator=g)
+    vc.normal_(generator=g)
+    q = randn(g, 200, 8, 64, dtype=torch.bfloat16)
+    kv, P = torch.tensor([400, 300], dtype=torch.int32, device="cuda"), st.st_pattern("dense")
+
+    def step(m):
+        return st.st_paged_attn(P, q[:2 * m], kc, vc, table, starts([m, m]), kv, m, 400)
+
+    want = step(1), step(100)
+    x = randn(g, 50, 2, 64, dtype=torch.float32)
+    st.st_set_wait_limit(20_000_000, force_timeout=True)
+    try:
+        got = step(1)
+        st.st_packed_attn_fwd(P, x, x, x, starts([50]), 50)
+        assert st.st_last_device_status() == st.ST_OK
+        step(100)
+        assert st.st_last_device_status() == st.ST_ERR_DEVICE_TIMEOUT
+        for a, b in zip(want[0] + want[1], got + step(100)):
+            assert torch.equal(a, b)
+        assert st.st_last_device_status() == st.ST_OK
+    finally:
+        st.st_set_wait_limit(0, force_timeout=False)
