@@ -18,6 +18,10 @@ using namespace st;
 namespace {
 
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;
+// A CTA that gives up waits once more, for as long, for its own copies and products
+// before it exits. They end within microseconds; a limit of less than this could let
+// it exit, or free tensor memory, under them.
+constexpr uint64_t kLeastWaitNs = 1000000ull;
 // Process-wide, read by every later launch from any host thread.
 std::atomic<uint64_t> g_wait_ns{kDefaultWaitNs};
 std::atomic<int> g_force_timeout{0};
@@ -476,7 +480,7 @@ st_status st_kernel_elapsed_ms(int32_t kernel, float* ms) {
 }
 
 st_status st_set_wait_limit(uint64_t ns, int32_t force_timeout) {
-  g_wait_ns.store(ns ? ns : kDefaultWaitNs);
+  g_wait_ns.store(ns ? std::max<uint64_t>(ns, kLeastWaitNs) : kDefaultWaitNs);
   g_force_timeout.store(force_timeout ? 1 : 0);
   return ST_OK;
 }

@@ -363,7 +363,8 @@ st_status st_last_device_status(void* stream);
 
 /* Upper bound, in nanoseconds, of every on-device wait of later launches
  * (default 2e9), process-wide: it applies to launches from every host thread
- * (the setting is atomic). 0 restores the default. A wait that runs out sets
+ * (the setting is atomic). 0 restores the default; a limit below 1 ms counts as 1 ms,
+ * which copies and products under way always need less than. A wait that runs out sets
  * the status word and makes the kernel return early; units of the launch that have
  * not started are dropped. For tests of the timeout path only, force_timeout != 0
  * makes the next bf16 / fp16 forward call whose kernel has such waits (of a layout, or

@@ -290,3 +290,26 @@ def test_a_forced_time_out_waits_for_a_kernel_with_waits():
         assert st.st_last_device_status() == st.ST_OK
     finally:
         st.st_set_wait_limit(0, force_timeout=False)
+
+
+def test_shortest_wait_limit_leaves_time_for_copies_under_way():
+    """A limit of a nanosecond counts as a millisecond: no wait of these calls is that long."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    lens = [700, 300, 1]
+    q, k, v, dout = (randn(g, 1001, h, 64, dtype=torch.bfloat16) for h in (8, 4, 4, 8))
+    cu, P = starts(lens), st.st_pattern("strided", "merged", 20)
+
+    def run():
+        o, lse = st.st_packed_attn_fwd(P, q, k, v, cu, 700)
+        return (o, lse, *st.st_packed_attn_bwd(P, q, k, v, o, lse, dout, cu, 700))
+
+    want = run()
+    torch.cuda.synchronize()
+    st.st_set_wait_limit(1, force_timeout=False)
+    try:
+        got = run()
+        assert st.st_last_device_status() == st.ST_OK
+    finally:
+        st.st_set_wait_limit(0, force_timeout=False)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
