@@ -332,7 +332,8 @@ class Pattern:
         self.l, self.c = int(l), int(c)
 
     def _desc(self, max_len):
-        return _Desc(self.kind, self.mode, int(max_len), self.l, self.c)
+        # a batch of empty sequences only has a longest one of 0
+        return _Desc(self.kind, self.mode, int(max_len) or 1, self.l, self.c)
 
 
 def st_pattern(kind, mode="merged", l=1, c=1) -> Pattern:
@@ -544,7 +545,7 @@ def _paged_workspace(pat, code, x, c, max_q):
 def st_paged_attn_workspace(pattern: Pattern, q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q,
                             max_kv) -> int:
     x, c, _ = _paged_args(q, k_cache, v_cache, page_table, cu_q, kv_lens)
-    return _paged_workspace(pattern._desc(max_kv), _dtype_code(q), x, c, int(max_q))
+    return _paged_workspace(pattern._desc(max_kv), _dtype_code(q), x, c, int(max_q) or 1)
 
 
 def st_paged_attn(pattern: Pattern, q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q, max_kv,
@@ -556,7 +557,7 @@ def st_paged_attn(pattern: Pattern, q, k_cache, v_cache, page_table, cu_q, kv_le
     expected, only steer how work is split. Returns o [total, H, d], lse float32 [total, H]."""
     import torch
     x, c, (pt, cu, kv) = _paged_args(q, k_cache, v_cache, page_table, cu_q, kv_lens)
-    code, pat, max_q = _dtype_code(q), pattern._desc(max_kv), int(max_q)
+    code, pat, max_q = _dtype_code(q), pattern._desc(max_kv), int(max_q) or 1
     nb = _paged_workspace(pat, code, x, c, max_q)
     sp = _call_stream(stream, q)
     if stream is None:

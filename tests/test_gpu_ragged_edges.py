@@ -313,3 +313,34 @@ def test_shortest_wait_limit_leaves_time_for_copies_under_way():
         st.st_set_wait_limit(0, force_timeout=False)
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+# ---- batches without tokens ---------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [0, 5])
+def test_batches_of_empty_sequences(rows, dtype):
+    """The longest sequence is 0 long; rows of no sequence stay as they were."""
+    H, Hkv, d, dt = 4, 2, 64, DT[dtype]
+    g = torch.Generator(device="cuda").manual_seed(9)
+    P, cu = st.st_pattern("strided", "merged", 8), starts([0, 0, 0])
+    q, k, v, dout = (randn(g, rows, h, d, dtype=dt) for h in (H, Hkv, Hkv, H))
+    o, lse, dq, dk, dv = (torch.full((rows, *s), 7.0, dtype=t, device="cuda") for s, t in (
+        ((H, d), dt), ((H,), torch.float32), ((H, d), dt), ((Hkv, d), dt), ((Hkv, d), dt)))
+    st.st_packed_attn_fwd_workspace(P, q, k, v, cu, 0)
+    st.st_packed_attn_bwd_workspace(P, q, k, v, cu, 0)
+    st.st_packed_attn_fwd(P, q, k, v, cu, 0, o=o, lse=lse)
+    st.st_packed_attn_bwd(P, q, k, v, o, lse, dout, cu, 0, dq=dq, dk=dk, dv=dv)
+    kc, vc, table = make_cache(g, [0, 0, 0], 16, Hkv, d, dt)
+    kv = torch.zeros(3, dtype=torch.int32, device="cuda")
+    st.st_cache_append(k, v, kc, vc, table, cu, kv)
+    st.st_paged_attn_workspace(P, q, kc, vc, table, cu, kv, 0, 0)
+    st.st_paged_attn(P, q, kc, vc, table, cu, kv, 0, 0, o=o, lse=lse)
+    assert st.st_last_device_status() == st.ST_OK
+    assert all(bool((x == 7.0).all()) for x in (o, lse, dq, dk, dv)) and bool(torch.isnan(kc).all())
+    for bad in (-1, -5):
+        with pytest.raises(st.StatusError):
+            st.st_packed_attn_fwd(P, q, k, v, cu, bad)
+        with pytest.raises(st.StatusError):
+            st.st_paged_attn(P, q, kc, vc, table, cu, kv, bad, 0)
