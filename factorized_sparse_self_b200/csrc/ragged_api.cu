@@ -171,6 +171,43 @@ int clamp_int(long long x, long long lo, long long hi) {
   return (int)std::max(lo, std::min(x, hi));
 }
 
+// Whether the few-row kernel takes a strided chunk of more rows than kFewRows. The rows
+// lie in many classes, so 256 of them may meet most of the context, one tile after the
+// other; units of 16 rows meet little, but those of one class, or of one window, each
+// read its keys again. So: where 256-row units would not fill a quarter of the GPU,
+// unless the 16-row units of all heads read more keys an SM than 1.5 times what the
+// tile kernel has to go through one after the other (its longest key range, or its
+// share of all units; and 256 keys for its start). us by the few-row kernel and by the tile
+// kernel, one chunk of n behind 16 K keys, merged, d = 128 (last column: split, behind 4 K):
+//   n, l           64, 64   256, 128  512, 128  256, 16   256, 4    512, 512
+//   H = 32, Hkv 8  39, 379  88, 131   86, 90    104, 74*  216, 76*  74, 43*
+//   H = 8, Hkv 2   23, 376  34, 129   41, 86    53, 69    88, 43*   33, 41
+// (*: goes to the tile kernel). Over 720 such calls (d 64, 128; l 4 to 512; 1 to 16 chunks
+// of 32 to 512) the choice takes 2 % longer than the better kernel of each, 2.0 times
+// at worst; the quarter of the GPU alone 7 %, 3.0 times at worst.
+template <class Units, class Ranges>
+bool strided_by_few(const Geo& g, const st_pattern_desc& p, int G, long long max_q, Units units,
+                    Ranges ranges) {
+  const long long sms = sm_count(), T = p.T, l = std::min<long long>(p.l, T);
+  const long long longest = units(256, max_q), all = std::max(longest, units(256, g.total));
+  if (p.kind != ST_STRIDED || 4 * all >= sms) return false;
+  const long long cls_rows = G * std::max(1LL, max_q / l), cls_keys = (T + l - 1) / l;
+  // keys that one unit meets in either order, and the units of all sequences
+  auto meets = [&](long long rows, long long& band, long long& cls) {
+    rows = std::min(rows, max_q * G);
+    band = std::min(T, l + 1 + (rows + G - 1) / G);
+    cls = std::min(T, std::max(1LL, rows / cls_rows) * cls_keys);
+  };
+  const long long seqs = std::max(1, std::min(g.S, g.total)), mean = (g.total + seqs - 1) / seqs;
+  long long b16, c16, b256, c256;
+  meets(16, b16, c16);
+  meets(256, b256, c256);
+  const long long few = seqs * units(16, mean) * (b16 + c16);
+  const long long tiles = seqs * units(256, mean) * (b256 + c256);
+  const long long range = std::max(b256, c256) / ranges(longest, all);
+  return 2 * few <= 3 * std::max(sms * (range + 256), tiles + sms * 256);
+}
+
 // Key ranges (the kernels cut short units into fewer). Units go to free SMs one
 // by one, so only few units leave SMs idle: those of one longest sequence (the
 // others may be short) have to be worth the GPU. A prompt's units see 1 .. T
@@ -187,16 +224,17 @@ FwdPlan plan_fwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype, long lo
   FwdPlan f{};
   const long long sms = sm_count(), keys = most_keys(p);
   const int G = g.split ? (g.G + 1) / 2 : g.G;
-  // Rows of a short strided chunk lie in many classes, so 256 of them meet most of
-  // the context, one tile after the other: 16 rows a unit are better until such
-  // units fill a quarter of the GPU. Merged, l = 128, Hkv = 8, d = 128, one sequence of
-  // 16 K keys, 128, 256, 512 rows: 27, 39, 55 us against the tile kernel's 117, 207,
-  // 207; four of 8 K keys, 256 rows: 70 against 127; 32 of 4 K keys, 32, 64 rows: 57,
-  // 102 against 64, 78.
   auto units = [&](int rows, long long tokens) { return (tokens * G + rows - 1) / rows * g.Hkv; };
-  f.few = paged && dtype != ST_F32 &&
-          (max_q * G <= kFewRows ||
-           (p.kind == ST_STRIDED && 4 * std::max(units(256, max_q), units(256, g.total)) < sms));
+  // the tile kernels' key ranges
+  auto ranges = [&](long long longest, long long all) {
+    long long n = 1;
+    if (all < 4 * sms) {
+      n = ((paged ? 2 : 1) * sms + longest - 1) / longest;
+      if (paged) n = std::min(n, std::max(4LL, 6 * sms / all));
+    }
+    return std::max(1LL, std::min(n, keys / 512));
+  };
+  f.few = paged && dtype != ST_F32 && (max_q * G <= kFewRows || strided_by_few(g, p, G, max_q, units, ranges));
   const int rows = f.few ? 16 : dtype == ST_F32 ? 64 : 256;
   const int key_tile = f.few ? 16 : dtype == ST_F32 ? 64 : 128;
   const long long longest = std::max(1LL, units(rows, max_q));
@@ -210,12 +248,7 @@ FwdPlan plan_fwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype, long lo
     f.nsplit = clamp_int((keys + f.least * key_tile - 1) / (f.least * key_tile), 1, std::min<long long>(fit, kPartsLimit));
   } else {
     f.least = 512 / key_tile;
-    long long n = 1;
-    if (all < 4 * sms) {
-      n = ((paged ? 2 : 1) * sms + longest - 1) / longest;
-      if (paged) n = std::min(n, std::max(4LL, 6 * sms / all));
-    }
-    f.nsplit = clamp_int(std::min(n, keys / 512), 1, std::min<long long>(fit, kPartsLimit));
+    f.nsplit = clamp_int(ranges(longest, all), 1, std::min<long long>(fit, kPartsLimit));
     // ranges of one length: shorter sequences are cut into fewer
     f.least = (int)std::max<long long>(f.least, (keys + key_tile - 1) / key_tile / f.nsplit);
   }
