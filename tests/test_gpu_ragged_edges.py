@@ -9,7 +9,7 @@ import torch
 import factorized_sparse_self_b200 as st
 from conftest import ROOT
 from ragged_ref import One, check
-from test_gpu_ragged import DT, make_cache, packed, randn, starts
+from test_gpu_ragged import DT, make_cache, packed, paged, randn, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -344,3 +344,108 @@ def test_batches_of_empty_sequences(rows, dtype):
             st.st_packed_attn_fwd(P, q, k, v, cu, bad)
         with pytest.raises(st.StatusError):
             st.st_paged_attn(P, q, kc, vc, table, cu, kv, bad, 0)
+
+
+# ---- alignment, groups and starts at their limits -----------------------------------------------------
+
+
+def sixteen_bytes_on(shape, dtype, fill=7.0):
+    """A contiguous tensor whose first element lies 16 bytes past a 256-byte boundary."""
+    n, skip = 1, 16 // torch.empty((), dtype=dtype).element_size()
+    for x in shape:
+        n *= x
+    return torch.full((n + skip,), fill, dtype=dtype, device="cuda")[skip:].view(shape)
+
+
+@pytest.mark.parametrize("ty", THREE, ids=lambda t: f"{t[0]}-d{t[1]}")
+@pytest.mark.parametrize("pat,lens,H,Hkv", SPLITS, ids=str)
+def test_tensors_on_16_byte_boundaries_only(pat, lens, H, Hkv, ty):
+    """Rows are stored 32 bytes at a time where they can be: the results are the same where they cannot."""
+    dtype, d = ty
+    dt, n = DT[dtype], sum(lens)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = [randn(g, n, h, d, dtype=dt) for h in (H, Hkv, Hkv, H)]
+    P, cu = st.st_pattern(*pat), starts(lens)
+    o, lse = st.st_packed_attn_fwd(P, *x[:3], cu, max(lens))
+    grads = st.st_packed_attn_bwd(P, *x[:3], o, lse, x[3], cu, max(lens))
+    y = [sixteen_bytes_on(t.shape, dt).copy_(t) for t in x]
+    assert all(t.data_ptr() % 32 == 16 for t in y)
+    o2, lse2, *grads2 = (sixteen_bytes_on(t.shape, t.dtype) for t in (o, lse, *grads))
+    st.st_packed_attn_fwd(P, *y[:3], cu, max(lens), o=o2, lse=lse2)
+    st.st_packed_attn_bwd(P, *y[:3], o2, lse2, y[3], cu, max(lens), dq=grads2[0], dk=grads2[1], dv=grads2[2])
+    assert st.st_last_device_status() == st.ST_OK
+    for a, b in zip((o, lse, *grads), (o2, lse2, *grads2)):
+        assert torch.equal(a, b)
+    # the same rows as a chunk and as single tokens over a cache that starts there
+    page = 16
+    kc, vc = (sixteen_bytes_on((-(-n // page), page, Hkv, d), dt, float("nan")) for _ in range(2))
+    table = torch.arange(kc.shape[0], dtype=torch.int32, device="cuda")[None].contiguous()
+    kv = torch.tensor([n], dtype=torch.int32, device="cuda")
+    st.st_cache_append(y[1], y[2], kc, vc, table, starts([n]), kv)
+    for m in (1, 90):
+        out = [st.st_paged_attn(P, q, kc, vc, table, starts([m]), kv, m, n, o=o3, lse=lse3) for q, o3, lse3 in (
+            (x[0][-m:].contiguous(), None, None),
+            (sixteen_bytes_on((m, H, d), dt).copy_(x[0][-m:]), sixteen_bytes_on((m, H, d), dt), sixteen_bytes_on((m, H), torch.float32)))]
+        for a, b in zip(*out):
+            assert torch.equal(a, b)
+        ro, to, rl, tl = One(pat, x[0][-m:], x[1], x[2], dt).outputs()
+        check("o", out[1][0], ro, to)
+    assert st.st_last_device_status() == st.ST_OK
+
+
+@pytest.mark.parametrize("ty", THREE, ids=lambda t: f"{t[0]}-d{t[1]}")
+@pytest.mark.parametrize("G", [64, 128, 129, 300])
+def test_groups_of_a_tile_of_heads_and_more(G, ty):
+    """One query's heads fill a tile, or several."""
+    dtype, d = ty
+    for pat in (("dense", "merged", 1, 1), ("strided", "merged", 5, 1), ("fixed", "split", 6, 2)):
+        packed(pat, G, 1, d, dtype, [19, 1, 40], backward=True, lead=2)
+        paged(pat, G, 1, d, dtype, [70, 33, 2], [1, 5, 1], 16)
+        paged(pat, G, 1, d, dtype, [70, 33, 2], [1, 1, 1], 16, max_q=1)
+
+
+@pytest.mark.parametrize("ty", THREE, ids=lambda t: f"{t[0]}-d{t[1]}")
+def test_starts_outside_the_rows_are_clamped(ty):
+    dtype, d = ty
+    g = torch.Generator(device="cuda").manual_seed(5)
+    n, H, Hkv = 310, 4, 2
+    q, k, v, dout = (randn(g, n, h, d, dtype=DT[dtype]) for h in (H, Hkv, Hkv, H))
+    P = st.st_pattern("strided", "merged", 12)
+
+    def run(cu):
+        cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        o, lse = st.st_packed_attn_fwd(P, q, k, v, cu, n)
+        return (o, lse, *st.st_packed_attn_bwd(P, q, k, v, o, lse, dout, cu, n))
+
+    for wild, tame in (([-5, 100, 10 ** 9], [0, 100, n]), ([-2 ** 31, -7, 2 ** 31 - 1, 2 ** 31 - 1], [0, 0, n, n])):
+        for a, b in zip(run(wild), run(tame)):
+            assert torch.equal(a, b)
+    assert st.st_last_device_status() == st.ST_OK
+
+
+def test_packed_offsets_past_32_bits():
+    """Tensors of more than 2^32 elements, and parts of them in fp32: the last sequence's rows and gradients."""
+    long, short, H, d = 1_060_000, 300, 32, 128
+    g = torch.Generator(device="cuda").manual_seed(6)
+    n = long + short
+    assert n * H * d > 2 ** 32
+    q, k, v, dout = (torch.randn(n, h, d, generator=g, device="cuda", dtype=torch.bfloat16) for h in (H, 1, 1, H))
+    P, cu = st.st_pattern("strided", "merged", 512), starts([long, short])
+    o, lse = st.st_packed_attn_fwd(P, q, k, v, cu, long)
+    grads = st.st_packed_attn_bwd(P, q, k, v, o, lse, dout, cu, long)
+    assert st.st_last_device_status() == st.ST_OK
+    a = long
+    one = One(("strided", "merged", 512, 1), q[a:], k[a:], v[a:], torch.bfloat16)
+    ro, to, rl, tl = one.outputs()
+    check("o", o[a:], ro, to)
+    check("lse", lse[a:], rl, tl)
+    for name, got, (want, tol) in zip(("dq", "dk", "dv"), grads, one.backward(dout[a:])):
+        check(name, got[a:], want, tol)
+    # causal: the first rows of the long sequence have what they would have alone
+    m = 200
+    one = One(("strided", "merged", 512, 1), q[:m], k[:m], v[:m], torch.bfloat16)
+    ro, to, rl, tl = one.outputs()
+    check("o", o[:m], ro, to)
+    check("lse", lse[:m], rl, tl)
+    del q, dout, o, grads
+    torch.cuda.empty_cache()
