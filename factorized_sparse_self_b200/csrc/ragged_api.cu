@@ -155,8 +155,14 @@ struct FwdPlan {
   int nparts;   // parts of a row (0: rows are written directly)
   bool taper;   // ranges get shorter, and short ones go last
   bool merge;   // the second order joins the first's part itself
+  bool fits;    // the units of a launch can be numbered
   size_t parts_o, bytes;
 };
+
+// The tile kernels number the units of a launch in 31 bits.
+bool units_fit(const Geo& g, int mult, int rows, long long per_slot) {
+  return slot_count(g, mult, rows) * g.Hkv * per_slot <= 0x7fffffff;
+}
 
 // Rows that one query row's pattern lets it attend, at most, in a sequence of T.
 long long most_keys(const st_pattern_desc& p) {
@@ -256,6 +262,9 @@ FwdPlan plan_fwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype, long lo
   const bool two = two_orders(p);
   f.merge = two && f.nsplit == 1 && !f.few;
   f.nparts = f.merge ? 1 : two ? 2 * f.nsplit : f.nsplit > 1 ? f.nsplit : 0;
+  Job jobs[2];
+  const int launched = f.merge ? 1 : make_jobs(p, jobs);
+  f.fits = f.few || dtype == ST_F32 || units_fit(g, G, rows, (long long)launched * f.nsplit);
   f.parts_o = round256(qrows * g.d * sizeof(float) * f.nparts);
   f.bytes = f.nparts ? f.parts_o + round256(qrows * sizeof(float) * f.nparts) : 0;
   return f;
@@ -318,6 +327,7 @@ struct BwdPlan {
   int njobs, nsplit;
   bool parts;  // dK, dV are joined from parts
   bool merge;  // the second launch adds the first one's part itself
+  bool fits;   // as of the forward
   int mend_tiles, mend_below;
   size_t delta, dq_part, parts_bytes, bytes;
 };
@@ -354,6 +364,9 @@ BwdPlan plan_bwd(const Geo& g, const st_pattern_desc& p, st_dtype dtype) {
   b.merge = both && b.nsplit == 1 && all >= 2 * sms;
   // one part is enough only where every key head has one job over all its keys
   b.parts = !b.merge && (b.nsplit > 1 || (b.njobs == 2 && (both || b.kjob[1].seg[0].kview == VIEW_SUM)));
+  b.fits = dtype == ST_F32 ||
+           (units_fit(g, g.split ? (g.G + 1) / 2 : g.G, 128, two_orders(p) ? 1 : n) &&
+            units_fit(g, 1, 128, (long long)(b.merge ? 1 : b.njobs) * b.nsplit));
   b.delta = round256(qrows * sizeof(float));
   b.dq_part = two_orders(p) ? round256(qrows * g.d * sizeof(float)) : 0;
   const int nparts = b.merge ? 1 : b.parts ? b.njobs * b.nsplit : 0;
@@ -373,8 +386,9 @@ st_status st_packed_attn_fwd_workspace(const st_pattern_desc* p, st_dtype dtype,
   if (!bytes) return ST_ERR_INVALID;
   st_status s = fill_geo(p, dtype, x, true, g);
   if (s != ST_OK) return s;
-  *bytes = plan_fwd(g, *p, dtype, p->T, false).bytes;
-  return ST_OK;
+  const FwdPlan f = plan_fwd(g, *p, dtype, p->T, false);
+  *bytes = f.bytes;
+  return f.fits ? ST_OK : ST_ERR_UNSUPPORTED;
 }
 
 st_status st_packed_attn_fwd(const st_pattern_desc* p, st_dtype dtype, const st_packed_desc* x,
@@ -389,6 +403,7 @@ st_status st_packed_attn_fwd(const st_pattern_desc* p, st_dtype dtype, const st_
       !aligned4(cu))
     return ST_ERR_INVALID;
   const FwdPlan f = plan_fwd(g, *p, dtype, p->T, false);
+  if (!f.fits) return ST_ERR_UNSUPPORTED;
   if (!workspace_ok(ws, ws_bytes, f.bytes)) return ST_ERR_WORKSPACE;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   s = get_status(g);
@@ -403,8 +418,9 @@ st_status st_packed_attn_bwd_workspace(const st_pattern_desc* p, st_dtype dtype,
   if (!bytes) return ST_ERR_INVALID;
   st_status s = fill_geo(p, dtype, x, true, g);
   if (s != ST_OK) return s;
-  *bytes = plan_bwd(g, *p, dtype).bytes;
-  return ST_OK;
+  const BwdPlan b = plan_bwd(g, *p, dtype);
+  *bytes = b.bytes;
+  return b.fits ? ST_OK : ST_ERR_UNSUPPORTED;
 }
 
 st_status st_packed_attn_bwd(const st_pattern_desc* p, st_dtype dtype, const st_packed_desc* x,
@@ -426,6 +442,7 @@ st_status st_packed_attn_bwd(const st_pattern_desc* p, st_dtype dtype, const st_
       !aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned4(cu))
     return ST_ERR_INVALID;
   const BwdPlan b = plan_bwd(g, *p, dtype);
+  if (!b.fits) return ST_ERR_UNSUPPORTED;
   if (!workspace_ok(ws, ws_bytes, b.bytes)) return ST_ERR_WORKSPACE;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   s = get_status(g);
@@ -502,8 +519,9 @@ st_status st_paged_attn_workspace(const st_pattern_desc* p, st_dtype dtype,
   st_status s = fill_geo(p, dtype, x, true, g);
   if (s == ST_OK) s = fill_cache(c, g);
   if (s != ST_OK) return s;
-  *bytes = plan_fwd(g, *p, dtype, max_q, true).bytes;
-  return ST_OK;
+  const FwdPlan f = plan_fwd(g, *p, dtype, max_q, true);
+  *bytes = f.bytes;
+  return f.fits ? ST_OK : ST_ERR_UNSUPPORTED;
 }
 
 st_status st_paged_attn(const st_pattern_desc* p, st_dtype dtype, const st_packed_desc* x,
@@ -521,6 +539,7 @@ st_status st_paged_attn(const st_pattern_desc* p, st_dtype dtype, const st_packe
       !aligned4(cu) || !aligned4(kv_lens) || !aligned4(table))
     return ST_ERR_INVALID;
   const FwdPlan f = plan_fwd(g, *p, dtype, max_q, true);
+  if (!f.fits) return ST_ERR_UNSUPPORTED;
   if (!workspace_ok(ws, ws_bytes, f.bytes)) return ST_ERR_WORKSPACE;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   s = get_status(g);
