@@ -24,14 +24,17 @@
 // warpgroups that share the 128 rows and take 64 columns each of a 128 x 128
 // tile (thread = row = TMEM lane); P and dS go back to TMEM as 16-bit pairs over
 // columns that have been read and are the A operand from there, so they never pass
-// through shared memory. Warp 9 issues the products, warps 8 and 11
-// load rows, warp 10 decodes units.
+// through shared memory. Both are rounded to the tensors' type: one type for both
+// operands of a product (a weight of dV errs by 2^-8 in bf16, 2^-11 in fp16, relative
+// to itself). Warp 9 issues the products, warps 8 and 11 load rows, warp 10 decodes
+// units.
 // TMEM: S, dP (key-major: transposed), 128 columns each, then the accumulators, d
 // columns each: dQ and P K, or dV and dK. P and dS both go over dP, so S is free as
 // soon as it is in registers and the next tile's is formed under this one's
 // exponentials. Query-major there is room for two S (not at d = 128 where units of any
-// length mend): P and dS go over S, and the next dP is formed before the tile's products, not behind them (backward of 12288
-// rasters, l = 192, split: 223 against 241 us).
+// length mend): P and dS go over S, and the next dP is formed before the tile's
+// products, not behind them (backward of 12288 rasters, l = 192, split: 223 against 241
+// us).
 #include "ragged_tc.cuh"
 
 namespace st {

@@ -17,6 +17,8 @@
 //   warps 0..7   softmax of half 0 and 1: thread = query row = TMEM lane, running
 //                maximum (O is rescaled in TMEM only when it grows by more than 2^8)
 //                and sum in fp32, P as 16-bit pairs over S.
+// The softmax holds a row's 128 scores in 208 registers; 256 bytes of its other state
+// are spilled at d = 128, 208 at d = 64.
 // TMEM: S0 S1 (P0 P1 in their first 64 columns) O0 O1, 128 columns each.
 #include "ragged_tc.cuh"
 
