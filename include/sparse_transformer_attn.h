@@ -264,10 +264,10 @@ st_status st_sparse_attn_bwd_noalloc(const st_layout* layout, st_dtype dtype, in
  *    result nor written.
  *  - Keys and values of a sequence's own rows must be finite; whatever lies in
  *    rows of no sequence, unused pages and unused slots of a page (infinities,
- *    NaN) has no effect. A query row whose scores are not numbers (NaN in q, or
- *    scores that overflow) gets O = NaN and LSE = NaN, whatever the split; no other
- *    row of O, LSE or dQ changes, nor any gradient of another sequence (dK, dV of
- *    its own sequence may become NaN).
+ *    NaN) has no effect. A query row with a score that is NaN or +inf (NaN in q, or
+ *    products that overflow) gets O = NaN and LSE = NaN, whatever the split; one
+ *    whose scores are all -inf counts as empty. No other row of O, LSE or dQ changes,
+ *    nor any gradient of another sequence (dK, dV of its own may become NaN).
  *  - workspace: device memory of at least the queried size, 256-byte aligned,
  *    overwritten; may be NULL when the size is 0. Calls (or replays of captured
  *    graphs) that may run at the same time need a workspace each.

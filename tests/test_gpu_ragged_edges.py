@@ -449,3 +449,29 @@ def test_packed_offsets_past_32_bits():
     check("lse", lse[:m], rl, tl)
     del q, dout, o, grads
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("ty", THREE, ids=lambda t: f"{t[0]}-d{t[1]}")
+@pytest.mark.parametrize("pat,lens,H,Hkv", SPLITS, ids=str)
+def test_results_repeat_bit_by_bit(pat, lens, H, Hkv, ty):
+    """One part a row, key ranges, two orders; units go to whichever SM is free, sums do not."""
+    dtype, d = ty
+    dt, n = DT[dtype], sum(lens)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q, k, v, dout = (randn(g, n, h, d, dtype=dt) for h in (H, Hkv, Hkv, H))
+    P, cu = st.st_pattern(*pat), starts(lens)
+    kc, vc, table = make_cache(g, lens, 16, Hkv, d, dt)
+    kv = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    st.st_cache_append(k, v, kc, vc, table, cu, kv)
+
+    def run():
+        o, lse = st.st_packed_attn_fwd(P, q, k, v, cu, max(lens))
+        out = [o, lse, *st.st_packed_attn_bwd(P, q, k, v, o, lse, dout, cu, max(lens))]
+        for m in (1, 64):
+            out += st.st_paged_attn(P, q[:2 * m], kc, vc, table, starts([m, m]), kv, m, max(lens))
+        return out
+
+    first = run()
+    for _ in range(8):
+        for a, b in zip(first, run()):
+            assert torch.equal(a, b)
